@@ -29,6 +29,9 @@ DEVERR = {
     4: "top-k id out of range",
     8: "pipeline wait timed out",
     16: "seq_len inconsistent",
+    32: "RoPE position out of range",
+    64: "page or sequence not in the state the call needs",
+    128: "no free page left",
 }
 HEADS, HEAD_DIM, BLOCK_SIZE, PAGE_BYTES = 64, 128, 64, 8448
 FP4_PAGE_BYTES = 4352  # 64 slots x (64 E2M1 code bytes + 4 scale bytes)
@@ -43,6 +46,9 @@ SYMBOLS = [
     "dsa_indexer_logits_topk_static", "dsa_set_launch_events",
     "dsa_indexer_k_rope_quant_write", "dsa_indexer_q_rope_quant_fold", "dsa_gather_rows",
     "dsa_indexer_k_quant_write_fp4", "dsa_selftest_wait_timeout",
+    "dsa_kv_write", "dsa_attn_decode_workspace_size", "dsa_attn_decode", "dsa_attn_selected_workspace_size",
+    "dsa_attn_selected", "dsa_attn_prompt", "dsa_pages_workspace_size", "dsa_pages_copy", "dsa_pages_fork",
+    "dsa_pages_free", "dsa_pages_compact",
 ]
 STATIC_WORKSPACE_BYTES = 32 << 20
 
@@ -100,6 +106,52 @@ class DsaStackPlanC(ctypes.Structure):
     ]
 
 
+class DsaKvC(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int64),
+        ("k_page_stride", ctypes.c_int64),
+        ("k_slot_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_page_stride", ctypes.c_int64),
+        ("v_slot_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+    ]
+
+
+class DsaAttnC(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("q_row_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("out_row_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("lse", ctypes.c_void_p),
+        ("num_heads", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class DsaPagesC(ctypes.Structure):
+    _fields_ = [
+        ("refs", ctypes.c_void_p),
+        ("num_blocks", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p),
+        ("bt_stride", ctypes.c_int64),
+        ("n_rows", ctypes.c_int32),
+        ("seq_lens", ctypes.c_void_p),
+    ]
+
+
+class DsaCacheDescC(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -143,6 +195,17 @@ def load(build_if_missing: bool = True):
             "dsa_selftest_wait_timeout": (ctypes.c_int, [P, P]),
             "dsa_indexer_q_rope_quant_fold": (ctypes.c_int, [P, P, I64, P, P, I64, F32, P, P, P, P, P]),
             "dsa_gather_rows": (ctypes.c_int, [P, I64, I64, I64, P, I64, I32, P, P, P]),
+            "dsa_kv_write": (ctypes.c_int, [P, I64, I64, P, I64, I64, I64, P, P, P, P]),
+            "dsa_attn_decode_workspace_size": (SZ, [P, I32, I32, I32]),
+            "dsa_attn_decode": (ctypes.c_int, [P, P, P, P, SZ, P, P]),
+            "dsa_attn_selected_workspace_size": (SZ, [I64, I32, I32, I32, I32]),
+            "dsa_attn_selected": (ctypes.c_int, [P, P, P, I64, I32, P, SZ, P, P]),
+            "dsa_attn_prompt": (ctypes.c_int, [P, P, P, P, P, P]),
+            "dsa_pages_workspace_size": (SZ, [I64, I32]),
+            "dsa_pages_copy": (ctypes.c_int, [P, I32, I64, P, P, I32, P, SZ, P, P]),
+            "dsa_pages_fork": (ctypes.c_int, [P, P, P, I32, P, I32, P, SZ, P, P]),
+            "dsa_pages_free": (ctypes.c_int, [P, P, I32, P, P]),
+            "dsa_pages_compact": (ctypes.c_int, [P, P, I32, P, SZ, P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "../../include/dsaidx.h"
+#include "host.h"
 #include "kernels.h"
 
 using namespace dsa;
@@ -38,19 +39,16 @@ int g_num_sms[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::mutex g_mutex;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-int from_cuda(cudaError_t e) {
+int dsa::from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return DSA_OK;
   if (e == cudaErrorNoKernelImageForDevice || e == cudaErrorNoDevice || e == cudaErrorInsufficientDriver)
     return DSA_ENODEV;
   return DSA_ECUDA;
 }
 
-// SM count of the current device; DSA_ENODEV unless it is an sm_103 part.
-int device_sms(int* sms) {
+int dsa::device_sms(int* sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ENODEV;
   if (dev < 0 || dev >= kMaxDevices) return DSA_ENODEV;
@@ -68,7 +66,7 @@ int device_sms(int* sms) {
   return DSA_OK;
 }
 
-int tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
+int dsa::tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
   std::lock_guard<std::mutex> lock(g_mutex);
   if (g_encode == nullptr) {
     void* fn = nullptr;
@@ -82,6 +80,8 @@ int tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
   *out = g_encode;
   return DSA_OK;
 }
+
+namespace {
 
 // K cache as a 3-D tensor {128 K values, 64 slots, num_blocks pages}: one box
 // is the 64 K rows of one page, landed with the 128-byte swizzle. FP8 pages

@@ -1,0 +1,631 @@
+// attn_prompt.cu — causal attention over prompts on the tcgen05 tensor cores
+// (sm_103a), keys in the paged cache or packed beside the queries.
+//
+//   S = Q K^T,  P = 2^(S scale log2(e) - M),  O = P V,  out = O / sum(P),
+//   lse = ln 2 * (M + log2 sum(P))
+// tile by tile over the keys. Any M gives the same quotient; it only has to
+// keep P in range, so a row's M is raised (and its O and sum rescaled) only
+// when a score passes it by more than 2^8. That makes the rescaling of O, a
+// round trip through TMEM, rare, and lets the softmax warps do it themselves.
+//
+// What bounds it: 4*D operations per (query head, visible pair), the bf16 /
+// fp16 rate of the tensor cores, with 128x128 tiles of S needing one exponential
+// per 4*D operations beside it.
+//
+// Mapping: a CTA holds two query tiles of 128 rows that share one stream of
+// K and V tiles (128 keys): two query heads of one KV head where the group is
+// even, else two consecutive token tiles of one head. While one tile's softmax
+// runs, the tensor cores run the other tile's P V and next Q K^T.
+//  * warps 0-3 / 4-7: softmax of tile 0 / 1, one row per thread: S from TMEM
+//    (128 columns in registers), P back over S's columns as the A operand of
+//    P V (never through shared memory), rescaling, and the final store.
+//  * warp 8: TMA. K and V tiles take turns in one ring (D = 128: five 32 KB
+//    stages); a page (64 slots of a head) is one box per 64 columns.
+//  * warp 9: issues the MMAs. V is read as stored, keys along rows: B is
+//    "MN-major", K and Q are K-major; all in the 128-byte swizzle.
+//  * TMEM: S/P of both tiles (2 x 128 columns), O of both (2 x D).
+// CTAs are numbered from the last query tile of the last request down, so the
+// longest tiles start first and the short ones fill the tail.
+//
+// V rows a tile holds but a row may not see meet P = 0 in the MMA, and 0 * NaN
+// is NaN: in the tiles cut by the causal edge or by the sequence's end, the
+// softmax warps first clear the rows behind the sequence and any non-finite V
+// element; rows that do see such an element get it added back at the end.
+#include "attn.h"
+#include "common.cuh"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kRowsTile = 128;  // query rows per tile
+constexpr int kKeys = 128;      // keys per tile
+constexpr int kSoftWarps = 8;
+// Three warpgroups, the third with two idle warps: registers move between
+// warpgroups. Launched with 168 a thread (384 * 168 = 64512), the softmax
+// warpgroups take 224 (a row of S) and the third keeps 56: 256 * 224 + 128 * 56
+// = 64512.
+constexpr int kPromptThreads = 32 * (kSoftWarps + 4);
+constexpr int kSoftRegs = 224, kIssueRegs = 56;
+static_assert(2 * 128 * kSoftRegs + 128 * kIssueRegs <= kPromptThreads * 168, "register split");
+constexpr float kSlackP = 8.0f;
+
+template <int D>
+struct PromptCfg {
+  static constexpr int kTileBytes = kKeys * D * 2;      // a Q, K or V tile
+  static constexpr int kBoxBytes = kBlock * 128;        // 64 slots of 64 columns
+  static constexpr int kColBytes = kKeys * 128;         // 64 columns of a tile
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kOffKv = 2 * kTileBytes;
+  static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
+  static constexpr int kNumBars = 2 * kStages + 2 + 2 + 2 + 2 + 1;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmemBytes = kOffMisc + 64 + 1024;  // + slack to align the base to 1024
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kO = 256;                   // first column of O
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+  static_assert(kO + 2 * D <= kTmemCols, "TMEM budget");
+};
+
+template <typename T>
+struct PElem;
+template <>
+struct PElem<__nv_bfloat16> {
+  static constexpr uint32_t kFmt = 1;
+  static constexpr float kHead = 0.0f;         // bf16 has fp32's exponents
+  static constexpr uint32_t kExp = 0x7F80u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+template <>
+struct PElem<__half> {
+  static constexpr uint32_t kFmt = 0;
+  static constexpr float kHead = 6.0f;         // M sits 6 below the maximum: P <= 2^14, smallest step 2^-30 of it
+  static constexpr uint32_t kExp = 0x7C00u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+
+__device__ __forceinline__ float pex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Instruction descriptor of kind::f16 -> fp32, M = 128.
+__host__ __device__ constexpr uint32_t f16_idesc(uint32_t fmt, int N, bool b_mn_major) {
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (128u >> 4 << 24);
+}
+
+// Matrix descriptor of a tile stored row by row along the reduction (keys of
+// V), 64 columns = 128 swizzled bytes a row: 8-row groups 1024 bytes apart,
+// the next 64 columns kKeys rows further.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((kKeys * 128) >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_t* bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
+      "%6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// The request and query tile of one CTA, found from the metadata by each warp.
+struct PromptTile {
+  int req;
+  int t0, ntok;   // first token (row of q) of the CTA's rows, tokens left in the request from there
+  int pos0;       // position of the first token
+  int keys;       // the request's keys
+  int kv0;        // packed: row of key 0
+  bool found;
+};
+
+__device__ __forceinline__ PromptTile find_tile(const PromptArgs& a, int rank, bool flag) {
+  const int lane = threadIdx.x & 31;
+  const int unit = a.pair_heads ? kRowsTile : 2 * kRowsTile;
+  PromptTile p{};
+  int before = 0;  // units of the requests behind this one
+  for (int base = 0; base < a.num_reqs - a.num_decodes; base += 32) {
+    const int r = a.num_reqs - 1 - base - lane;
+    int q0 = 0, q1 = 0, sl = 0, s0 = 0;
+    bool bad = false;
+    if (r >= a.num_decodes) {
+      q0 = __ldg(a.qsl + r);
+      q1 = __ldg(a.qsl + r + 1);
+      sl = __ldg(a.seq_lens + r);
+      if (a.kv_start != nullptr) s0 = __ldg(a.kv_start + r);
+      if (q1 < q0 || q0 < a.first_token || q1 > a.num_tokens) {
+        bad = true;
+        q1 = q0;  // no rows of its own to write
+      }
+      if (sl < 0 || sl > a.max_keys || (a.kv_start != nullptr && (s0 < 0 || s0 > a.num_blocks - sl))) {
+        bad = true;
+        sl = 0;
+      }
+      if (bad && flag) flag_error(a.err, DSA_DEVERR_SEQ_RANGE);
+    }
+    const int units = (q1 - q0 + unit - 1) / unit;
+    int incl = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    const int first = before + incl - units;
+    const uint32_t hit = __ballot_sync(0xffffffffu, rank >= first && rank < first + units);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      const int u = units - 1 - (rank - first);
+      p.req = __shfl_sync(0xffffffffu, r, src);
+      p.t0 = __shfl_sync(0xffffffffu, q0 + u * unit, src);
+      p.ntok = __shfl_sync(0xffffffffu, q1 - q0 - u * unit, src);
+      p.pos0 = __shfl_sync(0xffffffffu, sl - (q1 - q0) + u * unit, src);
+      p.keys = __shfl_sync(0xffffffffu, sl, src);
+      p.kv0 = __shfl_sync(0xffffffffu, s0, src);
+      p.found = true;
+      return p;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return p;
+}
+
+// Keys visible to the row at position pos.
+__device__ __forceinline__ int visible(int pos, int keys) { return min(max(pos + 1, 0), keys); }
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ PromptArgs a) {
+  using C = PromptCfg<D>;
+  using E = PElem<T>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* kv = smem + C::kOffKv;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* empty = full + S;
+  uint64_t* qfull = empty + S;
+  uint64_t* sfull = qfull + 2;
+  uint64_t* pfull = sfull + 2;
+  uint64_t* ofull = pfull + 2;
+  uint64_t* done = ofull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  // first tiles in which a non-finite V element was cleared: per softmax group, lowest and highest tile
+  int* bad_lo = reinterpret_cast<int*>(smem + C::kOffMisc + 8);
+  int* bad_hi = bad_lo + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hu = blockIdx.x % a.head_units, rank = blockIdx.x / a.head_units;
+  const PromptTile tile = find_tile(a, rank, hu == 0 && warp == 0);
+  if (!tile.found) return;
+  // the two query tiles: rows, heads, key tiles
+  int head[2], t0[2], rows[2], pos0[2], nt[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int shift = a.pair_heads ? 0 : x * kRowsTile;
+    head[x] = a.pair_heads ? 2 * hu + x : hu;
+    t0[x] = tile.t0 + shift;
+    rows[x] = min(kRowsTile, max(0, tile.ntok - shift));
+    pos0[x] = tile.pos0 + shift;
+    nt[x] = rows[x] > 0 ? (visible(pos0[x] + rows[x] - 1, tile.keys) + kKeys - 1) / kKeys : 0;
+  }
+  const int h = head[0] / a.group;
+  const int n_tiles = max(nt[0], nt[1]);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&qfull[x], 1);
+      mbar_init(&sfull[x], 1);
+      mbar_init(&pfull[x], 4);
+      mbar_init(&ofull[x], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    *bad_lo = 0x7FFFFFFF;
+    *bad_hi = -1;
+    fence_barrier_init();
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_tmap(&tmap_q);
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, C::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 8) {
+      // ----------------------------------------------------------------- TMA
+      int issued = 0;  // ring stages filled
+      bool ok = true;
+      if (lane == 0 && n_tiles > 0) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (nt[x] == 0) continue;
+          mbar_arrive_expect_tx(&qfull[x], C::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(smem + x * C::kTileBytes + c * C::kColBytes, &tmap_q, &qfull[x], c * 64, head[x], t0[x]);
+        }
+      }
+      const int n_pages = (tile.keys + kBlock - 1) / kBlock;
+      int32_t ids = 0;
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        int c2[2], c3[2], boxes;
+        if (a.kv_start == nullptr) {
+          if ((j & 15) == 0) {  // the next 32 pages
+            const int pg = 2 * j + lane;
+            ids = pg < n_pages ? __ldg(a.block_table + static_cast<int64_t>(tile.req) * a.bt_stride + pg) : 0;
+            if (ids < 0 || ids >= a.num_blocks) {
+              flag_error(a.err, DSA_DEVERR_BLOCK_RANGE);
+              ids = 0;
+            }
+          }
+          c3[0] = __shfl_sync(0xffffffffu, ids, 2 * (j & 15));
+          c3[1] = __shfl_sync(0xffffffffu, ids, 2 * (j & 15) + 1);
+          c2[0] = c2[1] = 0;
+          boxes = 2 * j + 1 < n_pages ? 2 : 1;
+        } else {
+          c2[0] = tile.kv0 + j * kKeys;
+          c2[1] = c2[0] + kBlock;
+          c3[0] = c3[1] = 0;
+          // a box may begin behind the last packed row only if it is not loaded at all
+          boxes = j * kKeys + kBlock < tile.keys ? 2 : 1;
+        }
+        if (lane == 0) {
+#pragma unroll
+          for (int kvi = 0; kvi < 2; ++kvi) {
+            const int st = issued % S, round = issued / S;
+            if (round > 0 && !mbar_wait(&empty[st], (round - 1) & 1, abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = kv + st * C::kTileBytes;
+            mbar_arrive_expect_tx(&full[st], boxes * C::kBoxBytes * (D / 64));
+            for (int b = 0; b < boxes; ++b)
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(dst + c * C::kColBytes + b * C::kBoxBytes, kvi == 0 ? &tmap_k : &tmap_v, &full[st], c * 64, h,
+                            c2[b], c3[b]);
+            ++issued;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+      if (lane == 0 && *abort_flag) {  // giving up: no copy may land after the CTA's end
+        const unsigned long long until = global_ns() + kWaitLimitNs;
+        for (int i = max(0, issued - S); i < issued; ++i)
+          while (!mbar_try_wait(smem_u32(&full[i % S]), (i / S) & 1) && global_ns() < until) {
+          }
+        for (int x = 0; x < 2; ++x)
+          if (nt[x] > 0)
+            while (!mbar_try_wait(smem_u32(&qfull[x]), 0) && global_ns() < until) {
+            }
+      }
+    } else if (warp == 9) {
+      // ----------------------------------------------------------------- MMA
+      if (lane == 0 && n_tiles > 0) {
+        constexpr uint32_t kIdS = f16_idesc(E::kFmt, kKeys, false), kIdO = f16_idesc(E::kFmt, D, true);
+        const uint64_t qd[2] = {sw128_kmajor_desc(smem_u32(smem)), sw128_kmajor_desc(smem_u32(smem + C::kTileBytes))};
+        auto scores = [&](int x, int st) {
+          const uint64_t kd = sw128_kmajor_desc(smem_u32(kv + st * C::kTileBytes));
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = ((k / 4) * C::kColBytes + (k % 4) * 32) >> 4;
+            mma_f16_ss(tmem + x * 128, qd[x] + off, kd + off, kIdS, k > 0);
+          }
+          mma_commit(&sfull[x]);
+        };
+        bool ok = mbar_wait(&full[0], 0, abort_flag, a.err);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (nt[x] == 0 || !ok) continue;
+          ok = mbar_wait(&qfull[x], 0, abort_flag, a.err);
+          if (ok) scores(x, 0);
+        }
+        mma_commit(&empty[0]);
+        for (int j = 0; j < n_tiles && ok; ++j) {
+          const int vseq = 2 * j + 1, kseq = 2 * j + 2;
+          const int vst = vseq % S, kst = kseq % S;
+          ok = mbar_wait(&full[vst], (vseq / S) & 1, abort_flag, a.err);
+          const uint64_t vd = sw128_mnmajor_desc(smem_u32(kv + vst * C::kTileBytes));
+          bool have_k = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (ok && j < nt[x]) {
+              ok = mbar_wait(&pfull[x], j & 1, abort_flag, a.err);
+              if (ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                  mma_f16_ts(tmem + C::kO + x * D, tmem + x * 128 + k * 8, vd + ((k * 16 * 128) >> 4), kIdO,
+                             j > 0 || k > 0);
+                if (j == nt[x] - 1) mma_commit(&ofull[x]);
+              }
+            }
+            if (x == 1) mma_commit(&empty[vst]);
+            if (ok && j + 1 < nt[x]) {
+              if (!have_k) ok = mbar_wait(&full[kst], (kseq / S) & 1, abort_flag, a.err);
+              have_k = true;
+              if (ok) scores(x, kst);
+            }
+          }
+          if (have_k) mma_commit(&empty[kst]);
+        }
+        if (*abort_flag) {  // giving up: let the MMAs in flight end before TMEM is freed
+          mma_commit(done);
+          const unsigned long long until = global_ns() + kWaitLimitNs;
+          while (!mbar_try_wait(smem_u32(done), 0) && global_ns() < until) {
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ------------------------------------------------------------- softmax
+    const int x = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + C::kO + x * D;
+    const int my_rows = x == 0 ? rows[0] : rows[1];
+    const int my_nt = x == 0 ? nt[0] : nt[1];
+    const int my_pos = x == 0 ? pos0[0] : pos0[1];
+    const int vis = visible(my_pos + min(r, my_rows - 1), tile.keys);
+    const float NEG = -INFINITY;
+    float M = NEG, L = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < my_nt; ++j) {
+      ok = mbar_wait(&sfull[x], j & 1, abort_flag, a.err);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_wait32(s[c]);
+      const int lim = vis - j * kKeys;  // visible columns
+      const bool edge = __any_sync(0xffffffffu, lim < kKeys);
+      if (edge) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c * 32 + i >= lim) s[c][i] = __float_as_uint(NEG);
+      }
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int i = 1; i < 32; ++i) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][i]));
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      if (__any_sync(0xffffffffu, top > M + (E::kHead + kSlackP))) {
+        const float n = fmaxf(M, top - E::kHead);
+        const float f = M == NEG ? 0.0f : pex2(M - n);
+        M = n;
+        L *= f;
+        if (j > 0) {  // O is complete up to tile j - 1: its MMAs precede this tile's scores
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + c * 32, o);
+            tmem_wait32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(to + c * 32, o);
+          }
+        }
+      }
+      const float ref = M == NEG ? 0.0f : M;
+      const uint64_t sc2 = pack_f32x2(a.scale_log2, a.scale_log2), ref2 = pack_f32x2(-ref, -ref);
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t p[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int c = 2 * half + i / 16, k = (i % 16) * 2;
+          const float2 e = unpack_f32x2(
+              fma_f32x2(pack_f32x2(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), sc2, ref2));
+          const float e0 = pex2(e.x), e1 = pex2(e.y);
+          // summed before P is rounded for the MMA: the rounding enters the numerator only
+          sum[i & 3] += e0 + e1;
+          p[i] = E::pack(e0, e1);
+        }
+        tmem_st32(ts + half * 32, p);
+      }
+      L += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      // V in a tile cut by the causal edge or the sequence's end
+      const int lo = visible(my_pos, tile.keys) - j * kKeys;  // columns every row of the tile sees
+      if (lo < kKeys && (x == 0 || j >= nt[0])) {
+        const int vseq = 2 * j + 1;
+        ok = mbar_wait(&full[vseq % S], (vseq / S) & 1, abort_flag, a.err);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        // thread r: key row r of the tile, which lies at 128-byte row r of each 64-column block
+        uint8_t* v = kv + (vseq % S) * C::kTileBytes + r * 128;
+        const bool behind = j * kKeys + r >= tile.keys;
+        bool bad = false;
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint4* w = reinterpret_cast<uint4*>(v + c * C::kColBytes + i * 16);
+            if (behind) {
+              *w = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 u = *w;
+            bool hit = false;
+            uint32_t* e = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if ((e[q] & E::kExp) == E::kExp) {
+                e[q] &= 0xFFFF0000u;
+                hit = true;
+              }
+              if ((e[q] & (E::kExp << 16)) == (E::kExp << 16)) {
+                e[q] &= 0x0000FFFFu;
+                hit = true;
+              }
+            }
+            if (hit) *w = u;
+            bad |= hit;
+          }
+        if (bad) {
+          atomicMin(bad_lo, j);
+          atomicMax(bad_hi, j);
+        }
+        fence_proxy_async();
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pfull[x]);
+    }
+    // ---- the row's result
+    if (ok && my_nt > 0) ok = mbar_wait(&ofull[x], 0, abort_flag, a.err);
+    if (__all_sync(0xffffffffu, ok)) {
+      tc_fence_after();
+      const int my_head = x == 0 ? head[0] : head[1];
+      const int my_t0 = x == 0 ? t0[0] : t0[1];
+      const bool mine = r < my_rows;
+      T* out = static_cast<T*>(a.out) + static_cast<int64_t>(my_t0 + r) * a.out_row + my_head * a.out_head;
+      const bool any = M != NEG;
+      const float inv = any ? 1.0f / L : 0.0f;
+      const int blo = my_nt > 0 ? *bad_lo : 0x7FFFFFFF, bhi = my_nt > 0 ? *bad_hi : -1;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (my_nt > 0) {
+          tmem_ld32(to + c * 32, o);
+          tmem_wait32(o);
+        }
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = any ? __uint_as_float(o[i]) * inv : 0.0f;
+        if (blo <= bhi && mine) {  // non-finite V elements that this row sees
+          const int end = min(vis, (bhi + 1) * kKeys);
+          for (int k = blo * kKeys; k < end; ++k) {
+            int64_t at;
+            if (a.kv_start == nullptr) {
+              const int id = __ldg(a.block_table + static_cast<int64_t>(tile.req) * a.bt_stride + k / kBlock);
+              if (id < 0 || id >= a.num_blocks) continue;
+              at = id * a.v_page + static_cast<int64_t>(k % kBlock) * a.v_slot;
+            } else {
+              at = static_cast<int64_t>(tile.kv0 + k) * a.v_slot;
+            }
+            const T* vr = static_cast<const T*>(a.v) + at + h * a.v_head + c * 32;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float e = static_cast<float>(vr[i]);
+              if (!isfinite(e)) f[i] += e;
+            }
+          }
+        }
+        if (mine) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint4 w;
+            w.x = E::pack(f[8 * q], f[8 * q + 1]);
+            w.y = E::pack(f[8 * q + 2], f[8 * q + 3]);
+            w.z = E::pack(f[8 * q + 4], f[8 * q + 5]);
+            w.w = E::pack(f[8 * q + 6], f[8 * q + 7]);
+            *reinterpret_cast<uint4*>(out + c * 32 + q * 8) = w;
+          }
+        }
+      }
+      if (mine && a.lse != nullptr)
+        a.lse[static_cast<int64_t>(my_t0 + r) * a.heads + my_head] = any ? (M + log2f(L)) * 0.6931471805599453f : NEG;
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+template <int D, typename T>
+cudaError_t launch(const PromptArgs& a, const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv,
+                   cudaStream_t stream) {
+  static uint64_t done = 0;
+  auto* fn = attn_prompt_kernel<D, T>;
+  cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(fn), PromptCfg<D>::kSmemBytes, &done);
+  if (e != cudaSuccess) return e;
+  fn<<<a.head_units * a.tile_units, kPromptThreads, PromptCfg<D>::kSmemBytes, stream>>>(*mq, *mk, *mv, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prompt(const PromptArgs& a, const CUtensorMap* mq, const CUtensorMap* mk,
+                               const CUtensorMap* mv, int head_dim, int dtype, cudaStream_t stream) {
+  if (dtype == DSA_BF16)
+    return head_dim == 128 ? launch<128, __nv_bfloat16>(a, mq, mk, mv, stream)
+                           : launch<64, __nv_bfloat16>(a, mq, mk, mv, stream);
+  return head_dim == 128 ? launch<128, __half>(a, mq, mk, mv, stream) : launch<64, __half>(a, mq, mk, mv, stream);
+}
+
+}  // namespace dsa

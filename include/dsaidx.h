@@ -70,6 +70,8 @@ typedef struct CUstream_st *dsa_stream_t; /* same type as cudaStream_t */
 #define DSA_DEVERR_TIMEOUT 8u     /* a pipeline wait gave up (about 1 s); kernel returned early */
 #define DSA_DEVERR_SEQ_RANGE 16u  /* seq_len < q_len, or seq_len beyond the block-table row */
 #define DSA_DEVERR_POS_RANGE 32u  /* a RoPE position outside [0, max_pos): the row is left unrotated */
+#define DSA_DEVERR_PAGE_STATE 64u /* a page or sequence not in the state a page call needs (see there) */
+#define DSA_DEVERR_NO_PAGE 128u   /* no free page left for a forked sequence */
 
 #define DSA_HEADS 64
 #define DSA_HEAD_DIM 128
@@ -336,6 +338,193 @@ DSA_API int dsa_schedule_build(int32_t n_layers, int32_t use_index_cache, int32_
 DSA_API int dsa_gather_rows(const uint8_t *rows, int64_t num_rows, int64_t row_bytes, int64_t row_stride,
                             const int32_t *physical, int64_t n_tokens, int32_t topk, uint8_t *out,
                             int32_t *dev_err, dsa_stream_t stream);
+
+/* ------------------------------------------------ the attention KV cache */
+/* The attention that reads the indexer's selection, or every key, and the
+ * cache it reads. The pages cited above leave the KV rows' format open; here
+ * a token has, per KV head, one K row and one V row of head_dim elements,
+ * bf16 or fp16, in pages of 64 slots like the indexer's cache, so one block
+ * table and one slot mapping serve both. Each of the two tensors has strides
+ * of its own, in elements: page, slot within the page, head; the row itself is
+ * contiguous. Any order of the axes works: [num_blocks, 64, heads, head_dim],
+ * [num_blocks, heads, 64, head_dim], K and V interleaved in one allocation.
+ *   k, v        device, 16-byte aligned
+ *   head_dim    64 or 128
+ *   num_blocks  pages, >= 1 (packed rows in dsa_attn_prompt: rows of k and v)
+ *   strides     multiples of 8, at least head_dim, below 2^39; the page stride
+ *               of a one-page cache and the head stride of a one-head cache
+ *               are not used. */
+#define DSA_BF16 0
+#define DSA_FP16 1
+typedef struct DsaKv {
+  void *k;
+  void *v;
+  int32_t dtype;        /* DSA_BF16 or DSA_FP16 */
+  int32_t num_kv_heads; /* >= 1 */
+  int32_t head_dim;     /* 64 or 128 */
+  int64_t num_blocks;
+  int64_t k_page_stride, k_slot_stride, k_head_stride;
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+} DsaKv;
+
+/* A step's K and V rows into the cache at their slots (slot = page*64 + slot
+ * within the page, the slot mapping of dsa_indexer_k_quant_write).
+ *   k, v          device [n_tokens, num_kv_heads, head_dim] of kv->dtype,
+ *                 16-byte aligned; row and head strides in elements, multiples
+ *                 of 8 (column views of a fused projection go in as they are)
+ *   slot_mapping  device int64 [n_tokens]; -1 = padding token, skipped
+ *   kv            the cache, written in place
+ * Slots must be distinct: of two tokens with one slot either may remain.
+ * Other slots outside the cache are skipped and flag DSA_DEVERR_SLOT_RANGE. */
+DSA_API int dsa_kv_write(const void *k, int64_t k_row_stride, int64_t k_head_stride, const void *v,
+                 int64_t v_row_stride, int64_t v_head_stride, int64_t n_tokens,
+                 const int64_t *slot_mapping, const DsaKv *kv, int32_t *dev_err, dsa_stream_t stream);
+
+/* ------------------------------------------------------------- attention */
+/* For query head e of token t, which shares KV head h = e / (num_heads /
+ * num_kv_heads), and the keys j that the token sees:
+ *   s_j = scale * q[t,e].k[j,h]
+ *   out[t,e] = sum_j e^(s_j) v[j,h] / sum_j e^(s_j),  lse[t,e] = ln sum_j e^(s_j).
+ * Scores, sums and the running maximum are fp32; the weights e^(s_j - max) are
+ * rounded to the inputs' type for the product with V, the result once more
+ * when it is stored. A token that sees no key gets out = 0, lse = -infinity.
+ * Keys that a token does not see have no influence on its row, whatever bits
+ * they hold (NaN and infinities included); a visible NaN gives NaN.
+ *   q, out   device [T, num_heads, head_dim] of the cache's type, 16-byte
+ *            aligned; row and head strides in elements, multiples of 8
+ *   lse      device fp32 [T, num_heads] contiguous, or NULL
+ *   num_heads  a multiple of kv->num_kv_heads
+ *   scale    <= 0 selects head_dim^-0.5 */
+typedef struct DsaAttn {
+  const void *q;
+  int64_t q_row_stride, q_head_stride;
+  void *out;
+  int64_t out_row_stride, out_head_stride;
+  float *lse;
+  int32_t num_heads;
+  float scale;
+} DsaAttn;
+
+/* The decode tokens of a batch, rows [0, num_decode_tokens) (one or several
+ * tokens per request), each over all keys it sees in its request's pages: keys
+ * [0, seq_lens[r] - q_len[r] + i] for query token i of request r. A padding
+ * request with seq_len 0 gives empty rows. Rows behind the decode tokens are
+ * left as they were. batch->num_blocks must equal kv->num_blocks and every
+ * seq_len is at most max_seq_len. The length of the keys is split over CTAs
+ * where that helps and joined in a fixed order: the same call on the same
+ * device gives the same bits.
+ *   ws, ws_bytes  device scratch, 16-byte aligned, of
+ *                 dsa_attn_decode_workspace_size() bytes; its contents need not
+ *                 be kept between calls, and calls that may overlap on the GPU
+ *                 need one each
+ * Flags: DSA_DEVERR_SEQ_RANGE (request id outside the decode requests, token
+ * outside its request, seq_len negative or beyond the block-table row or
+ * max_seq_len: the row is empty), DSA_DEVERR_BLOCK_RANGE (the page's keys are
+ * left out). */
+DSA_API size_t dsa_attn_decode_workspace_size(const DsaBatch *batch, int32_t num_heads,
+                                      int32_t num_kv_heads, int32_t head_dim);
+DSA_API int dsa_attn_decode(const DsaBatch *batch, const DsaKv *kv, const DsaAttn *attn, void *ws,
+                    size_t ws_bytes, int32_t *dev_err, dsa_stream_t stream);
+
+/* The sparse attention: token t over the physical slots that the indexer
+ * selected for it (dsa_topk_logical_to_physical, or phys_buf of the layer
+ * runner, as it stands in the consumer callback).
+ *   physical  device int32 [n_tokens, topk]: slots page*64 + slot, -1 = none,
+ *             in any order and anywhere in the row; a slot named twice counts
+ *             twice
+ *   topk      >= 1
+ *   ws        as for dsa_attn_decode, dsa_attn_selected_workspace_size() bytes
+ * Other slots outside the cache flag DSA_DEVERR_ID_RANGE and are left out. */
+DSA_API size_t dsa_attn_selected_workspace_size(int64_t n_tokens, int32_t topk, int32_t num_heads,
+                                        int32_t num_kv_heads, int32_t head_dim);
+DSA_API int dsa_attn_selected(const DsaKv *kv, const DsaAttn *attn, const int32_t *physical,
+                      int64_t n_tokens, int32_t topk, void *ws, size_t ws_bytes, int32_t *dev_err,
+                      dsa_stream_t stream);
+
+/* The prefill tokens of a batch, rows [num_decode_tokens, num_tokens): whole
+ * prompts or chunks of them, packed one request after the other. Query token i
+ * of request r sees keys [0, seq_lens[r] - q_len[r] + i]. Other rows are left
+ * as they were.
+ *   kv_start  NULL: the keys are in the paged cache, through the block table
+ *             (kv->num_blocks must equal batch->num_blocks);
+ *             else device int32 [num_reqs]: K and V are packed rows [rows,
+ *             heads, head_dim] (kv->num_blocks = rows, the slot stride is the
+ *             row stride, no page stride) and key s of request r is row
+ *             kv_start[r] + s; the block table is not used
+ * Flags: DSA_DEVERR_SEQ_RANGE (negative q_len, seq_len negative or beyond the
+ * block-table row, max_seq_len or the packed rows: the request's rows are
+ * empty), DSA_DEVERR_BLOCK_RANGE (the rows that see the page are unspecified),
+ * DSA_DEVERR_TIMEOUT. No workspace. */
+DSA_API int dsa_attn_prompt(const DsaBatch *batch, const DsaKv *kv, const int32_t *kv_start,
+                    const DsaAttn *attn, int32_t *dev_err, dsa_stream_t stream);
+
+/* ------------------------------------------------------ pages of a cache */
+/* Upkeep of sequences' pages: a pool of num_blocks pages with a reference
+ * count each (0 = free), and per sequence a block-table row and a length. The
+ * caches of all layers (K, V, the indexer's) share the pool; page p of every
+ * cache moves with it.
+ *   refs         device int32 [num_blocks], 16-byte aligned
+ *   block_table  device int32 [n_rows, bt_stride]
+ *   seq_lens     device int32 [n_rows]: ceil(len/64) entries of a row count
+ *   caches       host array [n_caches] (n_caches may be 0): page p is
+ *                page_bytes bytes (a multiple of 16) at base + p*page_stride
+ *                (device, 16-byte aligned; stride a multiple of 16, at least
+ *                page_bytes)
+ *   ws           device scratch, 16-byte aligned, of dsa_pages_workspace_size()
+ *                bytes (n = the call's list length), as for dsa_attn_decode
+ * The calls change refs, block_table and seq_lens in place and depend only on
+ * their contents, never on timing. */
+typedef struct DsaPages {
+  int32_t *refs;
+  int64_t num_blocks;
+  int32_t *block_table;
+  int64_t bt_stride;
+  int32_t n_rows;
+  int32_t *seq_lens;
+} DsaPages;
+typedef struct DsaCacheDesc {
+  void *base;
+  int64_t page_bytes;
+  int64_t page_stride;
+} DsaCacheDesc;
+DSA_API size_t dsa_pages_workspace_size(int64_t num_blocks, int32_t n);
+
+/* Copy page src[i] over page dst[i] in every cache, for i < n (device int32
+ * lists). A pair with a -1 is padding. A page may be the source of many pairs
+ * and the destination of one: of pairs with one destination the first stands,
+ * a pair whose destination is also a source is skipped, and both flag
+ * DSA_DEVERR_PAGE_STATE; pages outside the pool are skipped and flag
+ * DSA_DEVERR_BLOCK_RANGE. Counts and tables are not touched. */
+DSA_API int dsa_pages_copy(const DsaCacheDesc *caches, int32_t n_caches, int64_t num_blocks,
+                   const int32_t *src, const int32_t *dst, int32_t n, void *ws, size_t ws_bytes,
+                   int32_t *dev_err, dsa_stream_t stream);
+
+/* Fork sequences: row children[i] becomes a copy of row parents[i], i < n.
+ * Full pages are shared (counts up); a part-filled last page is copied in
+ * every cache to a fresh page, the lowest free ones in the order of the list.
+ * A child row must be empty (length 0), also of other children; entries that
+ * are not, and all but the first of those with one child, are skipped and flag
+ * DSA_DEVERR_PAGE_STATE. A child whose fresh page is not to be had stays empty
+ * (DSA_DEVERR_NO_PAGE). Rows outside [0, n_rows) and parents whose length is
+ * negative or beyond the row flag DSA_DEVERR_SEQ_RANGE, table entries outside
+ * the pool DSA_DEVERR_BLOCK_RANGE. */
+DSA_API int dsa_pages_fork(const DsaPages *pages, const int32_t *parents, const int32_t *children, int32_t n,
+                   const DsaCacheDesc *caches, int32_t n_caches, void *ws, size_t ws_bytes,
+                   int32_t *dev_err, dsa_stream_t stream);
+
+/* End sequences: the counts of the rows' pages go down by one, their entries
+ * become -1 and their lengths 0. A row named twice ends once. A page whose
+ * count is 0 already flags DSA_DEVERR_PAGE_STATE. No workspace. */
+DSA_API int dsa_pages_free(const DsaPages *pages, const int32_t *rows, int32_t n, int32_t *dev_err,
+                   dsa_stream_t stream);
+
+/* Compact the pool: with U pages in use (count > 0) those at or above U move
+ * to the free pages below U, the k-th of them (ascending) to the k-th free one;
+ * bytes in every cache, counts, and all block-table entries that name a moved
+ * page follow. seq_lens is not used. Afterwards pages [U, num_blocks) are free
+ * (their bytes stay as they were). */
+DSA_API int dsa_pages_compact(const DsaPages *pages, const DsaCacheDesc *caches, int32_t n_caches, void *ws,
+                      size_t ws_bytes, int32_t *dev_err, dsa_stream_t stream);
 
 /* ------------------------------------------- the layer-schedule runner */
 /* One decoding step over a stack of DSA layers with IndexCache: [IC] F/S
