@@ -360,56 +360,71 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     } else if (warp == 9) {
       // ----------------------------------------------------------------- MMA
-      if (lane == 0 && n_tiles > 0) {
+      // The warp waits as one; an elected thread issues. (With one lane alone
+      // in the loop, each MMA took about 115 cycles to issue, whatever its size.)
+      if (n_tiles > 0) {
         constexpr uint32_t kIdS = f16_idesc(E::kFmt, kKeys, false), kIdO = f16_idesc(E::kFmt, D, true);
         const uint64_t qd[2] = {sw128_kmajor_desc(smem_u32(smem)), sw128_kmajor_desc(smem_u32(smem + C::kTileBytes))};
         auto scores = [&](int x, int st) {
           const uint64_t kd = sw128_kmajor_desc(smem_u32(kv + st * C::kTileBytes));
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = ((k / 4) * C::kColBytes + (k % 4) * 32) >> 4;
-            mma_f16_ss(tmem + x * 128, qd[x] + off, kd + off, kIdS, k > 0);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t off = ((k / 4) * C::kColBytes + (k % 4) * 32) >> 4;
+              mma_f16_ss(tmem + x * 128, qd[x] + off, kd + off, kIdS, k > 0);
+            }
+            mma_commit(&sfull[x]);
           }
-          mma_commit(&sfull[x]);
+          __syncwarp();
         };
-        bool ok = mbar_wait(&full[0], 0, abort_flag, a.err);
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)) != 0;
+        };
+        auto release = [&](uint64_t* bar) {
+          if (elect_one()) mma_commit(bar);
+          __syncwarp();
+        };
+        bool ok = wait(&full[0], 0);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (nt[x] == 0 || !ok) continue;
-          ok = mbar_wait(&qfull[x], 0, abort_flag, a.err);
+          ok = wait(&qfull[x], 0);
           if (ok) scores(x, 0);
         }
-        mma_commit(&empty[0]);
+        release(&empty[0]);
         for (int j = 0; j < n_tiles && ok; ++j) {
           const int vseq = 2 * j + 1, kseq = 2 * j + 2;
           const int vst = vseq % S, kst = kseq % S;
-          ok = mbar_wait(&full[vst], (vseq / S) & 1, abort_flag, a.err);
+          ok = wait(&full[vst], (vseq / S) & 1);
           const uint64_t vd = sw128_mnmajor_desc(smem_u32(kv + vst * C::kTileBytes));
           bool have_k = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (ok && j < nt[x]) {
-              ok = mbar_wait(&pfull[x], j & 1, abort_flag, a.err);
+              ok = wait(&pfull[x], j & 1);
               if (ok) {
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                  mma_f16_ts(tmem + C::kO + x * D, tmem + x * 128 + k * 8, vd + ((k * 16 * 128) >> 4), kIdO,
-                             j > 0 || k > 0);
-                if (j == nt[x] - 1) mma_commit(&ofull[x]);
+                  for (int k = 0; k < kKeys / 16; ++k)
+                    mma_f16_ts(tmem + C::kO + x * D, tmem + x * 128 + k * 8, vd + ((k * 16 * 128) >> 4), kIdO,
+                               j > 0 || k > 0);
+                  if (j == nt[x] - 1) mma_commit(&ofull[x]);
+                }
+                __syncwarp();
               }
             }
-            if (x == 1) mma_commit(&empty[vst]);
+            if (x == 1) release(&empty[vst]);
             if (ok && j + 1 < nt[x]) {
-              if (!have_k) ok = mbar_wait(&full[kst], (kseq / S) & 1, abort_flag, a.err);
+              if (!have_k) ok = wait(&full[kst], (kseq / S) & 1);
               have_k = true;
               if (ok) scores(x, kst);
             }
           }
-          if (have_k) mma_commit(&empty[kst]);
+          if (have_k) release(&empty[kst]);
         }
         if (*abort_flag) {  // giving up: let the MMAs in flight end before TMEM is freed
-          mma_commit(done);
+          release(done);
           const unsigned long long until = global_ns() + kWaitLimitNs;
           while (!mbar_try_wait(smem_u32(done), 0) && global_ns() < until) {
           }
