@@ -4,9 +4,12 @@
 //   S = Q K^T,  P = 2^(S scale log2(e) - M),  O = P V,  out = O / sum(P),
 //   lse = ln 2 * (M + log2 sum(P))
 // tile by tile over the keys. Any M gives the same quotient; it only has to
-// keep P in range, so a row's M is raised (and its O and sum rescaled) only
-// when a score passes it by more than 2^8. That makes the rescaling of O, a
-// round trip through TMEM, rare, and lets the softmax warps do it themselves.
+// keep P in range. So a row's M is its maximum in the first tile, and P of a
+// later tile is computed by the M at hand, without a search for the maximum:
+// only when a row's weights come out too large is M raised (its O and sum
+// rescaled) and P computed again. M never sits above a score that was seen, so
+// the weights cannot all underflow. The rescaling of O, a round trip through
+// TMEM, is rare, and the softmax warps do it themselves.
 //
 // What bounds it: 4*D operations per (query head, visible pair), the bf16 /
 // fp16 rate of the tensor cores, with 128x128 tiles of S needing one exponential
@@ -21,7 +24,7 @@
 //    P V (never through shared memory), rescaling, and the final store.
 //  * warp 8: TMA. K and V tiles take turns in one ring (D = 128: five 32 KB
 //    stages); a page (64 slots of a head) is one box per 64 columns.
-//  * warp 9: issues the MMAs. V is read as stored, keys along rows: B is
+//  * warp 9: issues the MMAs, the tiles taking turns. V is read as stored, keys along rows: B is
 //    "MN-major", K and Q are K-major; all in the 128-byte swizzle.
 //  * TMEM: S/P of both tiles (2 x 128 columns), O of both (2 x D).
 // CTAs are numbered from the last query tile of the last request down, so the
@@ -43,12 +46,11 @@ constexpr int kKeys = 128;      // keys per tile
 constexpr int kSoftWarps = 8;
 // Three warpgroups, the third with two idle warps: registers move between
 // warpgroups. Launched with 168 a thread (384 * 168 = 64512), the softmax
-// warpgroups take 224 (a row of S) and the third keeps 56: 256 * 224 + 128 * 56
+// warpgroups take 208 (a row of S) and the third keeps 88: 256 * 208 + 128 * 88
 // = 64512.
 constexpr int kPromptThreads = 32 * (kSoftWarps + 4);
-constexpr int kSoftRegs = 224, kIssueRegs = 56;
+constexpr int kSoftRegs = 208, kIssueRegs = 88;
 static_assert(2 * 128 * kSoftRegs + 128 * kIssueRegs <= kPromptThreads * 168, "register split");
-constexpr float kSlackP = 8.0f;
 
 template <int D>
 struct PromptCfg {
@@ -72,7 +74,8 @@ struct PElem;
 template <>
 struct PElem<__nv_bfloat16> {
   static constexpr uint32_t kFmt = 1;
-  static constexpr float kHead = 0.0f;         // bf16 has fp32's exponents
+  // bf16 has fp32's exponents: weights may reach 2^30 before the reference moves.
+  static constexpr float kHead = 0.0f, kMaxSum = 1073741824.0f;
   static constexpr uint32_t kExp = 0x7F80u;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -82,7 +85,10 @@ struct PElem<__nv_bfloat16> {
 template <>
 struct PElem<__half> {
   static constexpr uint32_t kFmt = 0;
-  static constexpr float kHead = 6.0f;         // M sits 6 below the maximum: P <= 2^14, smallest step 2^-30 of it
+  // The reference is set 4 below a maximum and moves when a row's weights in a
+  // tile sum to more than 2^15 (fp16 holds 65504): the least step of a weight,
+  // 2^-24, is 2^-28 of the largest or less.
+  static constexpr float kHead = 4.0f, kMaxSum = 32768.0f;
   static constexpr uint32_t kExp = 0x7C00u;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __half2 v = __floats2half2_rn(a, b);
@@ -153,6 +159,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -219,6 +230,35 @@ __device__ __forceinline__ PromptTile find_tile(const PromptArgs& a, int rank, b
 // Keys visible to the row at position pos.
 __device__ __forceinline__ int visible(int pos, int keys) { return min(max(pos + 1, 0), keys); }
 
+// A row's weights of one tile, packed as the A operand, and their sum: S from
+// TMEM, 2^(s * scale + ref2); columns from lim on are out (EDGE only).
+template <typename T, bool EDGE>
+__device__ __forceinline__ float weights(uint32_t ts, int lim, uint64_t sc2, uint64_t ref2, uint32_t (&p)[2][32]) {
+  using E = PElem<T>;
+  uint64_t sum[4] = {0, 0, 0, 0};
+  uint32_t s[4][32];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_wait32(s[c]);
+#pragma unroll
+  for (int i = 0; i < 64; ++i) {
+    const int c = i / 16, k = (i % 16) * 2;
+    float a = __uint_as_float(s[c][k]), b = __uint_as_float(s[c][k + 1]);
+    if (EDGE) {
+      a = 2 * i < lim ? a : -INFINITY;
+      b = 2 * i + 1 < lim ? b : -INFINITY;
+    }
+    const float2 e = unpack_f32x2(fma_f32x2(pack_f32x2(a, b), sc2, ref2));
+    const float e0 = pex2(e.x), e1 = pex2(e.y);
+    // summed before P is rounded for the MMA: the rounding enters the numerator only
+    sum[i & 3] = add_f32x2(sum[i & 3], pack_f32x2(e0, e1));
+    p[i / 32][i % 32] = E::pack(e0, e1);
+  }
+  const float2 l = unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])));
+  return l.x + l.y;
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -263,7 +303,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], (nt[0] > 0) + (nt[1] > 0) > 0 ? (nt[0] > 0) + (nt[1] > 0) : 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&qfull[x], 1);
@@ -359,12 +399,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
       }
     } else if (warp == 9) {
-      // ----------------------------------------------------------------- MMA
-      // The warp waits as one; an elected thread issues. (With one lane alone
-      // in the loop, each MMA took about 115 cycles to issue, whatever its size.)
+      // --------------------------------------------------------------- MMA
+      // The warp waits as one and an elected thread issues: with one lane alone
+      // in the loop each MMA took about 115 cycles to issue, whatever its size.
+      // One warp for both tiles keeps them out of step, one's softmax under the
+      // other's MMAs: with a warp per tile they fell into step (1350 -> 1230
+      // TFLOP/s at 4 x 8192, 64/8 heads of 128).
       if (n_tiles > 0) {
         constexpr uint32_t kIdS = f16_idesc(E::kFmt, kKeys, false), kIdO = f16_idesc(E::kFmt, D, true);
         const uint64_t qd[2] = {sw128_kmajor_desc(smem_u32(smem)), sw128_kmajor_desc(smem_u32(smem + C::kTileBytes))};
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)) != 0;
+        };
         auto scores = [&](int x, int st) {
           const uint64_t kd = sw128_kmajor_desc(smem_u32(kv + st * C::kTileBytes));
           if (elect_one()) {
@@ -377,13 +423,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           __syncwarp();
         };
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)) != 0;
-        };
-        auto release = [&](uint64_t* bar) {
-          if (elect_one()) mma_commit(bar);
-          __syncwarp();
-        };
         bool ok = wait(&full[0], 0);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -391,40 +430,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           ok = wait(&qfull[x], 0);
           if (ok) scores(x, 0);
         }
-        release(&empty[0]);
+        int vst = 1 % S, kst = 2 % S;
+        uint32_t vpar = 0, kpar = 0;
+        ok = ok && wait(&full[vst], vpar);
         for (int j = 0; j < n_tiles && ok; ++j) {
-          const int vseq = 2 * j + 1, kseq = 2 * j + 2;
-          const int vst = vseq % S, kst = kseq % S;
-          ok = wait(&full[vst], (vseq / S) & 1);
           const uint64_t vd = sw128_mnmajor_desc(smem_u32(kv + vst * C::kTileBytes));
           bool have_k = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (ok && j < nt[x]) {
-              ok = wait(&pfull[x], j & 1);
-              if (ok) {
-                tc_fence_after();
-                if (elect_one()) {
+            if (j < nt[x]) {
+              ok = ok && wait(&pfull[x], j & 1);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
 #pragma unroll
-                  for (int k = 0; k < kKeys / 16; ++k)
-                    mma_f16_ts(tmem + C::kO + x * D, tmem + x * 128 + k * 8, vd + ((k * 16 * 128) >> 4), kIdO,
-                               j > 0 || k > 0);
-                  if (j == nt[x] - 1) mma_commit(&ofull[x]);
-                }
-                __syncwarp();
+                for (int k = 0; k < kKeys / 16; ++k)
+                  mma_f16_ts(tmem + C::kO + x * D, tmem + x * 128 + k * 8, vd + ((k * 16 * 128) >> 4), kIdO,
+                             j > 0 || k > 0);
+                if (j == nt[x] - 1) mma_commit(&ofull[x]);
               }
+              __syncwarp();
             }
-            if (x == 1) release(&empty[vst]);
             if (ok && j + 1 < nt[x]) {
-              if (!have_k) ok = wait(&full[kst], (kseq / S) & 1);
+              if (!have_k) ok = wait(&full[kst], kpar);
               have_k = true;
               if (ok) scores(x, kst);
             }
           }
-          if (have_k) release(&empty[kst]);
+          for (int i = 0; i < 2; ++i) {
+            if (++vst == S) vst = 0, vpar ^= 1;
+            if (++kst == S) kst = 0, kpar ^= 1;
+          }
+          if (ok && j + 1 < n_tiles) ok = wait(&full[vst], vpar);
         }
         if (*abort_flag) {  // giving up: let the MMAs in flight end before TMEM is freed
-          release(done);
+          if (elect_one()) mma_commit(done);
+          __syncwarp();
           const unsigned long long until = global_ns() + kWaitLimitNs;
           while (!mbar_try_wait(smem_u32(done), 0) && global_ns() < until) {
           }
@@ -445,82 +486,75 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const float NEG = -INFINITY;
     float M = NEG, L = 0.0f;
     bool ok = true;
+    const bool leader = (warp & 3) == 0 && lane == 0;
+    int kst = 0, vst = 1 % S;  // ring stages of tile j
+    uint32_t vpar = 0;
     for (int j = 0; j < my_nt; ++j) {
-      ok = mbar_wait(&sfull[x], j & 1, abort_flag, a.err);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&sfull[x], j & 1, abort_flag, a.err)) != 0;
+      if (!ok) break;
       tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_wait32(s[c]);
+      if (leader) {  // the scores are complete, and with them everything this tile's MMAs read before
+        mbar_arrive(&empty[kst]);
+        if (j > 0) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
+      }
       const int lim = vis - j * kKeys;  // visible columns
       const bool edge = __any_sync(0xffffffffu, lim < kKeys);
-      if (edge) {
+      // The weights by the reference at hand, without looking for the maximum
+      // first: only where a row has none yet, or its weights come out too large
+      // (or not a number), the maximum is taken and the weights once more.
+      // A row's decision is its own: no other row has a part in its bits.
+      bool raise = M == NEG && lim > 0;
+      uint32_t p[2][32];
+      float add;
+      for (int attempt = 0;; ++attempt) {
+        if (__any_sync(0xffffffffu, raise)) {
+          float top = NEG;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[32];
+            tmem_ld32(ts + c * 32, s);
+            tmem_wait32(s);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c * 32 + i >= lim) s[c][i] = __float_as_uint(NEG);
-      }
-      float mx[4];
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i >= lim) s[i] = __float_as_uint(NEG);
+            float mx[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        mx[c] = __uint_as_float(s[c][0]);
+            for (int i = 0; i < 32; ++i)
+              mx[i & 3] = i < 4 ? __uint_as_float(s[i]) : fmaxf(mx[i & 3], __uint_as_float(s[i]));
+            top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          }
+          const float n = raise ? fmaxf(M, top * a.scale_log2 - E::kHead) : M;
+          const float f = !raise ? 1.0f : M == NEG ? 0.0f : pex2(M - n);
+          M = n;
+          L *= f;
+          if (j > 0) {  // O is complete up to tile j - 1: its MMAs precede this tile's scores
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(to + c * 32, o);
+              tmem_wait32(o);
 #pragma unroll
-        for (int i = 1; i < 32; ++i) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][i]));
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-      if (__any_sync(0xffffffffu, top > M + (E::kHead + kSlackP))) {
-        const float n = fmaxf(M, top - E::kHead);
-        const float f = M == NEG ? 0.0f : pex2(M - n);
-        M = n;
-        L *= f;
-        if (j > 0) {  // O is complete up to tile j - 1: its MMAs precede this tile's scores
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(to + c * 32, o);
-            tmem_wait32(o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(to + c * 32, o);
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(to + c * 32, o);
+            }
           }
         }
+        const float ref = M == NEG ? 0.0f : M;
+        const uint64_t sc2 = pack_f32x2(a.scale_log2, a.scale_log2), ref2 = pack_f32x2(-ref, -ref);
+        add = edge ? weights<T, true>(ts, lim, sc2, ref2, p) : weights<T, false>(ts, lim, sc2, ref2, p);
+        raise = !raise && !(add <= E::kMaxSum);
+        if (attempt == 1 || !__any_sync(0xffffffffu, raise)) break;
       }
-      const float ref = M == NEG ? 0.0f : M;
-      const uint64_t sc2 = pack_f32x2(a.scale_log2, a.scale_log2), ref2 = pack_f32x2(-ref, -ref);
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      L += add;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t p[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int c = 2 * half + i / 16, k = (i % 16) * 2;
-          const float2 e = unpack_f32x2(
-              fma_f32x2(pack_f32x2(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), sc2, ref2));
-          const float e0 = pex2(e.x), e1 = pex2(e.y);
-          // summed before P is rounded for the MMA: the rounding enters the numerator only
-          sum[i & 3] += e0 + e1;
-          p[i] = E::pack(e0, e1);
-        }
-        tmem_st32(ts + half * 32, p);
-      }
-      L += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      // V in a tile cut by the causal edge or the sequence's end
+      for (int half = 0; half < 2; ++half) tmem_st32(ts + half * 32, p[half]);
+      // V in a tile cut by the causal edge or the sequence's end, before its first use
       const int lo = visible(my_pos, tile.keys) - j * kKeys;  // columns every row of the tile sees
       if (lo < kKeys && (x == 0 || j >= nt[0])) {
-        const int vseq = 2 * j + 1;
-        ok = mbar_wait(&full[vseq % S], (vseq / S) & 1, abort_flag, a.err);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[vst], vpar, abort_flag, a.err)) != 0;
+        if (!ok) break;
         // thread r: key row r of the tile, which lies at 128-byte row r of each 64-column block
-        uint8_t* v = kv + (vseq % S) * C::kTileBytes + r * 128;
+        uint8_t* v = kv + vst * C::kTileBytes + r * 128;
         const bool behind = j * kKeys + r >= tile.keys;
         bool bad = false;
         for (int c = 0; c < D / 64; ++c)
@@ -553,14 +587,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           atomicMax(bad_hi, j);
         }
         fence_proxy_async();
+        __syncwarp();
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&pfull[x]);
+      kst += 2;
+      if (kst >= S) kst -= S;
+      vst += 2;
+      if (vst >= S) vst -= S, vpar ^= 1;
     }
     // ---- the row's result
     if (ok && my_nt > 0) ok = mbar_wait(&ofull[x], 0, abort_flag, a.err);
+    if (leader && ok && my_nt > 0) {  // the stages that only the other tile still reads
+      const int other = x == 0 ? nt[1] : nt[0];
+      if (my_nt < other) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
+      for (int i = 2 * my_nt; i < 2 * other && ok; ++i) {
+        ok = mbar_wait(&full[i % S], (i / S) & 1, abort_flag, a.err);
+        mbar_arrive(&empty[i % S]);
+      }
+    }
     if (__all_sync(0xffffffffu, ok)) {
       tc_fence_after();
       const int my_head = x == 0 ? head[0] : head[1];
