@@ -19,14 +19,16 @@
 // K and V tiles (128 keys): two query heads of one KV head where the group is
 // even, else two consecutive token tiles of one head. While one tile's softmax
 // runs, the tensor cores run the other tile's P V and next Q K^T.
-//  * warps 0-3 / 4-7: softmax of tile 0 / 1, one row per thread: S from TMEM
-//    (128 columns in registers), P back over S's columns as the A operand of
-//    P V (never through shared memory), rescaling, and the final store.
+//  * warps 0-3 / 4-7: softmax of tile 0 / 1, a row per thread: S from TMEM, P
+//    back to TMEM as the A operand of P V (never through shared memory),
+//    rescaling, and the final store.
 //  * warp 8: TMA. K and V tiles take turns in one ring (D = 128: five 32 KB
 //    stages); a page (64 slots of a head) is one box per 64 columns.
-//  * warp 9: issues the MMAs, the tiles taking turns. V is read as stored, keys along rows: B is
-//    "MN-major", K and Q are K-major; all in the 128-byte swizzle.
-//  * TMEM: S/P of both tiles (2 x 128 columns), O of both (2 x D).
+//  * warp 9: issues the MMAs, the tiles taking turns. V is read as stored, keys
+//    along rows: B is "MN-major", K and Q are K-major; all in the 128-byte
+//    swizzle.
+//  * TMEM: S of both tiles (2 x 128 columns), O of both (2 x D), P over S or, at
+//    D = 64, beside it.
 // CTAs are numbered from the last query tile of the last request down, so the
 // longest tiles start first and the short ones fill the tail.
 //
@@ -49,8 +51,9 @@ constexpr int kSoftWarps = 8;
 // warpgroups take 208 (a row of S) and the third keeps 88: 256 * 208 + 128 * 88
 // = 64512.
 constexpr int kPromptThreads = 32 * (kSoftWarps + 4);
+constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
 constexpr int kSoftRegs = 208, kIssueRegs = 88;
-static_assert(2 * 128 * kSoftRegs + 128 * kIssueRegs <= kPromptThreads * 168, "register split");
+static_assert(32 * kSoftWarps * kSoftRegs + 128 * kIssueRegs <= kPromptThreads * 168, "register split");
 
 template <int D>
 struct PromptCfg {
@@ -62,11 +65,17 @@ struct PromptCfg {
   static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
   static constexpr int kNumBars = 2 * kStages + 2 + 2 + 2 + 2 + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmemBytes = kOffMisc + 64 + 1024;  // + slack to align the base to 1024
+  static constexpr int kOffCta = kOffMisc + 16;
+  static constexpr int kSmemBytes = kOffCta + 96 + 1024;  // + slack to align the base to 1024
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kO = 256;                   // first column of O
+  // P lies over its S (D = 128: TMEM is full), or beside it: then the next
+  // tile's scores do not wait for P V.
+  static constexpr bool kOwnP = D == 64;
+  static constexpr uint32_t kP = kOwnP ? kO + 2 * D : 0;      // first column of P
+  static constexpr uint32_t kPStep = kOwnP ? kKeys / 2 : 128;  // from tile 0's to tile 1's
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-  static_assert(kO + 2 * D <= kTmemCols, "TMEM budget");
+  static_assert(kO + 2 * D + (kOwnP ? kKeys : 0) <= kTmemCols, "TMEM budget");
 };
 
 template <typename T>
@@ -96,9 +105,10 @@ struct PElem<__half> {
   }
 };
 
+// Volatile: the order in which weights() issues them is kept.
 __device__ __forceinline__ float pex2(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -108,34 +118,36 @@ __host__ __device__ constexpr uint32_t f16_idesc(uint32_t fmt, int N, bool b_mn_
          (static_cast<uint32_t>(N >> 3) << 17) | (128u >> 4 << 24);
 }
 
-// Matrix descriptor of a tile stored row by row along the reduction (keys of
-// V), 64 columns = 128 swizzled bytes a row: 8-row groups 1024 bytes apart,
-// the next 64 columns kKeys rows further.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((kKeys * 128) >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
+// Shared-memory matrix descriptors, both with the 128-byte swizzle and 8-row
+// groups 1024 bytes apart: the high word is one constant, the low word holds
+// the start address (16-byte units) and, for a tile stored row by row along the
+// reduction (V, keys along rows: "MN-major"), the distance of the next 64
+// columns. K-major: sw128_kmajor_desc of the shared header, split.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t kmajor_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t mnmajor_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | (static_cast<uint32_t>((kKeys * 128) >> 4) << 16);
 }
 
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                            uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
       : "memory");
 }
 
@@ -148,15 +160,16 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_
       : "memory");
 }
 
+// This warp's 32 TMEM lanes, 32 columns (the counterpart of tmem_ld32).
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32}; " ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
@@ -231,32 +244,74 @@ __device__ __forceinline__ PromptTile find_tile(const PromptArgs& a, int rank, b
 __device__ __forceinline__ int visible(int pos, int keys) { return min(max(pos + 1, 0), keys); }
 
 // A row's weights of one tile, packed as the A operand, and their sum: S from
-// TMEM, 2^(s * scale + ref2); columns from lim on are out (EDGE only).
+// TMEM, 2^(s * scale + ref); columns from lim on are out (EDGE only). Written as
+// a software pipeline, eight columns' exponentials issued ahead of the previous
+// eight's sums and packing: left to the compiler's order a tile took 1000
+// cycles and more, so 780 (the exponentials alone are 512).
 template <typename T, bool EDGE>
 __device__ __forceinline__ float weights(uint32_t ts, int lim, uint64_t sc2, uint64_t ref2, uint32_t (&p)[2][32]) {
   using E = PElem<T>;
+  constexpr int G = 4;  // pairs of columns per step
   uint64_t sum[4] = {0, 0, 0, 0};
   uint32_t s[4][32];
 #pragma unroll
   for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
 #pragma unroll
   for (int c = 0; c < 4; ++c) tmem_wait32(s[c]);
+  float2 w[2][G];
 #pragma unroll
-  for (int i = 0; i < 64; ++i) {
-    const int c = i / 16, k = (i % 16) * 2;
-    float a = __uint_as_float(s[c][k]), b = __uint_as_float(s[c][k + 1]);
-    if (EDGE) {
-      a = 2 * i < lim ? a : -INFINITY;
-      b = 2 * i + 1 < lim ? b : -INFINITY;
+  for (int g = 0; g <= 64 / G; ++g) {
+    if (g < 64 / G) {
+      float2 x[G];
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int q = g * G + i;
+        float a = __uint_as_float(s[q / 16][(q % 16) * 2]), b = __uint_as_float(s[q / 16][(q % 16) * 2 + 1]);
+        if (EDGE) {
+          a = 2 * q < lim ? a : -INFINITY;
+          b = 2 * q + 1 < lim ? b : -INFINITY;
+        }
+        x[i] = unpack_f32x2(fma_f32x2(pack_f32x2(a, b), sc2, ref2));
+      }
+#pragma unroll
+      for (int i = 0; i < G; ++i) w[g & 1][i] = make_float2(pex2(x[i].x), pex2(x[i].y));
     }
-    const float2 e = unpack_f32x2(fma_f32x2(pack_f32x2(a, b), sc2, ref2));
-    const float e0 = pex2(e.x), e1 = pex2(e.y);
-    // summed before P is rounded for the MMA: the rounding enters the numerator only
-    sum[i & 3] = add_f32x2(sum[i & 3], pack_f32x2(e0, e1));
-    p[i / 32][i % 32] = E::pack(e0, e1);
+    if (g > 0) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int q = (g - 1) * G + i;
+        const float2 e = w[(g - 1) & 1][i];
+        // summed before P is rounded for the MMA: the rounding enters the numerator only
+        sum[i & 3] = add_f32x2(sum[i & 3], pack_f32x2(e.x, e.y));
+        p[q / 32][q % 32] = E::pack(e.x, e.y);
+      }
+    }
   }
   const float2 l = unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])));
   return l.x + l.y;
+}
+
+// What a CTA works on.
+struct PromptCta {
+  PromptTile tile;
+  // the two query tiles: head, first row of q, rows, position of the first, key tiles
+  int head[2], t0[2], rows[2], pos0[2], nt[2];
+};
+
+// V's elements (col, col + 1) of key k as far as they are not finite, else 0.
+template <typename T>
+__device__ __noinline__ float2 non_finite(const PromptArgs& a, const PromptCta& cta, int k, int col) {
+  int64_t at;
+  if (a.kv_start == nullptr) {
+    const int id = __ldg(a.block_table + static_cast<int64_t>(cta.tile.req) * a.bt_stride + k / kBlock);
+    if (id < 0 || id >= a.num_blocks) return make_float2(0.0f, 0.0f);
+    at = id * a.v_page + static_cast<int64_t>(k % kBlock) * a.v_slot;
+  } else {
+    at = static_cast<int64_t>(cta.tile.kv0 + k) * a.v_slot;
+  }
+  const T* v = static_cast<const T*>(a.v) + at + cta.head[0] / a.group * a.v_head + col;
+  const float x = static_cast<float>(v[0]), y = static_cast<float>(v[1]);
+  return make_float2(isfinite(x) ? 0.0f : x, isfinite(y) ? 0.0f : y);
 }
 
 template <int D, typename T>
@@ -284,53 +339,61 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hu = blockIdx.x % a.head_units, rank = blockIdx.x / a.head_units;
-  const PromptTile tile = find_tile(a, rank, hu == 0 && warp == 0);
-  if (!tile.found) return;
-  // the two query tiles: rows, heads, key tiles
-  int head[2], t0[2], rows[2], pos0[2], nt[2];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int shift = a.pair_heads ? 0 : x * kRowsTile;
-    head[x] = a.pair_heads ? 2 * hu + x : hu;
-    t0[x] = tile.t0 + shift;
-    rows[x] = min(kRowsTile, max(0, tile.ntok - shift));
-    pos0[x] = tile.pos0 + shift;
-    nt[x] = rows[x] > 0 ? (visible(pos0[x] + rows[x] - 1, tile.keys) + kKeys - 1) / kKeys : 0;
-  }
-  const int h = head[0] / a.group;
-  const int n_tiles = max(nt[0], nt[1]);
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], (nt[0] > 0) + (nt[1] > 0) > 0 ? (nt[0] > 0) + (nt[1] > 0) : 1);
+  PromptCta& cta = *reinterpret_cast<PromptCta*>(smem + C::kOffCta);
+  if (warp == 0) {
+    const PromptTile tile = find_tile(a, rank, hu == 0);
+    if (lane == 0) {
+      cta.tile = tile;
+      for (int x = 0; x < 2; ++x) {
+        const int shift = a.pair_heads ? 0 : x * kRowsTile;
+        const int rows = min(kRowsTile, max(0, tile.ntok - shift));
+        cta.head[x] = a.pair_heads ? 2 * hu + x : hu;
+        cta.t0[x] = tile.t0 + shift;
+        cta.rows[x] = rows;
+        cta.pos0[x] = tile.pos0 + shift;
+        cta.nt[x] =
+            rows > 0 ? (visible(tile.pos0 + shift + rows - 1, tile.keys) + kKeys - 1) / kKeys : 0;
+      }
+      const int users = (cta.nt[0] > 0) + (cta.nt[1] > 0);
+      for (int s = 0; s < S; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], users > 0 ? users : 1);
+      }
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&qfull[x], 1);
+        mbar_init(&sfull[x], 1);
+        mbar_init(&pfull[x], kSoftWarps / 2);
+        mbar_init(&ofull[x], 1);
+      }
+      mbar_init(done, 1);
+      *abort_flag = 0;
+      *bad_lo = 0x7FFFFFFF;
+      *bad_hi = -1;
+      fence_barrier_init();
     }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&qfull[x], 1);
-      mbar_init(&sfull[x], 1);
-      mbar_init(&pfull[x], 4);
-      mbar_init(&ofull[x], 1);
-    }
-    mbar_init(done, 1);
-    *abort_flag = 0;
-    *bad_lo = 0x7FFFFFFF;
-    *bad_hi = -1;
-    fence_barrier_init();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kTmaWarp && lane == 0) {
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
   }
-  if (warp == 9) tmem_alloc(tmem_slot, C::kTmemCols);
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, C::kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (!cta.tile.found) {  // the grid is an upper bound
+    if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
+    return;
+  }
+  // Kept in shared memory and read where they are used, to spare registers.
+  const volatile PromptCta& w = cta;
+  const int nt[2] = {w.nt[0], w.nt[1]};
+  const int n_tiles = max(nt[0], nt[1]);
 
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-    if (warp == 8) {
+    if (warp == kTmaWarp) {
       // ----------------------------------------------------------------- TMA
       int issued = 0;  // ring stages filled
       bool ok = true;
@@ -341,17 +404,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           mbar_arrive_expect_tx(&qfull[x], C::kTileBytes);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(smem + x * C::kTileBytes + c * C::kColBytes, &tmap_q, &qfull[x], c * 64, head[x], t0[x]);
+            tma_load_3d(smem + x * C::kTileBytes + c * C::kColBytes, &tmap_q, &qfull[x], c * 64, w.head[x], w.t0[x]);
         }
       }
-      const int n_pages = (tile.keys + kBlock - 1) / kBlock;
+      const int keys = w.tile.keys, req = w.tile.req, kv0 = w.tile.kv0, h = w.head[0] / a.group;
+      const int n_pages = (keys + kBlock - 1) / kBlock;
       int32_t ids = 0;
       for (int j = 0; j < n_tiles && ok; ++j) {
         int c2[2], c3[2], boxes;
         if (a.kv_start == nullptr) {
           if ((j & 15) == 0) {  // the next 32 pages
             const int pg = 2 * j + lane;
-            ids = pg < n_pages ? __ldg(a.block_table + static_cast<int64_t>(tile.req) * a.bt_stride + pg) : 0;
+            ids = pg < n_pages ? __ldg(a.block_table + static_cast<int64_t>(req) * a.bt_stride + pg) : 0;
             if (ids < 0 || ids >= a.num_blocks) {
               flag_error(a.err, DSA_DEVERR_BLOCK_RANGE);
               ids = 0;
@@ -362,11 +426,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           c2[0] = c2[1] = 0;
           boxes = 2 * j + 1 < n_pages ? 2 : 1;
         } else {
-          c2[0] = tile.kv0 + j * kKeys;
+          c2[0] = kv0 + j * kKeys;
           c2[1] = c2[0] + kBlock;
           c3[0] = c3[1] = 0;
           // a box may begin behind the last packed row only if it is not loaded at all
-          boxes = j * kKeys + kBlock < tile.keys ? 2 : 1;
+          boxes = j * kKeys + kBlock < keys ? 2 : 1;
         }
         if (lane == 0) {
 #pragma unroll
@@ -398,7 +462,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             while (!mbar_try_wait(smem_u32(&qfull[x]), 0) && global_ns() < until) {
             }
       }
-    } else if (warp == 9) {
+    } else if (warp == kMmaWarp) {
       // --------------------------------------------------------------- MMA
       // The warp waits as one and an elected thread issues: with one lane alone
       // in the loop each MMA took about 115 cycles to issue, whatever its size.
@@ -407,17 +471,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // TFLOP/s at 4 x 8192, 64/8 heads of 128).
       if (n_tiles > 0) {
         constexpr uint32_t kIdS = f16_idesc(E::kFmt, kKeys, false), kIdO = f16_idesc(E::kFmt, D, true);
-        const uint64_t qd[2] = {sw128_kmajor_desc(smem_u32(smem)), sw128_kmajor_desc(smem_u32(smem + C::kTileBytes))};
+        const uint32_t qd = kmajor_lo(smem_u32(smem)), kv0 = smem_u32(kv);
         auto wait = [&](uint64_t* bar, uint32_t parity) {
           return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)) != 0;
         };
         auto scores = [&](int x, int st) {
-          const uint64_t kd = sw128_kmajor_desc(smem_u32(kv + st * C::kTileBytes));
+          const uint32_t kd = kmajor_lo(kv0 + st * C::kTileBytes), qx = qd + ((x * C::kTileBytes) >> 4);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-              const uint64_t off = ((k / 4) * C::kColBytes + (k % 4) * 32) >> 4;
-              mma_f16_ss(tmem + x * 128, qd[x] + off, kd + off, kIdS, k > 0);
+              const uint32_t off = ((k / 4) * C::kColBytes + (k % 4) * 32) >> 4;
+              mma_f16_ss(tmem + x * 128, qx + off, kd + off, kIdS, k > 0);
             }
             mma_commit(&sfull[x]);
           }
@@ -434,28 +498,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         uint32_t vpar = 0, kpar = 0;
         ok = ok && wait(&full[vst], vpar);
         for (int j = 0; j < n_tiles && ok; ++j) {
-          const uint64_t vd = sw128_mnmajor_desc(smem_u32(kv + vst * C::kTileBytes));
+          const uint32_t vd = mnmajor_lo(kv0 + vst * C::kTileBytes);
           bool have_k = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (j < nt[x]) {
-              ok = ok && wait(&pfull[x], j & 1);
-              if (!ok) break;
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                  mma_f16_ts(tmem + C::kO + x * D, tmem + x * 128 + k * 8, vd + ((k * 16 * 128) >> 4), kIdO,
-                             j > 0 || k > 0);
-                if (j == nt[x] - 1) mma_commit(&ofull[x]);
-              }
-              __syncwarp();
-            }
-            if (ok && j + 1 < nt[x]) {
+            if (j >= nt[x]) continue;
+            ok = ok && wait(&pfull[x], j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            auto next_scores = [&]() {
+              if (j + 1 >= nt[x]) return;
               if (!have_k) ok = wait(&full[kst], kpar);
               have_k = true;
               if (ok) scores(x, kst);
+            };
+            if constexpr (C::kOwnP) next_scores();
+            if (!ok) break;
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                mma_f16_ts(tmem + C::kO + x * D, tmem + C::kP + x * C::kPStep + k * 8, vd + ((k * 16 * 128) >> 4),
+                           kIdO, j > 0 || k > 0);
+              if (C::kOwnP || j == nt[x] - 1) mma_commit(&ofull[x]);
             }
+            __syncwarp();
+            if constexpr (!C::kOwnP) next_scores();
           }
           for (int i = 0; i < 2; ++i) {
             if (++vst == S) vst = 0, vpar ^= 1;
@@ -475,17 +542,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ------------------------------------------------------------- softmax
+    // A row per thread, the row's TMEM lane in the quarter that its warp may read.
     const int x = warp >> 2;
-    const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+    const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + C::kO + x * D;
-    const int my_rows = x == 0 ? rows[0] : rows[1];
     const int my_nt = x == 0 ? nt[0] : nt[1];
-    const int my_pos = x == 0 ? pos0[0] : pos0[1];
-    const int vis = visible(my_pos + min(r, my_rows - 1), tile.keys);
+    const int vis = visible(w.pos0[x] + min(r, w.rows[x] - 1), w.tile.keys);
     const float NEG = -INFINITY;
     float M = NEG, L = 0.0f;
     bool ok = true;
+    bool fresh = true;  // some row of the warp may have no reference yet
+    // uniform bounds of what only some tiles need: the first tile that a row of
+    // the warp, and of the tile, does not see whole
+    const int edge_from = __reduce_min_sync(0xffffffffu, vis) / kKeys;
+    const int fix_from = x == 0 ? visible(w.pos0[0], w.tile.keys) / kKeys : max(visible(w.pos0[1], w.tile.keys) / kKeys, nt[0]);
     const bool leader = (warp & 3) == 0 && lane == 0;
     int kst = 0, vst = 1 % S;  // ring stages of tile j
     uint32_t vpar = 0;
@@ -493,41 +564,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(&sfull[x], j & 1, abort_flag, a.err)) != 0;
       if (!ok) break;
       tc_fence_after();
-      if (leader) {  // the scores are complete, and with them everything this tile's MMAs read before
+      if (leader) {  // the scores are complete, and with P in S's columns everything this tile's MMAs read before
         mbar_arrive(&empty[kst]);
-        if (j > 0) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
+        if (!C::kOwnP && j > 0) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
       }
       const int lim = vis - j * kKeys;  // visible columns
-      const bool edge = __any_sync(0xffffffffu, lim < kKeys);
       // The weights by the reference at hand, without looking for the maximum
       // first: only where a row has none yet, or its weights come out too large
-      // (or not a number), the maximum is taken and the weights once more.
-      // A row's decision is its own: no other row has a part in its bits.
-      bool raise = M == NEG && lim > 0;
+      // (or not a number), the maximum is taken and the weights once more. A
+      // row's decision is its own: no other row has a part in its bits.
+      bool raise = fresh && M == NEG && lim > 0;
       uint32_t p[2][32];
       float add;
-      for (int attempt = 0;; ++attempt) {
-        if (__any_sync(0xffffffffu, raise)) {
+      for (int attempt = fresh ? 1 : 0;; ++attempt) {
+        if (attempt > 0) {
           float top = NEG;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t s[32];
             tmem_ld32(ts + c * 32, s);
             tmem_wait32(s);
+            float mx[4] = {NEG, NEG, NEG, NEG};
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (c * 32 + i >= lim) s[i] = __float_as_uint(NEG);
-            float mx[4];
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              mx[i & 3] = i < 4 ? __uint_as_float(s[i]) : fmaxf(mx[i & 3], __uint_as_float(s[i]));
+              if (c * 32 + i < lim) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
             top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
           }
           const float n = raise ? fmaxf(M, top * a.scale_log2 - E::kHead) : M;
           const float f = !raise ? 1.0f : M == NEG ? 0.0f : pex2(M - n);
           M = n;
           L *= f;
-          if (j > 0) {  // O is complete up to tile j - 1: its MMAs precede this tile's scores
+          fresh = __any_sync(0xffffffffu, M == NEG);
+          if (j > 0) {  // O is complete up to tile j - 1: without kOwnP its MMAs precede this tile's scores
+            if (C::kOwnP && !__all_sync(0xffffffffu, mbar_wait(&ofull[x], (j - 1) & 1, abort_flag, a.err))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -541,53 +614,57 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         const float ref = M == NEG ? 0.0f : M;
         const uint64_t sc2 = pack_f32x2(a.scale_log2, a.scale_log2), ref2 = pack_f32x2(-ref, -ref);
-        add = edge ? weights<T, true>(ts, lim, sc2, ref2, p) : weights<T, false>(ts, lim, sc2, ref2, p);
+        add = j >= edge_from ? weights<T, true>(ts, lim, sc2, ref2, p) : weights<T, false>(ts, lim, sc2, ref2, p);
         raise = !raise && !(add <= E::kMaxSum);
-        if (attempt == 1 || !__any_sync(0xffffffffu, raise)) break;
+        if (attempt == 2 || !__any_sync(0xffffffffu, raise)) break;
       }
+      if (!ok) break;
       L += add;
+      if (C::kOwnP && j > 0) {  // the previous tile's P V has read P and V
+        ok = mbar_wait(&ofull[x], (j - 1) & 1, abort_flag, a.err);
+        tc_fence_after();
+        if (leader) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
+        __syncwarp();
+      }
 #pragma unroll
-      for (int half = 0; half < 2; ++half) tmem_st32(ts + half * 32, p[half]);
+      for (int half = 0; half < 2; ++half) tmem_st32(tmem + lanes + C::kP + x * C::kPStep + half * 32, p[half]);
       // V in a tile cut by the causal edge or the sequence's end, before its first use
-      const int lo = visible(my_pos, tile.keys) - j * kKeys;  // columns every row of the tile sees
-      if (lo < kKeys && (x == 0 || j >= nt[0])) {
+      if (j >= fix_from) {
         ok = __all_sync(0xffffffffu, mbar_wait(&full[vst], vpar, abort_flag, a.err)) != 0;
         if (!ok) break;
         // thread r: key row r of the tile, which lies at 128-byte row r of each 64-column block
         uint8_t* v = kv + vst * C::kTileBytes + r * 128;
-        const bool behind = j * kKeys + r >= tile.keys;
+        const bool behind = j * kKeys + r >= w.tile.keys;
         bool bad = false;
-        for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint4* w = reinterpret_cast<uint4*>(v + c * C::kColBytes + i * 16);
-            if (behind) {
-              *w = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 u = *w;
-            bool hit = false;
-            uint32_t* e = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if ((e[q] & E::kExp) == E::kExp) {
-                e[q] &= 0xFFFF0000u;
-                hit = true;
-              }
-              if ((e[q] & (E::kExp << 16)) == (E::kExp << 16)) {
-                e[q] &= 0x0000FFFFu;
-                hit = true;
-              }
-            }
-            if (hit) *w = u;
-            bad |= hit;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          uint4* at = reinterpret_cast<uint4*>(v + (i / 8) * C::kColBytes + (i % 8) * 16);
+          if (behind) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
           }
+          uint4 u = *at;
+          bool hit = false;
+          uint32_t* e = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if ((e[q] & E::kExp) == E::kExp) {
+              e[q] &= 0xFFFF0000u;
+              hit = true;
+            }
+            if ((e[q] & (E::kExp << 16)) == (E::kExp << 16)) {
+              e[q] &= 0x0000FFFFu;
+              hit = true;
+            }
+          }
+          if (hit) *at = u;
+          bad |= hit;
+        }
         if (bad) {
           atomicMin(bad_lo, j);
           atomicMax(bad_hi, j);
         }
         fence_proxy_async();
-        __syncwarp();
       }
       tmem_wait_st();
       tc_fence_before();
@@ -599,7 +676,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (vst >= S) vst -= S, vpar ^= 1;
     }
     // ---- the row's result
-    if (ok && my_nt > 0) ok = mbar_wait(&ofull[x], 0, abort_flag, a.err);
+    if (ok && my_nt > 0) ok = mbar_wait(&ofull[x], C::kOwnP ? (my_nt - 1) & 1 : 0, abort_flag, a.err);
     if (leader && ok && my_nt > 0) {  // the stages that only the other tile still reads
       const int other = x == 0 ? nt[1] : nt[0];
       if (my_nt < other) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
@@ -610,11 +687,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     if (__all_sync(0xffffffffu, ok)) {
       tc_fence_after();
-      const int my_head = x == 0 ? head[0] : head[1];
-      const int my_t0 = x == 0 ? t0[0] : t0[1];
-      const bool mine = r < my_rows;
+      const int my_head = w.head[x], my_t0 = w.t0[x];
+      const bool mine = r < w.rows[x], any = M != NEG;
       T* out = static_cast<T*>(a.out) + static_cast<int64_t>(my_t0 + r) * a.out_row + my_head * a.out_head;
-      const bool any = M != NEG;
       const float inv = any ? 1.0f / L : 0.0f;
       const int blo = my_nt > 0 ? *bad_lo : 0x7FFFFFFF, bhi = my_nt > 0 ? *bad_hi : -1;
 #pragma unroll 1
@@ -629,32 +704,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int i = 0; i < 32; ++i) f[i] = any ? __uint_as_float(o[i]) * inv : 0.0f;
         if (blo <= bhi && mine) {  // non-finite V elements that this row sees
           const int end = min(vis, (bhi + 1) * kKeys);
-          for (int k = blo * kKeys; k < end; ++k) {
-            int64_t at;
-            if (a.kv_start == nullptr) {
-              const int id = __ldg(a.block_table + static_cast<int64_t>(tile.req) * a.bt_stride + k / kBlock);
-              if (id < 0 || id >= a.num_blocks) continue;
-              at = id * a.v_page + static_cast<int64_t>(k % kBlock) * a.v_slot;
-            } else {
-              at = static_cast<int64_t>(tile.kv0 + k) * a.v_slot;
-            }
-            const T* vr = static_cast<const T*>(a.v) + at + h * a.v_head + c * 32;
+          for (int k = blo * kKeys; k < end; ++k)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float e = static_cast<float>(vr[i]);
-              if (!isfinite(e)) f[i] += e;
+            for (int i = 0; i < 32; i += 2) {
+              const float2 n = non_finite<T>(a, cta, k, c * 32 + i);
+              f[i] += n.x;
+              f[i + 1] += n.y;
             }
-          }
         }
         if (mine) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint4 w;
-            w.x = E::pack(f[8 * q], f[8 * q + 1]);
-            w.y = E::pack(f[8 * q + 2], f[8 * q + 3]);
-            w.z = E::pack(f[8 * q + 4], f[8 * q + 5]);
-            w.w = E::pack(f[8 * q + 6], f[8 * q + 7]);
-            *reinterpret_cast<uint4*>(out + c * 32 + q * 8) = w;
+            uint4 u;
+            u.x = E::pack(f[8 * q], f[8 * q + 1]);
+            u.y = E::pack(f[8 * q + 2], f[8 * q + 3]);
+            u.z = E::pack(f[8 * q + 4], f[8 * q + 5]);
+            u.w = E::pack(f[8 * q + 6], f[8 * q + 7]);
+            *reinterpret_cast<uint4*>(out + c * 32 + q * 8) = u;
           }
         }
       }
@@ -666,7 +732,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncwarp();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 template <int D, typename T>
