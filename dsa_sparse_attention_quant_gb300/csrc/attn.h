@@ -29,13 +29,13 @@ struct RowsArgs {
   const int32_t* physical;  // [n_tokens, topk]
   int topk;
   int64_t num_slots;
-  // work: ctas CTAs per pass; split: slices of the flat tile list of at least
-  // min_tiles tiles, else one item per CTA
-  int ctas, min_tiles;
+  // work: split: slices of at least min_tiles tiles of the flat tile list, else
+  // a token per slice; a CTA per slice, KV head and pass
+  int slices, min_tiles;
   bool split;
-  int4* desc;       // [ctas * passes]: {item begun here and continued, its last CTA}
-  float2* part_ml;  // [2 * ctas * passes][rows of a pass]
-  float* part_o;    // [2 * ctas * passes][rows of a pass][D]
+  int2* desc;       // [CTAs]: {token begun here and continued, its last slice}
+  float2* part_ml;  // [2 * CTAs][rows of a pass]
+  float* part_o;    // [2 * CTAs][rows of a pass][D]
   int32_t* err;
 };
 cudaError_t launch_attn_rows(const RowsArgs& a, int head_dim, int dtype, bool selected, cudaStream_t stream);

@@ -71,40 +71,46 @@ int max_keys(const DsaBatch* b) {
 // ---- single rows: how the work is cut, from the host's bounds alone.
 struct RowsPlan {
   int passes, rows;  // passes over the keys, rows of the workspace per pass
-  int64_t items;     // per pass
-  int ctas;          // per pass; at most kRowsCtas when split
+  int64_t slices;    // split: slices of the tile list, else the tokens
+  int64_t ctas;      // per slice, KV head and pass
   bool split;
   size_t off_ml, off_o, bytes;
 };
 
 // Two CTAs per SM on a part of up to 160 SMs.
 constexpr int kRowsCtas = 320;
-// Items of up to this many tiles are not cut: one CTA streams such an item in
-// about the time that the join's launch takes.
+// Tokens of up to this many tiles are not cut while a CTA for each fits on the
+// GPU at once: it streams such a row in about the time that the join's launch
+// takes. More CTAs than that run as slices, whose loads go on across tokens.
 constexpr int kDirectTiles = 8;
 // The least slice: shorter ones pay more for their partials than they save.
 constexpr int kMinTiles = 2;
 
+constexpr int kDirectCtas = 304;
+
+// One slice per CTA place: cut two or four times finer, so that CTAs that stream
+// slower take less, the partials and the CTAs' starts cost more than that gains
+// (32 requests of 4K to 8K keys: 130.8, 134.4, 145.0 us).
 RowsPlan rows_plan(int64_t tokens, int64_t keys, int heads, int hkv, int head_dim, int ctas) {
   RowsPlan p{};
   const int group = heads / hkv;
   p.rows = group <= 16 ? 16 : 32;
   p.passes = (group + p.rows - 1) / p.rows;
-  p.items = tokens * hkv;
   const int64_t tiles = keys > 0 ? (keys + kBlock - 1) / kBlock : 1;
-  p.split = tiles > kDirectTiles;
+  p.split = tiles > kDirectTiles || tokens * hkv * p.passes > kDirectCtas;
+  p.slices = tokens;
   if (p.split) {
-    const int64_t want = (p.items * tiles + kMinTiles - 1) / kMinTiles;
-    int64_t c = ctas / p.passes > 0 ? ctas / p.passes : 1;
-    if (c > want) c = want;
-    p.ctas = static_cast<int>(c);
-    const size_t n = static_cast<size_t>(p.ctas) * p.passes;
-    p.off_ml = align_up(n * sizeof(int4), 256);
+    const int64_t most = (tokens * tiles + kMinTiles - 1) / kMinTiles;
+    int64_t s = ctas / (static_cast<int64_t>(hkv) * p.passes);
+    if (s < 1) s = 1;
+    p.slices = s < most ? s : most;
+  }
+  p.ctas = p.slices * hkv * p.passes;
+  if (p.split) {
+    const size_t n = static_cast<size_t>(p.ctas);
+    p.off_ml = align_up(n * sizeof(int2), 256);
     p.off_o = p.off_ml + align_up(2 * n * p.rows * sizeof(float2), 256);
     p.bytes = p.off_o + 2 * n * p.rows * head_dim * sizeof(float);
-  } else {
-    p.ctas = p.items <= INT_MAX ? static_cast<int>(p.items) : 0;
-    p.bytes = 0;
   }
   return p;
 }
@@ -143,7 +149,7 @@ RowsArgs rows_args(const DsaKv& kv, const DsaAttn& at) {
 int run_rows(RowsArgs& a, int64_t tokens, int64_t keys, const DsaKv& kv, bool selected, void* ws, size_t ws_bytes,
              cudaStream_t stream) {
   RowsPlan need = rows_plan(tokens, keys, a.heads, a.hkv, kv.head_dim, kRowsCtas);
-  if (need.ctas < 1 || need.items * need.passes > INT_MAX) return DSA_EINVAL;
+  if (need.ctas > INT_MAX) return DSA_EINVAL;
   if (need.bytes > 0 && (ws == nullptr || !aligned16(ws))) return DSA_EINVAL;
   if (ws_bytes < need.bytes) return DSA_ENOSPACE;
   int sms;
@@ -152,11 +158,11 @@ int run_rows(RowsArgs& a, int64_t tokens, int64_t keys, const DsaKv& kv, bool se
   const RowsPlan p = rows_plan(tokens, keys, a.heads, a.hkv, kv.head_dim, 2 * sms < kRowsCtas ? 2 * sms : kRowsCtas);
   a.n_tokens = static_cast<int>(tokens);
   a.passes = p.passes;
-  a.ctas = p.ctas;
+  a.slices = static_cast<int>(p.slices);
   a.split = p.split;
   if (p.split) {
     uint8_t* base = static_cast<uint8_t*>(ws);
-    a.desc = reinterpret_cast<int4*>(base);
+    a.desc = reinterpret_cast<int2*>(base);
     a.part_ml = reinterpret_cast<float2*>(base + p.off_ml);
     a.part_o = reinterpret_cast<float*>(base + p.off_o);
   }

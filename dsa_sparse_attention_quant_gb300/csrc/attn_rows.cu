@@ -19,9 +19,11 @@
 // one pass over the keys per 32 heads, the passes' CTAs next to each other so
 // that the later pass finds K and V in L2.
 //
-// Mapping: the (token, KV head, 64-key tile) items form one flat list; each
-// CTA takes an equally long slice of it whatever the mix of lengths, and two
-// CTAs of four warps sit on an SM. A warp owns 16 keys of every tile and
+// Mapping: the (token, 64-key tile) pairs form one flat list, cut into equally
+// long slices whatever the mix of lengths; a slice is run by one CTA per KV
+// head (and pass), next to each other, so that the heads' rows of a slot, which
+// lie side by side in memory, are fetched at about the same time. Two CTAs of
+// four warps sit on an SM. A warp owns 16 keys of every tile and
 // streams them through its own ring of cp.async stages (zero-filled where a
 // key is absent, so garbage or NaN bits in unwritten slots never reach an
 // MMA); no block barrier sits in the stream. The stream runs on across items:
@@ -129,14 +131,21 @@ enum : int { kFirst = 1, kLast = 2, kStartsItem = 4, kEndsItem = 8 };
 // Keys a decode token sees, or 0 (a padding token, or flagged metadata), and
 // its request's block-table row.
 __device__ __forceinline__ int token_keys(const RowsArgs& a, int t, int* req, bool flag) {
+  // token t mostly belongs to request t: that one's metadata is read beside its id, not after it
   const int r = __ldg(a.req_id + t);
+  const bool guess = t < a.num_reqs;
+  int q0 = guess ? __ldg(a.qsl + t) : 0, q1 = guess ? __ldg(a.qsl + t + 1) : 0, sl = guess ? __ldg(a.seq_lens + t) : 0;
   *req = 0;
   if (r < 0 || r >= a.num_reqs) {
     if (flag) flag_error(a.err, DSA_DEVERR_SEQ_RANGE);
     return 0;
   }
   *req = r;
-  const int q0 = __ldg(a.qsl + r), q1 = __ldg(a.qsl + r + 1), sl = __ldg(a.seq_lens + r);
+  if (r != t) {
+    q0 = __ldg(a.qsl + r);
+    q1 = __ldg(a.qsl + r + 1);
+    sl = __ldg(a.seq_lens + r);
+  }
   if (t < q0 || t >= q1 || sl < 0 || sl > a.max_keys) {
     if (flag) flag_error(a.err, DSA_DEVERR_SEQ_RANGE);
     return 0;
@@ -148,7 +157,7 @@ __device__ __forceinline__ int tiles_of(int n) { return n > 0 ? (n + kTile - 1) 
 
 // The tiles of a CTA's slice, in order.
 struct Cursor {
-  int t, h, kt;  // token, KV head, tile of the item
+  int t, kt;     // token, tile of the token
   int tiles, n;  // of this token
   int req;
   int left;      // tiles of the slice not yet taken
@@ -167,58 +176,67 @@ __device__ __forceinline__ void enter_token(const RowsArgs& a, Cursor& c) {
   }
 }
 
-// Split mode: this CTA's slice of the flat tile list {first token, KV head,
-// tile, tiles, CTAs in use}. All threads call; slice[] is shared memory.
+// What find_slice() finds, in shared memory.
+struct Slice {
+  int64_t all, end;  // tiles in all, end of this slice
+  int t, kt;         // its first token and that token's tile
+  int left;          // its tiles
+  int in_use;        // slices in use
+  int n, req;        // of the first token
+};
+
+// Split mode: slice `part` of the flat tile list. All threads call.
 template <bool SEL>
-__device__ void find_slice(const RowsArgs& a, int cta, int* slice, int* scan) {
+__device__ void find_slice(const RowsArgs& a, int part, bool flag, Slice* s, int* scan) {
   const int T = a.n_tokens, tid = threadIdx.x;
+  int tot, n0 = 0, req0 = 0, first0 = 0;  // of token tid, when all tokens fit in one round
   int64_t total = 0;
   if (SEL) {
-    total = static_cast<int64_t>(T) * a.hkv * tiles_of(a.topk);
+    total = static_cast<int64_t>(T) * tiles_of(a.topk);
   } else {
-    int tot;
     for (int c0 = 0; c0 < T; c0 += kThreads) {
       const int t = c0 + tid;
-      int req;
-      const int tiles = t < T ? tiles_of(token_keys(a, t, &req, cta == 0)) : 0;
-      block_scan_incl(tiles, scan, &tot);
-      total += static_cast<int64_t>(tot) * a.hkv;
+      if (t < T) n0 = token_keys(a, t, &req0, flag);
+      const int tiles = t < T ? tiles_of(n0) : 0;
+      first0 = block_scan_incl(tiles, scan, &tot) - tiles;
+      total += tot;
     }
   }
   const int64_t most = (total + a.min_tiles - 1) / a.min_tiles;
-  const int n = static_cast<int>(most < a.ctas ? most : a.ctas);
-  const int64_t b0 = cta < n ? total * cta / n : total, b1 = cta < n ? total * (cta + 1) / n : total;
+  const int n = static_cast<int>(most < a.slices ? most : a.slices);
+  const int64_t b0 = part < n ? total * part / n : total, b1 = part < n ? total * (part + 1) / n : total;
   if (tid == 0) {
-    slice[3] = static_cast<int>(b1 - b0);
-    slice[4] = n;
-    slice[5] = cta < n;
-    *reinterpret_cast<int64_t*>(slice + 6) = total;
-    *reinterpret_cast<int64_t*>(slice + 8) = b0;
+    s->all = total;
+    s->end = b1;
+    s->left = static_cast<int>(b1 - b0);
+    s->in_use = n;
   }
   if (b0 < b1) {
     if (SEL) {
       if (tid == 0) {
         const int per = tiles_of(a.topk);
-        const int64_t item = b0 / per;
-        slice[0] = static_cast<int>(item / a.hkv);
-        slice[1] = static_cast<int>(item % a.hkv);
-        slice[2] = static_cast<int>(b0 % per);
+        s->t = static_cast<int>(b0 / per);
+        s->kt = static_cast<int>(b0 % per);
+        s->n = a.topk;
+        s->req = 0;
       }
     } else {
       int64_t carry = 0;
-      int tot;
       for (int c0 = 0; c0 < T && carry <= b0; c0 += kThreads) {
         const int t = c0 + tid;
-        int req;
-        const int tiles = t < T ? tiles_of(token_keys(a, t, &req, false)) : 0;
-        const int incl = block_scan_incl(tiles, scan, &tot);
-        const int64_t s = carry + static_cast<int64_t>(incl - tiles) * a.hkv;
-        if (tiles > 0 && s <= b0 && b0 < s + static_cast<int64_t>(tiles) * a.hkv) {
-          slice[0] = t;
-          slice[1] = static_cast<int>((b0 - s) / tiles);
-          slice[2] = static_cast<int>((b0 - s) % tiles);
+        if (T > kThreads) {
+          if (t < T) n0 = token_keys(a, t, &req0, false);
+          const int tiles = t < T ? tiles_of(n0) : 0;
+          first0 = block_scan_incl(tiles, scan, &tot) - tiles;
         }
-        carry += static_cast<int64_t>(tot) * a.hkv;
+        const int64_t at = carry + first0;
+        if (t < T && at <= b0 && b0 < at + tiles_of(n0)) {
+          s->t = t;
+          s->kt = static_cast<int>(b0 - at);
+          s->n = n0;
+          s->req = req0;
+        }
+        carry += T > kThreads ? tot : total;
       }
     }
   }
@@ -241,41 +259,46 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   float* obuf = reinterpret_cast<float*>(smem + C::kOffO);
   uint8_t* qbuf = smem + C::kOffQ;
-  int* slice = reinterpret_cast<int*>(smem + C::kOffScan);
+  Slice* slice = reinterpret_cast<Slice*>(smem + C::kOffScan);
 
-  const int cta = blockIdx.x / a.passes, pass = blockIdx.x - cta * a.passes;
+  const int col = blockIdx.x / a.passes, pass = blockIdx.x - col * a.passes;
+  const int part = col / a.hkv, h = col - part * a.hkv;    // slice (split) or token, KV head
   const int head0 = pass * C::kRows;                       // first query head of the group in this pass
   const int rows = min(C::kRows, a.group - head0);         // its query heads
 
+  // Launched while the stream's previous kernel drains: nothing is read before
+  // it has ended. The join's CTAs in turn may take the places of CTAs that have
+  // ended, and wait there.
+  pdl_wait();
+  if (a.split) pdl_launch_dependents();
   // ---- this CTA's slice
   Cursor cur;
   cur.fresh = true;
-  int in_use = 1;
   if (a.split) {
-    find_slice<SEL>(a, cta, slice, slice + 12);
-    if (!slice[5]) {  // fewer tiles than CTAs
-      if (threadIdx.x == 0 && a.desc != nullptr) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    find_slice<SEL>(a, part, blockIdx.x == 0, slice, reinterpret_cast<int*>(slice + 1));
+    cur.left = slice->left;
+    if (cur.left == 0) {  // fewer tiles than slices
+      if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int2(-1, 0);
       return;
     }
-    cur.t = slice[0];
-    cur.h = slice[1];
-    cur.kt = slice[2];
-    cur.left = slice[3];
-    in_use = slice[4];
-    enter_token<SEL>(a, cur);
+    cur.t = slice->t;
+    cur.kt = slice->kt;
+    cur.n = slice->n;
+    cur.req = slice->req;
+    cur.tiles = tiles_of(cur.n);
   } else {
-    cur.t = cta / a.hkv;
-    cur.h = cta - cur.t * a.hkv;
+    cur.t = part;
     cur.kt = 0;
-    if (!SEL && threadIdx.x == 0 && cur.h == 0 && pass == 0) {
-      int req;
-      token_keys(a, cur.t, &req, true);
+    if (SEL) {
+      cur.n = a.topk;
+      cur.req = 0;
+    } else {
+      cur.n = token_keys(a, cur.t, &cur.req, threadIdx.x == 0 && h == 0 && pass == 0);
     }
-    enter_token<SEL>(a, cur);
+    cur.tiles = tiles_of(cur.n);
     cur.left = cur.tiles;
   }
-  const int64_t slice_end_tile = a.split ? *reinterpret_cast<int64_t*>(slice + 8) + slice[3] : 0;
-  int desc_item = -1, desc_last = 0;  // this CTA begins an item that later CTAs continue
+  int desc_token = -1, desc_last = 0;  // the slice ends inside a token that it began: which, and its last slice
 
   // ---- the loader: one tile of this warp's 16 keys into a stage
   const T* kbase = static_cast<const T*>(a.k);
@@ -304,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
         // lanes 0-15 hold the K rows' offsets, lanes 16-31 the V rows'
         const bool isv = lane >= 16;
         const int64_t page = in ? nid / kBlock : 0, slot = in ? nid % kBlock : 0;
-        const int64_t off = isv ? page * a.v_page + slot * a.v_slot + cur.h * a.v_head
-                                : page * a.k_page + slot * a.k_slot + cur.h * a.k_head;
+        const int64_t off = isv ? page * a.v_page + slot * a.v_slot + h * a.v_head
+                                : page * a.k_page + slot * a.k_slot + h * a.k_head;
         if (mask != 0) {
 #pragma unroll
           for (int i = 0; i < kWarpKeys / RPI; ++i) {
@@ -328,9 +351,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
         if (have > 0) {
           mask = (1u << have) - 1u;
           const T* kp = kbase + nid * a.k_page + static_cast<int64_t>(warp * kWarpKeys + r0) * a.k_slot +
-                        cur.h * a.k_head + c * 8;
+                        h * a.k_head + c * 8;
           const T* vp = vbase + nid * a.v_page + static_cast<int64_t>(warp * kWarpKeys + r0) * a.v_slot +
-                        cur.h * a.v_head + c * 8;
+                        h * a.v_head + c * 8;
 #pragma unroll
           for (int i = 0; i < kWarpKeys / RPI; ++i) {
             const int r = i * RPI + r0;
@@ -345,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
       if (lane == 0) {
         const int flags = (cur.fresh ? kFirst : 0) | (last ? kLast : 0) | (cur.kt == 0 ? kStartsItem : 0) |
                           (ends ? kEndsItem : 0);
-        meta[stage] = make_int4(static_cast<int>(mask) | (flags << 16), cur.t, cur.h, cur.tiles - 1 - cur.kt);
+        meta[stage] = make_int4(static_cast<int>(mask) | (flags << 16), cur.t, cur.tiles - 1 - cur.kt, 0);
       }
       // advance
       cur.fresh = last;
@@ -354,11 +377,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
         ++cur.kt;
       } else {
         cur.kt = 0;
-        if (++cur.h == a.hkv) {
-          cur.h = 0;
-          ++cur.t;
-          if (cur.left > 0) enter_token<SEL>(a, cur);
-        }
+        ++cur.t;
+        if (cur.left > 0) enter_token<SEL>(a, cur);
       }
       fetch_id();
     }
@@ -396,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
 #pragma unroll
         for (int y = 0; y < D / 8; ++y) o[x][y][0] = o[x][y][1] = o[x][y][2] = o[x][y][3] = 0.0f;
       }
-      const T* q = static_cast<const T*>(a.q) + mt.y * a.q_row + static_cast<int64_t>(mt.z * a.group + head0) * a.q_head;
+      const T* q = static_cast<const T*>(a.q) + mt.y * a.q_row + static_cast<int64_t>(h * a.group + head0) * a.q_head;
       if constexpr (MT == 1) {
         const int g = lane >> 2, c2 = (lane & 3) * 2;
         const bool v0 = g < rows, v1 = g + 8 < rows;
@@ -618,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
             if (r >= rows) continue;
             const float L = l[x][e], M = m[x][e];
             if (whole) {
-              const int64_t head = static_cast<int64_t>(mt.z) * a.group + head0 + r;
+              const int64_t head = static_cast<int64_t>(h) * a.group + head0 + r;
               T* out = static_cast<T*>(a.out) + mt.y * a.out_row + head * a.out_head;
               const float inv = M == NEG ? 0.0f : 1.0f / L;
 #pragma unroll
@@ -635,76 +655,90 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
             }
           }
       }
-      if (!whole && starts) {  // it began here and goes on: mt.w tiles after this one, in the next CTAs
-        desc_item = mt.y * a.hkv + mt.z;
-        const int64_t all = *reinterpret_cast<int64_t*>(slice + 6), end = slice_end_tile + mt.w;
-        desc_last = static_cast<int>((end * in_use + all - 1) / all) - 1;
+      if (!whole && starts) {  // it began here and goes on: mt.z tiles after this one, in the next slices
+        desc_token = mt.y;
+        const int64_t end = slice->end + mt.z;
+        desc_last = static_cast<int>((end * slice->in_use + slice->all - 1) / slice->all) - 1;
       }
     }
   }
   cp_wait<0>();
-  if (a.split && threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(desc_item, desc_last, 0, 0);
-  pdl_launch_dependents();
+  if (a.split && threadIdx.x == 0) a.desc[blockIdx.x] = make_int2(desc_token, desc_last);
 }
 
-// The items cut by slice boundaries: CTA (b, row) adds the partials of row
-// `row` of the item that main CTA b began, in CTA order per warp and then
-// over the warps.
+// The tokens cut by slice boundaries: for the token and head that main CTA b
+// began, CTA (b, y) adds the partials of rows y * 8 / WAYS and following. WAYS
+// warps share a row, taking its slices in turn, each in order; their sums are
+// added in warp order. Many slices per token want all eight warps on a row (1
+// token of 131072 keys: 38 partials a row), few want a warp per row.
 constexpr int kJoinWarps = 8;
 
-template <int D, typename T>
+template <int D, typename T, int WAYS>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ RowsArgs a, int krows) {
   constexpr int V = D / 32;
-  __shared__ float so[kJoinWarps][D];
+  constexpr int kRowsCta = kJoinWarps / WAYS;
+  __shared__ float so[WAYS > 1 ? kJoinWarps : 1][D];
   __shared__ float2 sml[kJoinWarps];
-  pdl_wait();
-  const int cta = blockIdx.x / a.passes, pass = blockIdx.x - cta * a.passes;
-  const int r = blockIdx.y, head0 = pass * krows;
-  const int4 d = a.desc[blockIdx.x];
-  if (d.x < 0 || head0 + r >= a.group) return;
+  const int col = blockIdx.x / a.passes, pass = blockIdx.x - col * a.passes;
+  const int part = col / a.hkv, h = col - part * a.hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kRowsCta + warp / WAYS, head0 = pass * krows;
+  const bool in = head0 + r < a.group && r < krows;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int2 d = a.desc[blockIdx.x];
+  if (d.x < 0) return;
   float M = -INFINITY, L = 0.0f, o[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.0f;
+  if (in) {
 #pragma unroll 4
-  for (int c = cta + warp; c <= d.y; c += kJoinWarps) {
-    const int64_t slot = 2 * (static_cast<int64_t>(c) * a.passes + pass) + (c == cta ? 1 : 0);
-    const float2 v = a.part_ml[slot * krows + r];
-    const float* p = a.part_o + (slot * krows + r) * D + lane * V;
-    float w[V];
+    for (int c = part + warp % WAYS; c <= d.y; c += WAYS) {
+      const int64_t slot = 2 * ((static_cast<int64_t>(c) * a.hkv + h) * a.passes + pass) + (c == part ? 1 : 0);
+      const float2 v = a.part_ml[slot * krows + r];
+      const float* p = a.part_o + (slot * krows + r) * D + lane * V;
+      float w[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) w[i] = p[i];
-    if (v.x == -INFINITY) continue;
-    const float n = fmaxf(M, v.x);
-    const float f = ex2(M - n), e = ex2(v.x - n);  // M = -inf: 0
-    M = n;
-    L = L * f + v.y * e;
+      for (int i = 0; i < V; ++i) w[i] = p[i];
+      if (v.x == -INFINITY) continue;
+      const float n = fmaxf(M, v.x);
+      const float f = ex2(M - n), e = ex2(v.x - n);  // M = -inf: 0
+      M = n;
+      L = L * f + v.y * e;
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = o[i] * f + w[i] * e;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) so[warp][lane * V + i] = o[i];
-  if (lane == 0) sml[warp] = make_float2(M, L);
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  float m = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sml[w].x);
-  float l = 0.0f, acc = 0.0f;
-  if (m != -INFINITY) {
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      const float f = ex2(sml[w].x - m);
-      l += sml[w].y * f;
-      acc += so[w][threadIdx.x] * f;
+      for (int i = 0; i < V; ++i) o[i] = o[i] * f + w[i] * e;
     }
-    acc /= l;
   }
-  const int t = d.x / a.hkv, h = d.x - t * a.hkv;
+  if constexpr (WAYS > 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) so[warp][lane * V + i] = o[i];
+    if (lane == 0) sml[warp] = make_float2(M, L);
+    __syncthreads();
+    if (warp % WAYS != 0) return;
+    M = -INFINITY;
+    L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAYS; ++w) M = fmaxf(M, sml[warp + w].x);
+    if (M != -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WAYS; ++w) {
+        const float f = ex2(sml[warp + w].x - M);
+        L += sml[warp + w].y * f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] += so[warp + w][lane * V + i] * f;
+      }
+    }
+  }
+  if (!in) return;
   const int64_t head = static_cast<int64_t>(h) * a.group + head0 + r;
-  static_cast<T*>(a.out)[t * a.out_row + head * a.out_head + threadIdx.x] = static_cast<T>(acc);
-  if (a.lse != nullptr && threadIdx.x == 0)
-    a.lse[static_cast<int64_t>(t) * a.heads + head] = m == -INFINITY ? m : (m + log2f(l)) * 0.6931471805599453f;
+  const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + d.x * a.out_row + head * a.out_head + lane * V);
+#pragma unroll
+  for (int i = 0; i < V; i += 2) out[i / 2] = Elem<T>::pack(o[i] * inv, o[i + 1] * inv);
+  if (a.lse != nullptr && lane == 0)
+    a.lse[static_cast<int64_t>(d.x) * a.heads + head] = M == -INFINITY ? M : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 template <int D, typename T, int MT, bool SEL>
@@ -714,10 +748,12 @@ cudaError_t launch(const RowsArgs& a, int grid, cudaStream_t stream) {
   auto* fn = attn_rows_kernel<D, T, MT, SEL>;
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(fn), C::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
-  fn<<<grid, kThreads, C::kSmemBytes, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || !a.split) return e;
+  if ((e = launch_pdl(fn, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, a)) != cudaSuccess || !a.split) return e;
   const int rows = a.group < C::kRows ? a.group : C::kRows;
-  return launch_pdl(attn_join_kernel<D, T>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, stream, a, C::kRows);
+  if (a.slices > 4 * static_cast<int64_t>(a.n_tokens))
+    return launch_pdl(attn_join_kernel<D, T, 8>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, stream, a, C::kRows);
+  return launch_pdl(attn_join_kernel<D, T, 1>, dim3(grid, (rows + 7) / 8), dim3(32 * kJoinWarps), 0, stream, a,
+                    C::kRows);
 }
 
 template <int D, typename T>
@@ -730,7 +766,7 @@ cudaError_t launch_dt(const RowsArgs& a, int grid, bool sel, cudaStream_t stream
 }  // namespace
 
 cudaError_t launch_attn_rows(const RowsArgs& a, int head_dim, int dtype, bool selected, cudaStream_t stream) {
-  const int grid = a.ctas * a.passes;
+  const int grid = a.slices * a.hkv * a.passes;
   if (dtype == DSA_BF16)
     return head_dim == 128 ? launch_dt<128, __nv_bfloat16>(a, grid, selected, stream)
                            : launch_dt<64, __nv_bfloat16>(a, grid, selected, stream);
