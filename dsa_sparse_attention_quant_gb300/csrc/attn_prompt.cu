@@ -63,10 +63,11 @@ struct PromptCfg {
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kOffKv = 2 * kTileBytes;
   static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
-  static constexpr int kNumBars = 2 * kStages + 2 + 2 + 2 + 2 + 1;
+  static constexpr int kNumBars = 2 * kStages + 5 * 2 + 2 * 2 + 1 + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffCta = kOffMisc + 16;
-  static constexpr int kSmemBytes = kOffCta + 96 + 1024;  // + slack to align the base to 1024
+  static constexpr int kOffNext = (kOffMisc + 16 + 15) / 16 * 16;  // the 16 bytes of a taken-over CTA's index
+  static constexpr int kOffCta = kOffNext + 16;
+  static constexpr int kSmemBytes = kOffCta + 2 * 96 + 1024;  // + slack to align the base to 1024
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kO = 256;                   // first column of O
   // P lies over its S (D = 128: TMEM is full), or beside it: then the next
@@ -291,12 +292,40 @@ __device__ __forceinline__ float weights(uint32_t ts, int lim, uint64_t sc2, uin
   return l.x + l.y;
 }
 
-// What a CTA works on.
+// What a CTA works on: one unit of the grid, its own or a taken-over one.
 struct PromptCta {
   PromptTile tile;
   // the two query tiles: head, first row of q, rows, position of the first, key tiles
   int head[2], t0[2], rows[2], pos0[2], nt[2];
+  // key tiles in which a non-finite V element was cleared: lowest and highest
+  int bad_lo, bad_hi;
+  int stop;  // no unit: the end
 };
+static_assert(sizeof(PromptCta) <= 96, "room for two");
+
+// Ask for the index of a CTA that has not started yet, which then will not
+// start: *next and bar get the answer (16 bytes).
+__device__ __forceinline__ void ask_next(void* next, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(next)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The answer: that CTA's index, or -1 when none was left.
+__device__ __forceinline__ int read_next(const void* next) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "mov.s32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+      : "=r"(x)
+      : "r"(smem_u32(next))
+      : "memory");
+  return x;
+}
 
 // V's elements (col, col + 1) of key k as far as they are not finite, else 0.
 template <typename T>
@@ -327,50 +356,38 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* empty = full + S;
   uint64_t* qfull = empty + S;
-  uint64_t* sfull = qfull + 2;
+  uint64_t* qempty = qfull + 2;
+  uint64_t* sfull = qempty + 2;
   uint64_t* pfull = sfull + 2;
   uint64_t* ofull = pfull + 2;
-  uint64_t* done = ofull + 2;
+  uint64_t* ufull = ofull + 2;   // a unit's PromptCta is written
+  uint64_t* uempty = ufull + 2;  // and read by all
+  uint64_t* asked = uempty + 2;
+  uint64_t* done = asked + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  // first tiles in which a non-finite V element was cleared: per softmax group, lowest and highest tile
-  int* bad_lo = reinterpret_cast<int*>(smem + C::kOffMisc + 8);
-  int* bad_hi = bad_lo + 1;
+  uint8_t* next = smem + C::kOffNext;
+  PromptCta* ctas = reinterpret_cast<PromptCta*>(smem + C::kOffCta);  // two, taking turns
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hu = blockIdx.x % a.head_units, rank = blockIdx.x / a.head_units;
-  PromptCta& cta = *reinterpret_cast<PromptCta*>(smem + C::kOffCta);
-  if (warp == 0) {
-    const PromptTile tile = find_tile(a, rank, hu == 0);
-    if (lane == 0) {
-      cta.tile = tile;
-      for (int x = 0; x < 2; ++x) {
-        const int shift = a.pair_heads ? 0 : x * kRowsTile;
-        const int rows = min(kRowsTile, max(0, tile.ntok - shift));
-        cta.head[x] = a.pair_heads ? 2 * hu + x : hu;
-        cta.t0[x] = tile.t0 + shift;
-        cta.rows[x] = rows;
-        cta.pos0[x] = tile.pos0 + shift;
-        cta.nt[x] =
-            rows > 0 ? (visible(tile.pos0 + shift + rows - 1, tile.keys) + kKeys - 1) / kKeys : 0;
-      }
-      const int users = (cta.nt[0] > 0) + (cta.nt[1] > 0);
-      for (int s = 0; s < S; ++s) {
-        mbar_init(&full[s], 1);
-        mbar_init(&empty[s], users > 0 ? users : 1);
-      }
-      for (int x = 0; x < 2; ++x) {
-        mbar_init(&qfull[x], 1);
-        mbar_init(&sfull[x], 1);
-        mbar_init(&pfull[x], kSoftWarps / 2);
-        mbar_init(&ofull[x], 1);
-      }
-      mbar_init(done, 1);
-      *abort_flag = 0;
-      *bad_lo = 0x7FFFFFFF;
-      *bad_hi = -1;
-      fence_barrier_init();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 2);  // both tiles' softmax warps, whether they use the stage or not
     }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&qfull[x], 1);
+      mbar_init(&qempty[x], 1);
+      mbar_init(&sfull[x], 1);
+      mbar_init(&pfull[x], kSoftWarps / 2);
+      mbar_init(&ofull[x], 1);
+      mbar_init(&ufull[x], 1);
+      mbar_init(&uempty[x], kSoftWarps + 1);
+    }
+    mbar_init(asked, 1);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
   }
   if (warp == kTmaWarp && lane == 0) {
     prefetch_tmap(&tmap_q);
@@ -382,84 +399,159 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (!cta.tile.found) {  // the grid is an upper bound
-    if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
-    return;
-  }
-  // Kept in shared memory and read where they are used, to spare registers.
-  const volatile PromptCta& w = cta;
-  const int nt[2] = {w.nt[0], w.nt[1]};
-  const int n_tiles = max(nt[0], nt[1]);
+
+  // The next unit for a warp that follows the TMA warp, or false at the end.
+  int units = 0;
+  auto next_unit = [&](const volatile PromptCta** w) {
+    const int u = units & 1;
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(&ufull[u], (units >> 1) & 1, abort_flag, a.err)) != 0;
+    *w = &ctas[u];
+    ++units;
+    return ok && !(*w)->stop;
+  };
+  auto unit_read = [&]() {  // of the unit that next_unit gave last
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&uempty[(units - 1) & 1]);
+  };
 
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == kTmaWarp) {
-      // ----------------------------------------------------------------- TMA
-      int issued = 0;  // ring stages filled
-      bool ok = true;
-      if (lane == 0 && n_tiles > 0) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (nt[x] == 0) continue;
-          mbar_arrive_expect_tx(&qfull[x], C::kTileBytes);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(smem + x * C::kTileBytes + c * C::kColBytes, &tmap_q, &qfull[x], c * 64, w.head[x], w.t0[x]);
+      // --------------------------------------------------------------- TMA
+      int seq = 0;       // ring stages filled so far
+      int nq[2] = {0, 0};  // units that loaded query tile x
+      int item = blockIdx.x;
+      int asks = 0;  // answers read
+      bool ok = true, ended = false, pending = false;
+      while (ok) {
+        const int u = units & 1;
+        if (units >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&uempty[u], ((units >> 1) - 1) & 1, abort_flag, a.err)) != 0;
+        if (!ok) break;
+        PromptCta& c = ctas[u];
+        const int hu = item < 0 ? 0 : item % a.head_units;
+        PromptTile tile{};
+        // the grid is an upper bound: behind the first unit that is not there, none is
+        if (item >= 0 && !ended) tile = find_tile(a, item / a.head_units, hu == 0);
+        ended = ended || !tile.found;
+        if (item >= 0 && ended) {  // pass over it, and the ones behind it
+          if (lane == 0) {
+            mbar_arrive_expect_tx(asked, 16);
+            ask_next(next, asked);
+          }
+          pending = true;
         }
-      }
-      const int keys = w.tile.keys, req = w.tile.req, kv0 = w.tile.kv0, h = w.head[0] / a.group;
-      const int n_pages = (keys + kBlock - 1) / kBlock;
-      int32_t ids = 0;
-      for (int j = 0; j < n_tiles && ok; ++j) {
-        int c2[2], c3[2], boxes;
-        if (a.kv_start == nullptr) {
-          if ((j & 15) == 0) {  // the next 32 pages
-            const int pg = 2 * j + lane;
-            ids = pg < n_pages ? __ldg(a.block_table + static_cast<int64_t>(req) * a.bt_stride + pg) : 0;
-            if (ids < 0 || ids >= a.num_blocks) {
-              flag_error(a.err, DSA_DEVERR_BLOCK_RANGE);
-              ids = 0;
+        int nt[2] = {0, 0};
+        if (!ended && item >= 0) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int shift = a.pair_heads ? 0 : x * kRowsTile;
+            const int rows = min(kRowsTile, max(0, tile.ntok - shift));
+            nt[x] = rows > 0 ? (visible(tile.pos0 + shift + rows - 1, tile.keys) + kKeys - 1) / kKeys : 0;
+            if (lane == 0) {
+              c.head[x] = a.pair_heads ? 2 * hu + x : hu;
+              c.t0[x] = tile.t0 + shift;
+              c.rows[x] = rows;
+              c.pos0[x] = tile.pos0 + shift;
+              c.nt[x] = nt[x];
             }
           }
-          c3[0] = __shfl_sync(0xffffffffu, ids, 2 * (j & 15));
-          c3[1] = __shfl_sync(0xffffffffu, ids, 2 * (j & 15) + 1);
-          c2[0] = c2[1] = 0;
-          boxes = 2 * j + 1 < n_pages ? 2 : 1;
-        } else {
-          c2[0] = kv0 + j * kKeys;
-          c2[1] = c2[0] + kBlock;
-          c3[0] = c3[1] = 0;
-          // a box may begin behind the last packed row only if it is not loaded at all
-          boxes = j * kKeys + kBlock < keys ? 2 : 1;
         }
-        if (lane == 0) {
-#pragma unroll
-          for (int kvi = 0; kvi < 2; ++kvi) {
-            const int st = issued % S, round = issued / S;
-            if (round > 0 && !mbar_wait(&empty[st], (round - 1) & 1, abort_flag, a.err)) {
-              ok = false;
-              break;
+        if (!(item >= 0 && ended)) {
+          if (lane == 0) {
+            c.tile = tile;
+            c.bad_lo = 0x7FFFFFFF;
+            c.bad_hi = -1;
+            c.stop = item < 0;
+            mbar_arrive(&ufull[u]);
+            if (item >= 0) {
+              mbar_arrive_expect_tx(asked, 16);
+              ask_next(next, asked);
             }
-            uint8_t* dst = kv + st * C::kTileBytes;
-            mbar_arrive_expect_tx(&full[st], boxes * C::kBoxBytes * (D / 64));
-            for (int b = 0; b < boxes; ++b)
+          }
+          pending = item >= 0;
+          ++units;
+          if (item < 0) break;
+          const int n_tiles = max(nt[0], nt[1]);
+          const int h = (a.pair_heads ? 2 * hu : hu) / a.group;
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_load_4d(dst + c * C::kColBytes + b * C::kBoxBytes, kvi == 0 ? &tmap_k : &tmap_v, &full[st], c * 64, h,
-                            c2[b], c3[b]);
-            ++issued;
+          for (int x = 0; x < 2; ++x) {
+            if (nt[x] == 0 || !ok) continue;
+            if (nq[x] > 0) ok = __all_sync(0xffffffffu, mbar_wait(&qempty[x], (nq[x] - 1) & 1, abort_flag, a.err)) != 0;
+            ++nq[x];
+            if (ok && lane == 0) {
+              mbar_arrive_expect_tx(&qfull[x], C::kTileBytes);
+#pragma unroll
+              for (int b = 0; b < D / 64; ++b)
+                tma_load_3d(smem + x * C::kTileBytes + b * C::kColBytes, &tmap_q, &qfull[x], b * 64,
+                            a.pair_heads ? 2 * hu + x : hu, tile.t0 + (a.pair_heads ? 0 : x * kRowsTile));
+            }
+          }
+          const int n_pages = (tile.keys + kBlock - 1) / kBlock;
+          int32_t ids = 0;
+          for (int j = 0; j < n_tiles && ok; ++j) {
+            int c2[2], c3[2], boxes;
+            if (a.kv_start == nullptr) {
+              if ((j & 15) == 0) {  // the next 32 pages
+                const int pg = 2 * j + lane;
+                ids = pg < n_pages ? __ldg(a.block_table + static_cast<int64_t>(tile.req) * a.bt_stride + pg) : 0;
+                if (ids < 0 || ids >= a.num_blocks) {
+                  flag_error(a.err, DSA_DEVERR_BLOCK_RANGE);
+                  ids = 0;
+                }
+              }
+              c3[0] = __shfl_sync(0xffffffffu, ids, 2 * (j & 15));
+              c3[1] = __shfl_sync(0xffffffffu, ids, 2 * (j & 15) + 1);
+              c2[0] = c2[1] = 0;
+              boxes = 2 * j + 1 < n_pages ? 2 : 1;
+            } else {
+              c2[0] = tile.kv0 + j * kKeys;
+              c2[1] = c2[0] + kBlock;
+              c3[0] = c3[1] = 0;
+              // a box may begin behind the last packed row only if it is not loaded at all
+              boxes = j * kKeys + kBlock < tile.keys ? 2 : 1;
+            }
+            if (lane == 0) {
+#pragma unroll
+              for (int kvi = 0; kvi < 2; ++kvi) {
+                const int st = seq % S, round = seq / S;
+                if (round > 0 && !mbar_wait(&empty[st], (round - 1) & 1, abort_flag, a.err)) {
+                  ok = false;
+                  break;
+                }
+                uint8_t* dst = kv + st * C::kTileBytes;
+                mbar_arrive_expect_tx(&full[st], boxes * C::kBoxBytes * (D / 64));
+                for (int b = 0; b < boxes; ++b)
+#pragma unroll
+                  for (int k = 0; k < D / 64; ++k)
+                    tma_load_4d(dst + k * C::kColBytes + b * C::kBoxBytes, kvi == 0 ? &tmap_k : &tmap_v, &full[st],
+                                k * 64, h, c2[b], c3[b]);
+                ++seq;
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        // the unit after this one
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(asked, asks & 1, abort_flag, a.err)) != 0;
+        if (ok) {
+          ++asks;
+          pending = false;
+          item = read_next(next);
+          fence_proxy_async();  // read before the next answer is written
+          __syncwarp();
+        }
       }
       if (lane == 0 && *abort_flag) {  // giving up: no copy may land after the CTA's end
         const unsigned long long until = global_ns() + kWaitLimitNs;
-        for (int i = max(0, issued - S); i < issued; ++i)
+        if (pending)
+          while (!mbar_try_wait(smem_u32(asked), asks & 1) && global_ns() < until) {
+          }
+        for (int i = max(0, seq - S); i < seq; ++i)
           while (!mbar_try_wait(smem_u32(&full[i % S]), (i / S) & 1) && global_ns() < until) {
           }
         for (int x = 0; x < 2; ++x)
-          if (nt[x] > 0)
-            while (!mbar_try_wait(smem_u32(&qfull[x]), 0) && global_ns() < until) {
+          if (nq[x] > 0)
+            while (!mbar_try_wait(smem_u32(&qfull[x]), (nq[x] - 1) & 1) && global_ns() < until) {
             }
       }
     } else if (warp == kMmaWarp) {
@@ -469,7 +561,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // One warp for both tiles keeps them out of step, one's softmax under the
       // other's MMAs: with a warp per tile they fell into step (1350 -> 1230
       // TFLOP/s at 4 x 8192, 64/8 heads of 128).
-      if (n_tiles > 0) {
+      {
         constexpr uint32_t kIdS = f16_idesc(E::kFmt, kKeys, false), kIdO = f16_idesc(E::kFmt, D, true);
         const uint32_t qd = kmajor_lo(smem_u32(smem)), kv0 = smem_u32(kv);
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -487,48 +579,68 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           __syncwarp();
         };
-        bool ok = wait(&full[0], 0);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (nt[x] == 0 || !ok) continue;
-          ok = wait(&qfull[x], 0);
-          if (ok) scores(x, 0);
-        }
-        int vst = 1 % S, kst = 2 % S;
-        uint32_t vpar = 0, kpar = 0;
-        ok = ok && wait(&full[vst], vpar);
-        for (int j = 0; j < n_tiles && ok; ++j) {
-          const uint32_t vd = mnmajor_lo(kv0 + vst * C::kTileBytes);
-          bool have_k = false;
+        auto release = [&](uint64_t* bar) {
+          if (elect_one()) mma_commit(bar);
+          __syncwarp();
+        };
+        bool ok = true;
+        int seq = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // ring stages, units and tiles so far
+        const volatile PromptCta* w;
+        while (ok && next_unit(&w)) {
+          const int nt[2] = {w->nt[0], w->nt[1]};
+          unit_read();
+          const int n_tiles = max(nt[0], nt[1]);
+          if (n_tiles == 0) continue;
+          ok = wait(&full[seq % S], (seq / S) & 1);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (j >= nt[x]) continue;
-            ok = ok && wait(&pfull[x], j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            auto next_scores = [&]() {
-              if (j + 1 >= nt[x]) return;
-              if (!have_k) ok = wait(&full[kst], kpar);
-              have_k = true;
-              if (ok) scores(x, kst);
-            };
-            if constexpr (C::kOwnP) next_scores();
-            if (!ok) break;
-            if (elect_one()) {
+            if (nt[x] == 0 || !ok) continue;
+            ok = wait(&qfull[x], nq[x]++ & 1);
+            if (ok) scores(x, seq % S);
+            if (nt[x] == 1) release(&qempty[x]);
+          }
+          int vst = (seq + 1) % S, kst = (seq + 2) % S;
+          uint32_t vpar = ((seq + 1) / S) & 1, kpar = ((seq + 2) / S) & 1;
+          ok = ok && wait(&full[vst], vpar);
+          for (int j = 0; j < n_tiles && ok; ++j) {
+            const uint32_t vd = mnmajor_lo(kv0 + vst * C::kTileBytes);
+            bool have_k = false;
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                mma_f16_ts(tmem + C::kO + x * D, tmem + C::kP + x * C::kPStep + k * 8, vd + ((k * 16 * 128) >> 4),
-                           kIdO, j > 0 || k > 0);
-              if (C::kOwnP || j == nt[x] - 1) mma_commit(&ofull[x]);
+            for (int x = 0; x < 2; ++x) {
+              if (j >= nt[x]) continue;
+              if (C::kOwnP && !have_k && j + 1 < nt[x]) {  // mostly there already: not left until P is
+                ok = ok && wait(&full[kst], kpar);
+                have_k = true;
+              }
+              ok = ok && wait(&pfull[x], np[x]++ & 1);
+              if (!ok) break;
+              tc_fence_after();
+              auto next_scores = [&]() {
+                if (j + 1 >= nt[x]) return;
+                if (!have_k) ok = wait(&full[kst], kpar);
+                have_k = true;
+                if (ok) scores(x, kst);
+                if (j + 2 == nt[x]) release(&qempty[x]);  // the unit's last use of this query tile
+              };
+              if constexpr (C::kOwnP) next_scores();
+              if (!ok) break;
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                  mma_f16_ts(tmem + C::kO + x * D, tmem + C::kP + x * C::kPStep + k * 8, vd + ((k * 16 * 128) >> 4),
+                             kIdO, j > 0 || k > 0);
+                if (C::kOwnP || j == nt[x] - 1) mma_commit(&ofull[x]);
+              }
+              __syncwarp();
+              if constexpr (!C::kOwnP) next_scores();
             }
-            __syncwarp();
-            if constexpr (!C::kOwnP) next_scores();
+            for (int i = 0; i < 2; ++i) {
+              if (++vst == S) vst = 0, vpar ^= 1;
+              if (++kst == S) kst = 0, kpar ^= 1;
+            }
+            if (ok && j + 1 < n_tiles) ok = wait(&full[vst], vpar);
           }
-          for (int i = 0; i < 2; ++i) {
-            if (++vst == S) vst = 0, vpar ^= 1;
-            if (++kst == S) kst = 0, kpar ^= 1;
-          }
-          if (ok && j + 1 < n_tiles) ok = wait(&full[vst], vpar);
+          seq += 2 * n_tiles;
         }
         if (*abort_flag) {  // giving up: let the MMAs in flight end before TMEM is freed
           if (elect_one()) mma_commit(done);
@@ -547,185 +659,198 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + C::kO + x * D;
-    const int my_nt = x == 0 ? nt[0] : nt[1];
-    const int vis = visible(w.pos0[x] + min(r, w.rows[x] - 1), w.tile.keys);
     const float NEG = -INFINITY;
-    float M = NEG, L = 0.0f;
-    bool ok = true;
-    bool fresh = true;  // some row of the warp may have no reference yet
-    // uniform bounds of what only some tiles need: the first tile that a row of
-    // the warp, and of the tile, does not see whole
-    const int edge_from = __reduce_min_sync(0xffffffffu, vis) / kKeys;
-    const int fix_from = x == 0 ? visible(w.pos0[0], w.tile.keys) / kKeys : max(visible(w.pos0[1], w.tile.keys) / kKeys, nt[0]);
     const bool leader = (warp & 3) == 0 && lane == 0;
-    int kst = 0, vst = 1 % S;  // ring stages of tile j
-    uint32_t vpar = 0;
-    for (int j = 0; j < my_nt; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&sfull[x], j & 1, abort_flag, a.err)) != 0;
-      if (!ok) break;
-      tc_fence_after();
-      if (leader) {  // the scores are complete, and with P in S's columns everything this tile's MMAs read before
-        mbar_arrive(&empty[kst]);
-        if (!C::kOwnP && j > 0) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
-      }
-      const int lim = vis - j * kKeys;  // visible columns
-      // The weights by the reference at hand, without looking for the maximum
-      // first: only where a row has none yet, or its weights come out too large
-      // (or not a number), the maximum is taken and the weights once more. A
-      // row's decision is its own: no other row has a part in its bits.
-      bool raise = fresh && M == NEG && lim > 0;
-      uint32_t p[2][32];
-      float add;
-      for (int attempt = fresh ? 1 : 0;; ++attempt) {
-        if (attempt > 0) {
-          float top = NEG;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t s[32];
-            tmem_ld32(ts + c * 32, s);
-            tmem_wait32(s);
-            float mx[4] = {NEG, NEG, NEG, NEG};
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c * 32 + i < lim) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
-            top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          }
-          const float n = raise ? fmaxf(M, top * a.scale_log2 - E::kHead) : M;
-          const float f = !raise ? 1.0f : M == NEG ? 0.0f : pex2(M - n);
-          M = n;
-          L *= f;
-          fresh = __any_sync(0xffffffffu, M == NEG);
-          if (j > 0) {  // O is complete up to tile j - 1: without kOwnP its MMAs precede this tile's scores
-            if (C::kOwnP && !__all_sync(0xffffffffu, mbar_wait(&ofull[x], (j - 1) & 1, abort_flag, a.err))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(to + c * 32, o);
-              tmem_wait32(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(to + c * 32, o);
-            }
-          }
-        }
-        const float ref = M == NEG ? 0.0f : M;
-        const uint64_t sc2 = pack_f32x2(a.scale_log2, a.scale_log2), ref2 = pack_f32x2(-ref, -ref);
-        add = j >= edge_from ? weights<T, true>(ts, lim, sc2, ref2, p) : weights<T, false>(ts, lim, sc2, ref2, p);
-        raise = !raise && !(add <= E::kMaxSum);
-        if (attempt == 2 || !__any_sync(0xffffffffu, raise)) break;
-      }
-      if (!ok) break;
-      L += add;
-      if (C::kOwnP && j > 0) {  // the previous tile's P V has read P and V
-        ok = mbar_wait(&ofull[x], (j - 1) & 1, abort_flag, a.err);
-        tc_fence_after();
-        if (leader) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
-        __syncwarp();
-      }
-#pragma unroll
-      for (int half = 0; half < 2; ++half) tmem_st32(tmem + lanes + C::kP + x * C::kPStep + half * 32, p[half]);
-      // V in a tile cut by the causal edge or the sequence's end, before its first use
-      if (j >= fix_from) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[vst], vpar, abort_flag, a.err)) != 0;
+    bool ok = true;
+    int seq = 0;  // ring stages so far
+    int ns = 0, no = 0;  // tiles, and rounds of ofull, so far
+    const volatile PromptCta* wp;
+    while (ok && next_unit(&wp)) {
+      const volatile PromptCta& w = *wp;
+      PromptCta& cta = ctas[(units - 1) & 1];
+      const int my_nt = w.nt[x], other_nt = w.nt[x ^ 1];
+      const int vis = visible(w.pos0[x] + min(r, w.rows[x] - 1), w.tile.keys);
+      float M = NEG, L = 0.0f;
+      bool fresh = true;  // some row of the warp may have no reference yet
+      // uniform bounds of what only some tiles need: the first tile that a row of
+      // the warp, and of the tile, does not see whole
+      const int edge_from = __reduce_min_sync(0xffffffffu, vis) / kKeys;
+      const int fix_from = x == 0 ? visible(w.pos0[0], w.tile.keys) / kKeys
+                                  : max(visible(w.pos0[1], w.tile.keys) / kKeys, other_nt);
+      int kst = seq % S, vst = (seq + 1) % S;  // ring stages of tile j
+      uint32_t vpar = ((seq + 1) / S) & 1;
+      for (int j = 0; j < my_nt; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[x], ns++ & 1, abort_flag, a.err)) != 0;
         if (!ok) break;
-        // thread r: key row r of the tile, which lies at 128-byte row r of each 64-column block
-        uint8_t* v = kv + vst * C::kTileBytes + r * 128;
-        const bool behind = j * kKeys + r >= w.tile.keys;
-        bool bad = false;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          uint4* at = reinterpret_cast<uint4*>(v + (i / 8) * C::kColBytes + (i % 8) * 16);
-          if (behind) {
-            *at = make_uint4(0, 0, 0, 0);
-            continue;
-          }
-          uint4 u = *at;
-          bool hit = false;
-          uint32_t* e = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if ((e[q] & E::kExp) == E::kExp) {
-              e[q] &= 0xFFFF0000u;
-              hit = true;
-            }
-            if ((e[q] & (E::kExp << 16)) == (E::kExp << 16)) {
-              e[q] &= 0x0000FFFFu;
-              hit = true;
-            }
-          }
-          if (hit) *at = u;
-          bad |= hit;
+        tc_fence_after();
+        if (leader) {  // the scores are complete, and with P in S's columns everything this tile's MMAs read before
+          mbar_arrive(&empty[kst]);
+          if (!C::kOwnP && j > 0) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
         }
-        if (bad) {
-          atomicMin(bad_lo, j);
-          atomicMax(bad_hi, j);
-        }
-        fence_proxy_async();
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[x]);
-      kst += 2;
-      if (kst >= S) kst -= S;
-      vst += 2;
-      if (vst >= S) vst -= S, vpar ^= 1;
-    }
-    // ---- the row's result
-    if (ok && my_nt > 0) ok = mbar_wait(&ofull[x], C::kOwnP ? (my_nt - 1) & 1 : 0, abort_flag, a.err);
-    if (leader && ok && my_nt > 0) {  // the stages that only the other tile still reads
-      const int other = x == 0 ? nt[1] : nt[0];
-      if (my_nt < other) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
-      for (int i = 2 * my_nt; i < 2 * other && ok; ++i) {
-        ok = mbar_wait(&full[i % S], (i / S) & 1, abort_flag, a.err);
-        mbar_arrive(&empty[i % S]);
-      }
-    }
-    if (__all_sync(0xffffffffu, ok)) {
-      tc_fence_after();
-      const int my_head = w.head[x], my_t0 = w.t0[x];
-      const bool mine = r < w.rows[x], any = M != NEG;
-      T* out = static_cast<T*>(a.out) + static_cast<int64_t>(my_t0 + r) * a.out_row + my_head * a.out_head;
-      const float inv = any ? 1.0f / L : 0.0f;
-      const int blo = my_nt > 0 ? *bad_lo : 0x7FFFFFFF, bhi = my_nt > 0 ? *bad_hi : -1;
+        const int lim = vis - j * kKeys;  // visible columns
+        // The weights by the reference at hand, without looking for the maximum
+        // first: only where a row has none yet, or its weights come out too large
+        // (or not a number), the maximum is taken and the weights once more. A
+        // row's decision is its own: no other row has a part in its bits.
+        bool raise = fresh && M == NEG && lim > 0;
+        uint32_t p[2][32];
+        float add;
+        for (int attempt = fresh ? 1 : 0;; ++attempt) {
+          if (attempt > 0) {
+            float top = NEG;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (my_nt > 0) {
-          tmem_ld32(to + c * 32, o);
-          tmem_wait32(o);
-        }
-        float f[32];
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32];
+              tmem_ld32(ts + c * 32, s);
+              tmem_wait32(s);
+              float mx[4] = {NEG, NEG, NEG, NEG};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = any ? __uint_as_float(o[i]) * inv : 0.0f;
-        if (blo <= bhi && mine) {  // non-finite V elements that this row sees
-          const int end = min(vis, (bhi + 1) * kKeys);
-          for (int k = blo * kKeys; k < end; ++k)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 n = non_finite<T>(a, cta, k, c * 32 + i);
-              f[i] += n.x;
-              f[i + 1] += n.y;
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + i < lim) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+              top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
             }
-        }
-        if (mine) {
+            const float n = raise ? fmaxf(M, top * a.scale_log2 - E::kHead) : M;
+            const float f = !raise ? 1.0f : M == NEG ? 0.0f : pex2(M - n);
+            M = n;
+            L *= f;
+            fresh = __any_sync(0xffffffffu, M == NEG);
+            if (j > 0) {  // O is complete up to tile j - 1: without kOwnP its MMAs precede this tile's scores
+              if (C::kOwnP && !__all_sync(0xffffffffu, mbar_wait(&ofull[x], (no + j - 1) & 1, abort_flag, a.err))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(to + c * 32, o);
+                tmem_wait32(o);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint4 u;
-            u.x = E::pack(f[8 * q], f[8 * q + 1]);
-            u.y = E::pack(f[8 * q + 2], f[8 * q + 3]);
-            u.z = E::pack(f[8 * q + 4], f[8 * q + 5]);
-            u.w = E::pack(f[8 * q + 6], f[8 * q + 7]);
-            *reinterpret_cast<uint4*>(out + c * 32 + q * 8) = u;
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(to + c * 32, o);
+              }
+            }
           }
+          const float ref = M == NEG ? 0.0f : M;
+          const uint64_t sc2 = pack_f32x2(a.scale_log2, a.scale_log2), ref2 = pack_f32x2(-ref, -ref);
+          add = j >= edge_from ? weights<T, true>(ts, lim, sc2, ref2, p) : weights<T, false>(ts, lim, sc2, ref2, p);
+          raise = !raise && !(add <= E::kMaxSum);
+          if (attempt == 2 || !__any_sync(0xffffffffu, raise)) break;
+        }
+        if (!ok) break;
+        L += add;
+        if (C::kOwnP && j > 0) {  // the previous tile's P V has read P and V
+          ok = mbar_wait(&ofull[x], (no + j - 1) & 1, abort_flag, a.err);
+          tc_fence_after();
+          if (leader) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
+          __syncwarp();
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) tmem_st32(tmem + lanes + C::kP + x * C::kPStep + half * 32, p[half]);
+        // V in a tile cut by the causal edge or the sequence's end, before its first use
+        if (j >= fix_from) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[vst], vpar, abort_flag, a.err)) != 0;
+          if (!ok) break;
+          // thread r: key row r of the tile, which lies at 128-byte row r of each 64-column block
+          uint8_t* v = kv + vst * C::kTileBytes + r * 128;
+          const bool behind = j * kKeys + r >= w.tile.keys;
+          bool bad = false;
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {
+            uint4* at = reinterpret_cast<uint4*>(v + (i / 8) * C::kColBytes + (i % 8) * 16);
+            if (behind) {
+              *at = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 u = *at;
+            bool hit = false;
+            uint32_t* e = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if ((e[q] & E::kExp) == E::kExp) {
+                e[q] &= 0xFFFF0000u;
+                hit = true;
+              }
+              if ((e[q] & (E::kExp << 16)) == (E::kExp << 16)) {
+                e[q] &= 0x0000FFFFu;
+                hit = true;
+              }
+            }
+            if (hit) *at = u;
+            bad |= hit;
+          }
+          if (bad) {
+            atomicMin(&cta.bad_lo, j);
+            atomicMax(&cta.bad_hi, j);
+          }
+          fence_proxy_async();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[x]);
+        kst += 2;
+        if (kst >= S) kst -= S;
+        vst += 2;
+        if (vst >= S) vst -= S, vpar ^= 1;
+      }
+      // ---- the row's result
+      if (ok && my_nt > 0) {
+        ok = mbar_wait(&ofull[x], (C::kOwnP ? no + my_nt - 1 : no) & 1, abort_flag, a.err);
+        no += C::kOwnP ? my_nt : 1;
+      }
+      if (leader && ok) {  // the last tile's V, then the stages that only the other tile reads
+        if (my_nt > 0) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
+        for (int i = seq + 2 * my_nt; i < seq + 2 * other_nt && ok; ++i) {
+          ok = mbar_wait(&full[i % S], (i / S) & 1, abort_flag, a.err);
+          mbar_arrive(&empty[i % S]);
         }
       }
-      if (mine && a.lse != nullptr)
-        a.lse[static_cast<int64_t>(my_t0 + r) * a.heads + my_head] = any ? (M + log2f(L)) * 0.6931471805599453f : NEG;
+      seq += 2 * max(my_nt, other_nt);
+      ok = __all_sync(0xffffffffu, ok) != 0;
+      if (ok) {
+        tc_fence_after();
+        const int my_head = w.head[x], my_t0 = w.t0[x];
+        const bool mine = r < w.rows[x], any = M != NEG;
+        T* out = static_cast<T*>(a.out) + static_cast<int64_t>(my_t0 + r) * a.out_row + my_head * a.out_head;
+        const float inv = any ? 1.0f / L : 0.0f;
+        const int blo = my_nt > 0 ? w.bad_lo : 0x7FFFFFFF, bhi = my_nt > 0 ? w.bad_hi : -1;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (my_nt > 0) {
+            tmem_ld32(to + c * 32, o);
+            tmem_wait32(o);
+          }
+          float f[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[i] = any ? __uint_as_float(o[i]) * inv : 0.0f;
+          if (blo <= bhi && mine) {  // non-finite V elements that this row sees
+            const int end = min(vis, (bhi + 1) * kKeys);
+            for (int k = blo * kKeys; k < end; ++k)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 n = non_finite<T>(a, cta, k, c * 32 + i);
+                f[i] += n.x;
+                f[i + 1] += n.y;
+              }
+          }
+          if (mine) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint4 u;
+              u.x = E::pack(f[8 * q], f[8 * q + 1]);
+              u.y = E::pack(f[8 * q + 2], f[8 * q + 3]);
+              u.z = E::pack(f[8 * q + 4], f[8 * q + 5]);
+              u.w = E::pack(f[8 * q + 6], f[8 * q + 7]);
+              *reinterpret_cast<uint4*>(out + c * 32 + q * 8) = u;
+            }
+          }
+        }
+        if (mine && a.lse != nullptr)
+          a.lse[static_cast<int64_t>(my_t0 + r) * a.heads + my_head] = any ? (M + log2f(L)) * 0.6931471805599453f : NEG;
+      }
+  unit_read();
     }
     tc_fence_before();
   }
