@@ -235,8 +235,8 @@ def _caches(caches, num_blocks):
     """The C array for caches whose first axis is the page."""
     flat = []
     for t in caches:
-        shape = _here(t, "a cache").shape
-        if len(shape) < 2 or shape[0] != num_blocks:
+        _here(t, "a cache")
+        if t.dim() < 2 or t.size(0) != num_blocks:
             raise DsaError(f"a cache must have {num_blocks} pages as its first axis")
         if t.is_contiguous():
             size = stride = t.nbytes // num_blocks

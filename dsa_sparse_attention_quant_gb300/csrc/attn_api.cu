@@ -235,8 +235,10 @@ PagesWs pages_carve(int64_t num_blocks, int32_t n, void* base) {
 
 constexpr int64_t kMaxBlocks = INT_MAX / kBlock;
 
+constexpr int kMaxLists = 16;
+
 int check_caches(const DsaCacheDesc* caches, int32_t n) {
-  if (n < 0 || (n > 0 && caches == nullptr)) return DSA_EINVAL;
+  if (n < 0 || n > kMaxLists * kMaxCaches || (n > 0 && caches == nullptr)) return DSA_EINVAL;
   for (int32_t i = 0; i < n; ++i) {
     const DsaCacheDesc& c = caches[i];
     if (!c.base || !aligned16(c.base) || c.page_bytes < 16 || c.page_bytes % 16 != 0 || c.page_stride % 16 != 0 ||
@@ -256,11 +258,9 @@ int check_pages(const DsaPages* g, bool lens) {
 }
 
 // Calls f(lists, n) with the caches in lists of kMaxCaches; one empty list without caches.
-constexpr int kMaxLists = 16;
 template <typename F>
 int with_lists(const DsaCacheDesc* caches, int32_t n, F f) {
   constexpr int64_t part = 32768;
-  if (n > kMaxLists * kMaxCaches) return DSA_EINVAL;
   CacheList lists[kMaxLists];
   int m = 0;
   for (int32_t i = 0; i < n || m == 0; ++m) {

@@ -15,7 +15,8 @@ namespace dsa {
 namespace {
 
 // ------------------------------------------------------------------ kv write
-// A warp per token: both rows' 16-byte chunks, eight in flight per lane.
+// A warp per token: both rows' 16-byte chunks, eight in flight per lane. Bound
+// by HBM, one read and one write of the rows.
 constexpr int kWriteThreads = 256;
 
 template <int D>
@@ -368,9 +369,10 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const __grid
   }
 }
 
-// CTAs that copy: four 256-thread CTAs per SM, fewer for little work.
+// CTAs that copy: eight per SM, fewer for little work. (Five of them fit at
+// once; with four per SM, all resident, a 1 GB move took 184 us, so 178.)
 int copy_ctas(int64_t units, int num_sms) {
-  const int64_t cap = static_cast<int64_t>(num_sms) * 4;
+  const int64_t cap = static_cast<int64_t>(num_sms) * 8;
   return static_cast<int>(units < cap ? (units > 0 ? units : 1) : cap);
 }
 
@@ -379,7 +381,9 @@ int copy_ctas(int64_t units, int num_sms) {
 cudaError_t launch_kv_write(const KvWriteArgs& a, int head_dim, int num_sms, cudaStream_t stream) {
   const int64_t per = kWriteThreads / 32;
   int64_t grid = (a.n_tokens + per - 1) / per;
-  const int64_t cap = static_cast<int64_t>(num_sms) * 8;
+  // a warp per token as a rule: with eight CTAs per SM looping over the tokens,
+  // 32768 tokens of 8 x 128 took 45.8 us, so 44.1
+  const int64_t cap = static_cast<int64_t>(num_sms) * 64;
   if (grid > cap) grid = cap;
   if (head_dim == 128)
     kv_write_kernel<128><<<static_cast<unsigned>(grid), kWriteThreads, 0, stream>>>(a);

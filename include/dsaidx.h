@@ -466,7 +466,7 @@ DSA_API int dsa_attn_prompt(const DsaBatch *batch, const DsaKv *kv, const int32_
  *   refs         device int32 [num_blocks], 16-byte aligned
  *   block_table  device int32 [n_rows, bt_stride]
  *   seq_lens     device int32 [n_rows]: ceil(len/64) entries of a row count
- *   caches       host array [n_caches] (n_caches may be 0): page p is
+ *   caches       host array [n_caches] (0 to 1024 of them): page p is
  *                page_bytes bytes (a multiple of 16) at base + p*page_stride
  *                (device, 16-byte aligned; stride a multiple of 16, at least
  *                page_bytes)
