@@ -292,6 +292,26 @@ __device__ __forceinline__ float weights(uint32_t ts, int lim, uint64_t sc2, uin
   return l.x + l.y;
 }
 
+// Within each four lanes: piece q of lane i goes to piece i of lane q.
+__device__ __forceinline__ void transpose4(uint4 (&u)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint4& lo = u[bit == 1 ? 2 * k : k];
+      uint4& hi = u[bit == 1 ? 2 * k + 1 : k + 2];
+      const bool up = lane & bit;
+      uint4 v = up ? lo : hi;
+      v.x = __shfl_xor_sync(0xffffffffu, v.x, bit);
+      v.y = __shfl_xor_sync(0xffffffffu, v.y, bit);
+      v.z = __shfl_xor_sync(0xffffffffu, v.z, bit);
+      v.w = __shfl_xor_sync(0xffffffffu, v.w, bit);
+      lo = up ? v : lo;
+      hi = up ? hi : v;
+    }
+}
+
 // What a CTA works on: one unit of the grid, its own or a taken-over one.
 struct PromptCta {
   PromptTile tile;
@@ -327,20 +347,27 @@ __device__ __forceinline__ int read_next(const void* next) {
   return x;
 }
 
-// V's elements (col, col + 1) of key k as far as they are not finite, else 0.
-template <typename T>
-__device__ __noinline__ float2 non_finite(const PromptArgs& a, const PromptCta& cta, int k, int col) {
-  int64_t at;
-  if (a.kv_start == nullptr) {
-    const int id = __ldg(a.block_table + static_cast<int64_t>(cta.tile.req) * a.bt_stride + k / kBlock);
-    if (id < 0 || id >= a.num_blocks) return make_float2(0.0f, 0.0f);
-    at = id * a.v_page + static_cast<int64_t>(k % kBlock) * a.v_slot;
-  } else {
-    at = static_cast<int64_t>(cta.tile.kv0 + k) * a.v_slot;
+// Add V's elements of keys [k0, k1) to a stored row of D values, as far as they
+// are not finite: what was cleared for the MMA.
+template <int D, typename T>
+__device__ __forceinline__ void add_non_finite(const PromptArgs& a, const PromptCta& cta, int k0, int k1, T* out) {
+#pragma unroll 1
+  for (int k = k0; k < k1; ++k) {
+    int64_t at;
+    if (a.kv_start == nullptr) {
+      const int id = __ldg(a.block_table + static_cast<int64_t>(cta.tile.req) * a.bt_stride + k / kBlock);
+      if (id < 0 || id >= a.num_blocks) continue;
+      at = id * a.v_page + static_cast<int64_t>(k % kBlock) * a.v_slot;
+    } else {
+      at = static_cast<int64_t>(cta.tile.kv0 + k) * a.v_slot;
+    }
+    const T* v = static_cast<const T*>(a.v) + at + cta.head[0] / a.group * a.v_head;
+#pragma unroll 1
+    for (int i = 0; i < D; ++i) {
+      const float x = static_cast<float>(v[i]);
+      if (!isfinite(x)) out[i] = static_cast<T>(static_cast<float>(out[i]) + x);
+    }
   }
-  const T* v = static_cast<const T*>(a.v) + at + cta.head[0] / a.group * a.v_head + col;
-  const float x = static_cast<float>(v[0]), y = static_cast<float>(v[1]);
-  return make_float2(isfinite(x) ? 0.0f : x, isfinite(y) ? 0.0f : y);
 }
 
 template <int D, typename T>
@@ -425,7 +452,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       bool ok = true, ended = false, pending = false;
       while (ok) {
         const int u = units & 1;
-        if (units >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&uempty[u], ((units >> 1) - 1) & 1, abort_flag, a.err)) != 0;
+        if (units >= 2)
+          ok = __all_sync(0xffffffffu, mbar_wait(&uempty[u], ((units >> 1) - 1) & 1, abort_flag, a.err)) != 0;
         if (!ok) break;
         PromptCta& c = ctas[u];
         const int hu = item < 0 ? 0 : item % a.head_units;
@@ -699,15 +727,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (attempt > 0) {
             float top = NEG;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t s[32];
-              tmem_ld32(ts + c * 32, s);
-              tmem_wait32(s);
-              float mx[4] = {NEG, NEG, NEG, NEG};
+            for (int c = 0; c < 2; ++c) {
+              uint32_t s[2][32];
+              tmem_ld32(ts + c * 64, s[0]);
+              tmem_ld32(ts + c * 64 + 32, s[1]);
+              tmem_wait32(s[0]);
+              tmem_wait32(s[1]);
+              const int end = j < edge_from ? kKeys : lim - c * 64;
+              float mx[8];
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c * 32 + i < lim) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
-              top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+              for (int i = 0; i < 64; ++i) {
+                const float v = i < end ? __uint_as_float(s[i / 32][i % 32]) : NEG;
+                mx[i & 7] = i < 8 ? v : fmaxf(mx[i & 7], v);
+              }
+              top = fmaxf(top, fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                     fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))));
             }
             const float n = raise ? fmaxf(M, top * a.scale_log2 - E::kHead) : M;
             const float f = !raise ? 1.0f : M == NEG ? 0.0f : pex2(M - n);
@@ -751,33 +785,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (j >= fix_from) {
           ok = __all_sync(0xffffffffu, mbar_wait(&full[vst], vpar, abort_flag, a.err)) != 0;
           if (!ok) break;
-          // thread r: key row r of the tile, which lies at 128-byte row r of each 64-column block
+          // thread r: key row r of the tile, which lies at 128-byte row r of each
+          // 64-column block; its 16-byte pieces in another order in each lane, so
+          // that the lanes' banks differ
           uint8_t* v = kv + vst * C::kTileBytes + r * 128;
-          const bool behind = j * kKeys + r >= w.tile.keys;
           bool bad = false;
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            uint4* at = reinterpret_cast<uint4*>(v + (i / 8) * C::kColBytes + (i % 8) * 16);
-            if (behind) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 u = *at;
-            bool hit = false;
-            uint32_t* e = reinterpret_cast<uint32_t*>(&u);
+          if (j * kKeys + r >= w.tile.keys) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if ((e[q] & E::kExp) == E::kExp) {
-                e[q] &= 0xFFFF0000u;
-                hit = true;
-              }
-              if ((e[q] & (E::kExp << 16)) == (E::kExp << 16)) {
-                e[q] &= 0x0000FFFFu;
-                hit = true;
+            for (int i = 0; i < D / 8; ++i)
+              *reinterpret_cast<uint4*>(v + (i / 8) * C::kColBytes + ((i ^ r) % 8) * 16) = make_uint4(0, 0, 0, 0);
+          } else {
+            // an exponent of all ones, plus its last bit's weight, carries into the sign's place
+            constexpr uint32_t kOnes = E::kExp * 0x10001u, kOne = (E::kExp & (0u - E::kExp)) * 0x10001u;
+            uint32_t hit = 0;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              const uint4 u = *reinterpret_cast<const uint4*>(v + (i / 8) * C::kColBytes + ((i ^ r) % 8) * 16);
+              hit |= ((u.x & kOnes) + kOne) | ((u.y & kOnes) + kOne) | ((u.z & kOnes) + kOne) | ((u.w & kOnes) + kOne);
+            }
+            bad = hit & 0x80008000u;
+            if (bad) {
+              for (int i = 0; i < D / 2; ++i) {
+                uint32_t* at = reinterpret_cast<uint32_t*>(v + (i / 32) * C::kColBytes + (i % 32) * 4);
+                const uint32_t e = (*at & kOnes) + kOne;
+                *at &= ((e & 0x8000u) ? 0u : 0xFFFFu) | ((e & 0x80000000u) ? 0u : 0xFFFF0000u);
               }
             }
-            if (hit) *at = u;
-            bad |= hit;
           }
           if (bad) {
             atomicMin(&cta.bad_lo, j);
@@ -811,41 +844,38 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (ok) {
         tc_fence_after();
         const int my_head = w.head[x], my_t0 = w.t0[x];
-        const bool mine = r < w.rows[x], any = M != NEG;
-        T* out = static_cast<T*>(a.out) + static_cast<int64_t>(my_t0 + r) * a.out_row + my_head * a.out_head;
+        const int my_rows = w.rows[x];
+        const bool mine = r < my_rows, any = M != NEG;
         const float inv = any ? 1.0f / L : 0.0f;
         const int blo = my_nt > 0 ? w.bad_lo : 0x7FFFFFFF, bhi = my_nt > 0 ? w.bad_hi : -1;
+        // after the exchange below this lane stores 16 bytes of rows r / 4 * 4 + q
+        T* out = static_cast<T*>(a.out) + static_cast<int64_t>(my_t0 + (r & ~3)) * a.out_row + my_head * a.out_head +
+                 (lane & 3) * 8;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 32; ++c, out += 32) {
           uint32_t o[32];
           if (my_nt > 0) {
             tmem_ld32(to + c * 32, o);
             tmem_wait32(o);
           }
-          float f[32];
+          uint4 u[4];
+          auto pk = [&](int i) {
+            return any ? E::pack(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv) : 0u;
+          };
 #pragma unroll
-          for (int i = 0; i < 32; ++i) f[i] = any ? __uint_as_float(o[i]) * inv : 0.0f;
-          if (blo <= bhi && mine) {  // non-finite V elements that this row sees
-            const int end = min(vis, (bhi + 1) * kKeys);
-            for (int k = blo * kKeys; k < end; ++k)
+          for (int q = 0; q < 4; ++q) u[q] = make_uint4(pk(8 * q), pk(8 * q + 2), pk(8 * q + 4), pk(8 * q + 6));
+          transpose4(u);
+          T* at = out;
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 n = non_finite<T>(a, cta, k, c * 32 + i);
-                f[i] += n.x;
-                f[i + 1] += n.y;
-              }
-          }
-          if (mine) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint4 u;
-              u.x = E::pack(f[8 * q], f[8 * q + 1]);
-              u.y = E::pack(f[8 * q + 2], f[8 * q + 3]);
-              u.z = E::pack(f[8 * q + 4], f[8 * q + 5]);
-              u.w = E::pack(f[8 * q + 6], f[8 * q + 7]);
-              *reinterpret_cast<uint4*>(out + c * 32 + q * 8) = u;
-            }
-          }
+          for (int q = 0; q < 4; ++q, at += a.out_row)
+            if ((r & ~3) + q < my_rows) *reinterpret_cast<uint4*>(at) = u[q];
+        }
+        if (blo <= bhi) {
+          __syncwarp();  // the row was stored by four lanes
+          if (mine)
+            add_non_finite<D, T>(a, cta, blo * kKeys, min(vis, (bhi + 1) * kKeys),
+                                 static_cast<T*>(a.out) + static_cast<int64_t>(my_t0 + r) * a.out_row +
+                                     my_head * a.out_head);
         }
         if (mine && a.lse != nullptr)
           a.lse[static_cast<int64_t>(my_t0 + r) * a.heads + my_head] = any ? (M + log2f(L)) * 0.6931471805599453f : NEG;
