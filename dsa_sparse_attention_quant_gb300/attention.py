@@ -43,9 +43,7 @@ assert (_KV.size, _ATTN.size, _PAGES.size) == tuple(ctypes.sizeof(c) for c in (D
 
 def _here(t, what, dtype=None):
     """A CUDA tensor of the current device (and of dtype)."""
-    if not isinstance(t, torch.Tensor):
-        raise DsaError(f"{what} must be a CUDA tensor")
-    at = t.get_device()
+    at = t.get_device() if isinstance(t, torch.Tensor) else -1
     if at < 0:
         raise DsaError(f"{what} must be a CUDA tensor")
     if at != _device():
@@ -65,40 +63,30 @@ def _err(dev_err):
     return None if dev_err is None else _dense(dev_err, "dev_err", torch.int32).data_ptr()
 
 
-def _strides(t, what):
-    """Strides of all axes but the last, which must be contiguous; an axis of
-    one element gets the row's length, since torch leaves such a stride
-    arbitrary."""
-    s = t.stride()
-    if s[-1] != 1:
-        raise DsaError(f"{what} must have a contiguous last axis")
-    shape = t.shape
-    if 1 in shape:
-        return [x if n > 1 else shape[-1] for x, n in zip(s[:-1], shape[:-1])]
-    return s[:-1]
-
-
-def _kv(k_cache, v_cache, packed=False):
-    """(C description, heads, head_dim) of a cache [num_blocks, 64, heads,
+def _kv(k, v, packed=False):
+    """(C description, heads, head_dim, dtype) of a cache [num_blocks, 64, heads,
     head_dim], or of packed rows [rows, heads, head_dim]; any strides with a
     contiguous last axis."""
-    shape = _here(k_cache, "k").shape
-    dtype = k_cache.dtype
+    _here(k, "k")
+    shape, dtype = k.shape, k.dtype
     code = _DTYPES.get(dtype)
     if code is None:
         raise DsaError(f"k must be bf16 or fp16, got {dtype}")
-    if _here(v_cache, "v", dtype).shape != shape:
+    if not isinstance(v, torch.Tensor) or v.get_device() != k.get_device() or v.dtype is not dtype or v.shape != shape:
+        _here(v, "v", dtype)
         raise DsaError("k and v must have one shape")
-    ks, vs = _strides(k_cache, "k"), _strides(v_cache, "v")
+    ks, vs = k.stride(), v.stride()
+    if ks[-1] != 1 or vs[-1] != 1:
+        raise DsaError("k and v must have a contiguous last axis")
     if packed:
         if len(shape) != 3:
             raise DsaError("k and v must be [rows, heads, head_dim]")
         n, heads, d = shape
-        return _KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), code, heads, d, n, d, *ks, d, *vs), heads, d
+        return _KV.pack(k.data_ptr(), v.data_ptr(), code, heads, d, n, d, ks[0], ks[1], d, vs[0], vs[1]), heads, d, dtype
     if len(shape) != 4 or shape[1] != BLOCK_SIZE:
         raise DsaError("k and v must be [num_blocks, 64, heads, head_dim]")
     n, _, heads, d = shape
-    return _KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), code, heads, d, n, *ks, *vs), heads, d
+    return _KV.pack(k.data_ptr(), v.data_ptr(), code, heads, d, n, *ks[:3], *vs[:3]), heads, d, dtype
 
 
 def _made(stream, shape, dtype, device, covered):
@@ -123,14 +111,19 @@ def _attn(q, out, lse, kv_heads, d, dtype, scale, first, rows, stream):
         raise DsaError(f"{heads} query heads cannot share {kv_heads} KV heads")
     if out is None:
         out = _made(stream, shape, dtype, q.device, first == 0 and rows == n)
-    elif _here(out, "out", dtype).shape != shape:
+    elif not isinstance(out, torch.Tensor) or out.get_device() != q.get_device() or out.dtype is not dtype \
+            or out.shape != shape:
+        _here(out, "out", dtype)
         raise DsaError("out must have q's shape")
     if lse is None:
         lse = _made(stream, shape[:2], torch.float32, q.device, first == 0 and rows == n)
     elif _dense(lse, "lse", torch.float32).shape != shape[:2]:
         raise DsaError("lse must be [tokens, heads]")
-    return (_ATTN.pack(q.data_ptr(), *_strides(q, "q"), out.data_ptr(), *_strides(out, "out"), lse.data_ptr(), heads,
-                       scale), out, lse, heads)
+    qs, os = q.stride(), out.stride()
+    if qs[2] != 1 or os[2] != 1:
+        raise DsaError("q and out must have a contiguous last axis")
+    return (_ATTN.pack(q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1], lse.data_ptr(), heads, scale), out,
+            lse, heads)
 
 
 def _on(stream):
@@ -155,16 +148,18 @@ def _scratch(ws, nbytes, device, stream):
 def kv_write(k, v, slot_mapping, k_cache, v_cache, dev_err=None, stream=None):
     """Write the rows k and v [tokens, heads, head_dim] at their slots (int64,
     -1 = padding) of the caches [num_blocks, 64, heads, head_dim]."""
-    kv, heads, d = _kv(k_cache, v_cache)
+    kv, heads, d, dtype = _kv(k_cache, v_cache)
     n = _dense(slot_mapping, "slot_mapping", torch.int64).numel()
     want = (n, heads, d)
     for t, what in ((k, "k rows"), (v, "v rows")):
-        if _here(t, what, k_cache.dtype).shape != want:
+        if _here(t, what, dtype).shape != want:
             raise DsaError(f"{what} must be [{n}, {heads}, {d}]")
+        if t.stride(2) != 1:
+            raise DsaError(f"{what} must have a contiguous last axis")
     if n == 0:
         return
-    st = load().dsa_kv_write(k.data_ptr(), *_strides(k, "k rows"), v.data_ptr(), *_strides(v, "v rows"), n,
-                             slot_mapping.data_ptr(), kv, _err(dev_err), _on(stream))
+    st = load().dsa_kv_write(k.data_ptr(), *k.stride()[:2], v.data_ptr(), *v.stride()[:2], n, slot_mapping.data_ptr(),
+                             kv, _err(dev_err), _on(stream))
     _check(st, "dsa_kv_write")
 
 
@@ -178,8 +173,8 @@ def attn_decode(batch, q, k_cache, v_cache, scale: float = 0.0, out=None, lse=No
     """Attention of the batch's decode tokens, rows [0, num_decode_tokens) of q
     [tokens, heads, head_dim], over their requests' pages. Returns (out, lse);
     the other rows of a passed ``out`` and ``lse`` stay as they were."""
-    kv, kv_heads, d = _kv(k_cache, v_cache)
-    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, k_cache.dtype, scale, 0, batch.num_decode_tokens, stream)
+    kv, kv_heads, d, dtype = _kv(k_cache, v_cache)
+    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, dtype, scale, 0, batch.num_decode_tokens, stream)
     ws = _scratch(ws, lambda: attn_decode_workspace_size(batch, heads, kv_heads, d), q.device, stream)
     st = load().dsa_attn_decode(ctypes.byref(batch.c), kv, at, ws.data_ptr(), ws.numel(), _err(dev_err), _on(stream))
     _check(st, "dsa_attn_decode")
@@ -195,12 +190,12 @@ def attn_selected(q, k_cache, v_cache, physical, scale: float = 0.0, out=None, l
                   stream=None):
     """Attention of each row of q [tokens, heads, head_dim] over the slots
     physical [tokens, topk] (int32, -1 = none) selects for it. Returns (out, lse)."""
-    kv, kv_heads, d = _kv(k_cache, v_cache)
+    kv, kv_heads, d, dtype = _kv(k_cache, v_cache)
     shape = _dense(physical, "physical", torch.int32).shape
     if len(shape) != 2 or shape[1] < 1:
         raise DsaError("physical must be [tokens, topk]")
     n, topk = shape
-    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, k_cache.dtype, scale, 0, n, stream)
+    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, dtype, scale, 0, n, stream)
     if q.shape[0] != n:
         raise DsaError(f"q has {q.shape[0]} rows, physical {n}")
     ws = _scratch(ws, lambda: attn_selected_workspace_size(n, topk, heads, kv_heads, d), q.device, stream)
@@ -216,14 +211,13 @@ def attn_prompt(batch, q, k, v, scale: float = 0.0, kv_start=None, out=None, lse
     with ``kv_start`` (int32 [num_reqs]) packed rows [rows, heads, head_dim]
     where key s of request r is row kv_start[r] + s. Returns (out, lse); the
     other rows of a passed ``out`` and ``lse`` stay as they were."""
-    kv, kv_heads, d = _kv(k, v, packed=kv_start is not None)
+    kv, kv_heads, d, dtype = _kv(k, v, packed=kv_start is not None)
     start = None
     if kv_start is not None:
         start = _dense(kv_start, "kv_start", torch.int32).data_ptr()
         if kv_start.numel() < batch.num_reqs:
             raise DsaError("kv_start needs an entry per request")
-    at, out, lse, _ = _attn(q, out, lse, kv_heads, d, k.dtype, scale, batch.num_decode_tokens, batch.num_tokens,
-                            stream)
+    at, out, lse, _ = _attn(q, out, lse, kv_heads, d, dtype, scale, batch.num_decode_tokens, batch.num_tokens, stream)
     st = load().dsa_attn_prompt(ctypes.byref(batch.c), kv, start, at, _err(dev_err), _on(stream))
     _check(st, "dsa_attn_prompt")
     return out, lse

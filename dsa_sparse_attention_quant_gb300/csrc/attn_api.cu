@@ -29,21 +29,23 @@ int check_kv(const DsaKv* kv, bool packed, DsaKv* out) {
   const int d = kv->head_dim;
   if (kv->num_kv_heads == 1) out->k_head_stride = out->v_head_stride = d;
   if (packed || kv->num_blocks == 1) out->k_page_stride = out->v_page_stride = d;
+  if (packed && kv->num_blocks == 1) out->k_slot_stride = out->v_slot_stride = d;
   for (int64_t s : {out->k_page_stride, out->k_slot_stride, out->k_head_stride, out->v_page_stride,
                     out->v_slot_stride, out->v_head_stride})
     if (!stride_ok(s, d)) return DSA_EINVAL;
   return DSA_OK;
 }
 
-// rows: the rows of q and out that the call may reach.
-int check_attn(const DsaAttn* at, const DsaKv& kv, DsaAttn* out) {
+// rows: the rows of q and out that the call may reach, from the first.
+int check_attn(const DsaAttn* at, const DsaKv& kv, int64_t rows, DsaAttn* out) {
   if (at == nullptr) return DSA_EINVAL;
   *out = *at;
   if (!at->q || !at->out || !aligned16(at->q) || !aligned16(at->out)) return DSA_EINVAL;
   if (at->lse != nullptr && reinterpret_cast<uintptr_t>(at->lse) % 4 != 0) return DSA_EINVAL;
   if (at->num_heads < 1 || at->num_heads > 65535 || at->num_heads % kv.num_kv_heads != 0) return DSA_EINVAL;
   if (at->num_heads == 1) out->q_head_stride = out->out_head_stride = kv.head_dim;
-  for (int64_t s : {at->q_row_stride, out->q_head_stride, at->out_row_stride, out->out_head_stride})
+  if (rows == 1) out->q_row_stride = out->out_row_stride = kv.head_dim;
+  for (int64_t s : {out->q_row_stride, out->q_head_stride, out->out_row_stride, out->out_head_stride})
     if (!stride_ok(s, kv.head_dim)) return DSA_EINVAL;
   if (std::isinf(at->scale) && at->scale > 0) return DSA_EINVAL;
   if (!(at->scale > 0.0f)) out->scale = kv.head_dim == 128 ? 0.08838834764831845f : 0.125f;
@@ -343,7 +345,9 @@ int dsa_attn_decode(const DsaBatch* batch, const DsaKv* kv, const DsaAttn* attn,
   int st = check_step(batch);
   if (st != DSA_OK) return st;
   if (batch->num_decode_tokens == 0) return DSA_OK;
-  if ((st = check_kv(kv, false, &c)) != DSA_OK || (st = check_attn(attn, c, &at)) != DSA_OK) return st;
+  if ((st = check_kv(kv, false, &c)) != DSA_OK ||
+      (st = check_attn(attn, c, batch->num_decode_tokens, &at)) != DSA_OK)
+    return st;
   if (batch->num_blocks != c.num_blocks || batch->num_decodes < 1) return DSA_EINVAL;
   RowsArgs a = rows_args(c, at);
   a.qsl = batch->query_start_loc;
@@ -370,7 +374,7 @@ int dsa_attn_selected(const DsaKv* kv, const DsaAttn* attn, const int32_t* physi
   if (n_tokens < 0 || n_tokens > INT_MAX || topk < 1) return DSA_EINVAL;
   if (n_tokens == 0) return DSA_OK;
   int st = check_kv(kv, false, &c);
-  if (st != DSA_OK || (st = check_attn(attn, c, &at)) != DSA_OK) return st;
+  if (st != DSA_OK || (st = check_attn(attn, c, n_tokens, &at)) != DSA_OK) return st;
   if (physical == nullptr) return DSA_EINVAL;
   RowsArgs a = rows_args(c, at);
   a.physical = physical;
@@ -389,7 +393,9 @@ int dsa_attn_prompt(const DsaBatch* batch, const DsaKv* kv, const int32_t* kv_st
   const int64_t rows = batch->num_tokens - batch->num_decode_tokens;
   if (rows == 0) return DSA_OK;
   const bool packed = kv_start != nullptr;
-  if ((st = check_kv(kv, packed, &c)) != DSA_OK || (st = check_attn(attn, c, &at)) != DSA_OK) return st;
+  if ((st = check_kv(kv, packed, &c)) != DSA_OK ||
+      (st = check_attn(attn, c, batch->num_tokens, &at)) != DSA_OK)
+    return st;
   if (reqs < 1 || (!packed && batch->num_blocks != c.num_blocks)) return DSA_EINVAL;
   int sms;
   if ((st = device_sms(&sms)) != DSA_OK) return st;

@@ -351,9 +351,8 @@ DSA_API int dsa_gather_rows(const uint8_t *rows, int64_t num_rows, int64_t row_b
  *   k, v        device, 16-byte aligned
  *   head_dim    64 or 128
  *   num_blocks  pages, >= 1 (packed rows in dsa_attn_prompt: rows of k and v)
- *   strides     multiples of 8, at least head_dim, below 2^39; the page stride
- *               of a one-page cache and the head stride of a one-head cache
- *               are not used. */
+ *   strides     multiples of 8, at least head_dim, below 2^39; that of an axis
+ *               of one element (one page, one head, one packed row) is not used */
 #define DSA_BF16 0
 #define DSA_FP16 1
 typedef struct DsaKv {
@@ -391,7 +390,8 @@ DSA_API int dsa_kv_write(const void *k, int64_t k_row_stride, int64_t k_head_str
  * Keys that a token does not see have no influence on its row, whatever bits
  * they hold (NaN and infinities included); a visible NaN gives NaN.
  *   q, out   device [T, num_heads, head_dim] of the cache's type, 16-byte
- *            aligned; row and head strides in elements, multiples of 8
+ *            aligned; row and head strides in elements, multiples of 8, at
+ *            least head_dim (that of an axis of one element is not used)
  *   lse      device fp32 [T, num_heads] contiguous, or NULL
  *   num_heads  a multiple of kv->num_kv_heads
  *   scale    <= 0 selects head_dim^-0.5 */
