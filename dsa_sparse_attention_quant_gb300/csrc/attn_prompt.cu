@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (nt[x] == 0 || !ok) continue;
-            if (nq[x] > 0) ok = __all_sync(0xffffffffu, mbar_wait(&qempty[x], (nq[x] - 1) & 1, abort_flag, a.err)) != 0;
+            if (nq[x] > 0)
+              ok = __all_sync(0xffffffffu, mbar_wait(&qempty[x], (nq[x] - 1) & 1, abort_flag, a.err)) != 0;
             ++nq[x];
             if (ok && lane == 0) {
               mbar_arrive_expect_tx(&qfull[x], C::kTileBytes);
@@ -845,7 +846,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc_fence_after();
         const int my_head = w.head[x], my_t0 = w.t0[x];
         const int my_rows = w.rows[x];
-        const bool mine = r < my_rows, any = M != NEG;
+        // (no score but NaN leaves M alone, and a sum of NaN)
+        const bool mine = r < my_rows, any = M != NEG || L != 0.0f;
         const float inv = any ? 1.0f / L : 0.0f;
         const int blo = my_nt > 0 ? w.bad_lo : 0x7FFFFFFF, bhi = my_nt > 0 ? w.bad_hi : -1;
         // after the exchange below this lane stores 16 bytes of rows r / 4 * 4 + q

@@ -386,7 +386,8 @@ DSA_API int dsa_kv_write(const void *k, int64_t k_row_stride, int64_t k_head_str
  *   out[t,e] = sum_j e^(s_j) v[j,h] / sum_j e^(s_j),  lse[t,e] = ln sum_j e^(s_j).
  * Scores, sums and the running maximum are fp32; the weights e^(s_j - max) are
  * rounded to the inputs' type for the product with V, the result once more
- * when it is stored. A token that sees no key gets out = 0, lse = -infinity.
+ * when it is stored. A token that sees no key, or whose scores are all
+ * -infinity, gets out = 0, lse = -infinity.
  * Keys that a token does not see have no influence on its row, whatever bits
  * they hold (NaN and infinities included); a visible NaN gives NaN.
  *   q, out   device [T, num_heads, head_dim] of the cache's type, 16-byte

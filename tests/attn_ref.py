@@ -8,7 +8,8 @@ type, ``torch.finfo(t).eps / 2``; A = sum_j p_j |v_j| / sum_j p_j):
     the exponential's 2^-21, relative;
   * weights are rounded to the type for the product with V: u * A;
   * fp32 sums over n keys: n * 2^-24 * A in the numerator, n * 2^-24 of the sum;
-  * fp16 weights below 2^-24 are lost: at most n * 2^-30 of the largest weight,
+  * fp16 weights below 2^-24 are rounded to a multiple of it, an error of 2^-25
+    at most, where the row's largest weight is 2^4 or more: n * 2^-29 of it,
     times max |v|;
   * the result is rounded to the type: u * |out| (fp16: or half its least step).
 """
@@ -32,7 +33,7 @@ def attend(q, k, v, scale, dtype):
     u = torch.finfo(dtype).eps / 2
     es = (d + 8) * 2.0 ** -23 * float(((k.abs() @ q.abs()) * scale + s.abs()).max()) + 2.0 ** -21
     sums = n * 2.0 ** -24
-    low = n * 2.0 ** -30 * float(v.abs().max()) if dtype == torch.float16 else 0.0
+    low = n * 2.0 ** -29 * float(v.abs().max()) if dtype == torch.float16 else 0.0
     tol = (u + 2 * es + 2 * sums) * a + u * out.abs() + low + (2.0 ** -25 if dtype == torch.float16 else 0.0)
     return out, float(lse), tol, es + sums + 2.0 ** -22 * (1 + abs(float(lse)))
 
@@ -55,7 +56,7 @@ def attend_rows(q, k, v, visible, scale, dtype):
     mag = torch.where(seen, (q.abs() @ k.abs().T) * scale + raw.abs(), torch.zeros_like(raw))
     es = (d + 8) * 2.0 ** -23 * mag.amax(1) + 2.0 ** -21
     sums = vis.double() * 2.0 ** -24
-    low = vis.double() * 2.0 ** -30 * v.abs().max() if dtype == torch.float16 else sums * 0
+    low = vis.double() * 2.0 ** -29 * v.abs().max() if dtype == torch.float16 else sums * 0
     tol = (u + 2 * es + 2 * sums)[:, None] * a + u * out.abs() + low[:, None]
     tol = tol + (2.0 ** -25 if dtype == torch.float16 else 0.0)
     return out, lse, tol, es + sums + 2.0 ** -22 * (1 + torch.where(vis > 0, lse, torch.zeros_like(lse)).abs())

@@ -183,6 +183,26 @@ def test_prompt_non_finite_rows_reach_only_those_that_see_them(hq, hkv, dtype):
     assert torch.equal(lse[:350], clean_lse[:350]) and bool(torch.isnan(lse[350:]).all())
 
 
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (3, 1)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_prompt_rows_of_nothing_but_nan_or_infinity(hq, hkv, dtype):
+    n = 300
+    p = Prompts(16, [n, n], [n, n], hq, hkv, 128, dtype, False, gap=0)
+    clean, _ = p.run()
+    p.k[:, 0, 5] = torch.where(torch.arange(2 * n, device=DEV) < 140, math.nan, p.k[:, 0, 5].float()).to(dtype)
+    out, lse = p.run()
+    assert bool(torch.isnan(out[:n]).all()) and bool(torch.isnan(lse[:n]).all())   # rows that see NaN scores, or only them
+    assert torch.equal(out[n:], clean[n:])
+    p.q.abs_()
+    p.k[:140] = -math.inf        # the first rows' scores are all -infinity: as if they saw no key
+    out, lse = p.run()
+    assert bool((out[:140] == 0).all()) and bool((lse[:140] == -math.inf).all())
+    assert bool(torch.isfinite(out[140:]).all()) and bool(torch.isfinite(lse[140:]).all())
+    for e in range(hq):          # the later ones see the finite keys alone
+        k, v = p.k[140:n, 0], p.v[140:n, 0]
+        check(out[140:n, e], lse[140:n, e], attend_rows(p.q[140:n, e], k, v, range(1, n - 139), 128 ** -0.5, dtype))
+
+
 def test_prompt_bad_metadata_is_flagged():
     p = Prompts(12, [100, 200, 90], [100, 200, 90], 4, 2, 64, torch.bfloat16, True)
     err = i32([0])

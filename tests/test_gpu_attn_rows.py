@@ -171,6 +171,27 @@ def test_decode_visible_nan_stays_in_its_rows():
     assert not bool(torch.isnan(out[0, 2:]).any()) and not bool(torch.isnan(out[1]).any())
 
 
+@pytest.mark.parametrize("keys", [40, 3000])
+def test_rows_of_nothing_but_nan_or_infinity(keys):
+    s = Step(18, [keys, keys, keys, 5], [1] * 4, 4, 2, 64, torch.bfloat16)
+    bt = s.batch.block_table.long()
+    pages = [bt[r, :(keys + 63) // 64] for r in range(3)]
+    s.k[pages[0], :, 0, 3] = math.nan       # request 0, KV head 0: every score NaN
+    s.q[1].abs_()
+    s.k[pages[1], :, 1, :] = -math.inf      # request 1, KV head 1: every score -infinity
+    s.q[2].abs_()
+    s.k[pages[2][0], 7, 1, :] = math.inf    # request 2, KV head 1: one score +infinity
+    phys = torch.full((4, keys), -1, dtype=torch.int32, device=DEV)
+    for r in range(3):
+        j = torch.arange(keys, device=DEV)
+        phys[r] = (bt[r][j // 64] * 64 + j % 64).to(torch.int32)
+    for out, lse in (dsa.attn_decode(s.batch, s.q, s.k, s.v), dsa.attn_selected(s.q, s.k, s.v, phys)):
+        assert bool(torch.isnan(out[0, :2]).all()) and bool(torch.isnan(lse[0, :2]).all())
+        assert bool(torch.isfinite(out[0, 2:]).all()) and bool(torch.isfinite(out[1, :2]).all())
+        assert bool((out[1, 2:] == 0).all()) and bool((lse[1, 2:] == -math.inf).all())
+        assert bool(torch.isnan(out[2, 2:]).all()) and bool(torch.isfinite(out[2, :2]).all())
+
+
 def test_decode_bad_metadata_is_flagged():
     s = Step(17, [100, 200, 300], [1, 1, 1], 4, 2, 64, torch.bfloat16)
     err = i32([0])
