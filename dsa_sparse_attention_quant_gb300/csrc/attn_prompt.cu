@@ -23,12 +23,16 @@
 //    back to TMEM as the A operand of P V (never through shared memory),
 //    rescaling, and the final store.
 //  * warp 8: TMA. K and V tiles take turns in one ring (D = 128: five 32 KB
-//    stages); a page (64 slots of a head) is one box per 64 columns.
+//    stages, D = 64: twelve of 16 KB); a page (64 slots of a head) is one box per
+//    64 columns.
 //  * warp 9: issues the MMAs, the tiles taking turns. V is read as stored, keys
 //    along rows: B is "MN-major", K and Q are K-major; all in the 128-byte
 //    swizzle.
-//  * TMEM: S of both tiles (2 x 128 columns), O of both (2 x D), P over S or, at
-//    D = 64, beside it.
+//  * TMEM: O of both tiles (2 x D columns) and buffers of S (128 columns), P over
+//    its S. D = 128: a buffer for each tile. D = 64: room for three that all steps
+//    take in turn, so that a step's Q K^T is issued three steps ahead and the
+//    softmax warps, which bound it there, find their next scores ready (2 x 8192,
+//    32/8 heads: 553 -> 525 us against two buffers and P beside them).
 // CTAs are numbered from the last query tile of the last request down, so the
 // longest tiles start first and the short ones fill the tail.
 //
@@ -60,23 +64,23 @@ struct PromptCfg {
   static constexpr int kTileBytes = kKeys * D * 2;      // a Q, K or V tile
   static constexpr int kBoxBytes = kBlock * 128;        // 64 slots of 64 columns
   static constexpr int kColBytes = kKeys * 128;         // 64 columns of a tile
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 5 : 12;
   static constexpr int kOffKv = 2 * kTileBytes;
   static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
-  static constexpr int kNumBars = 2 * kStages + 5 * 2 + 2 * 2 + 1 + 1;
+  // Buffers of S that the tiles take in turn, P over its S. D = 128: TMEM holds
+  // one for each tile. D = 64: three for both, so a tile's next scores are there
+  // when its weights are done.
+  static constexpr bool kRing = D == 64;
+  static constexpr int kBufs = kRing ? 3 : 1;  // of a tile at a time, at most
+  static constexpr int kNumBars = 2 * kStages + 2 * 2 + 2 * kBufs + 3 + 2 * 2 + 2 * 2 + 1 + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffNext = (kOffMisc + 16 + 15) / 16 * 16;  // the 16 bytes of a taken-over CTA's index
   static constexpr int kOffCta = kOffNext + 16;
   static constexpr int kSmemBytes = kOffCta + 2 * 96 + 1024;  // + slack to align the base to 1024
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kO = 256;                   // first column of O
-  // P lies over its S (D = 128: TMEM is full), or beside it: then the next
-  // tile's scores do not wait for P V.
-  static constexpr bool kOwnP = D == 64;
-  static constexpr uint32_t kP = kOwnP ? kO + 2 * D : 0;      // first column of P
-  static constexpr uint32_t kPStep = kOwnP ? kKeys / 2 : 128;  // from tile 0's to tile 1's
+  static constexpr uint32_t kO = kRing ? 3 * kKeys : 2 * kKeys;  // first column of O
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-  static_assert(kO + 2 * D + (kOwnP ? kKeys : 0) <= kTmemCols, "TMEM budget");
+  static_assert(kO + 2 * D <= kTmemCols, "TMEM budget");
 };
 
 template <typename T>
@@ -255,14 +259,18 @@ __device__ __forceinline__ float weights(uint32_t ts, int lim, uint64_t sc2, uin
   constexpr int G = 4;  // pairs of columns per step
   uint64_t sum[4] = {0, 0, 0, 0};
   uint32_t s[4][32];
+  tmem_ld32(ts, s[0]);
+  tmem_wait32(s[0]);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_wait32(s[c]);
+  for (int c = 1; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
   float2 w[2][G];
 #pragma unroll
   for (int g = 0; g <= 64 / G; ++g) {
     if (g < 64 / G) {
+      if (g == 16 / G) {
+#pragma unroll
+        for (int c = 1; c < 4; ++c) tmem_wait32(s[c]);
+      }
       float2 x[G];
 #pragma unroll
       for (int i = 0; i < G; ++i) {
@@ -384,10 +392,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint64_t* empty = full + S;
   uint64_t* qfull = empty + S;
   uint64_t* qempty = qfull + 2;
-  uint64_t* sfull = qempty + 2;
-  uint64_t* pfull = sfull + 2;
-  uint64_t* ofull = pfull + 2;
-  uint64_t* ufull = ofull + 2;   // a unit's PromptCta is written
+  uint64_t* sfull = qempty + 2;          // tile x's nth scores: [x * kBufs + n % kBufs]
+  uint64_t* pfull = sfull + 2 * C::kBufs;  // the weights in a buffer
+  uint64_t* ofull = pfull + 3;             // its O, complete up to the nth tile (kRing) or unit: [x + 2 * (n % 2)]
+  uint64_t* ufull = ofull + 4;   // a unit's PromptCta is written
   uint64_t* uempty = ufull + 2;  // and read by all
   uint64_t* asked = uempty + 2;
   uint64_t* done = asked + 1;
@@ -405,12 +413,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     for (int x = 0; x < 2; ++x) {
       mbar_init(&qfull[x], 1);
       mbar_init(&qempty[x], 1);
-      mbar_init(&sfull[x], 1);
-      mbar_init(&pfull[x], kSoftWarps / 2);
+      for (int b = 0; b < C::kBufs; ++b) mbar_init(&sfull[x * C::kBufs + b], 1);
       mbar_init(&ofull[x], 1);
+      mbar_init(&ofull[x + 2], 1);
       mbar_init(&ufull[x], 1);
       mbar_init(&uempty[x], kSoftWarps + 1);
     }
+    for (int b = 0; b < 3; ++b) mbar_init(&pfull[b], kSoftWarps / 2);
     mbar_init(asked, 1);
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -596,15 +605,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         auto wait = [&](uint64_t* bar, uint32_t parity) {
           return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)) != 0;
         };
-        auto scores = [&](int x, int st) {
+        int seq = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // ring stages, units and tiles so far
+        int on[2] = {0, 0};  // which of the two ofull the tile completes next
+        // ring stages and parities of the next K and V; kRing: buffers of the next S
+        // and P, and which of its sfull a tile completes next
+        int kst = 0, vst = 1, sbuf = 0, pbuf = 0, sn[2] = {0, 0};
+        uint32_t kpar = 0, vpar = 0, ppar = 0;
+        auto scores = [&](int x, int st, int buf, uint64_t* bar) {
           const uint32_t kd = kmajor_lo(kv0 + st * C::kTileBytes), qx = qd + ((x * C::kTileBytes) >> 4);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t off = ((k / 4) * C::kColBytes + (k % 4) * 32) >> 4;
-              mma_f16_ss(tmem + x * 128, qx + off, kd + off, kIdS, k > 0);
+              mma_f16_ss(tmem + buf * kKeys, qx + off, kd + off, kIdS, k > 0);
             }
-            mma_commit(&sfull[x]);
+            mma_commit(bar);
+          }
+          __syncwarp();
+        };
+        auto values = [&](int x, int st, int buf, bool acc) {
+          const uint32_t vd = mnmajor_lo(kv0 + st * C::kTileBytes);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_f16_ts(tmem + C::kO + x * D, tmem + buf * kKeys + k * 8, vd + ((k * 16 * 128) >> 4), kIdO,
+                         acc || k > 0);
+            if constexpr (C::kRing) mma_commit(&ofull[x + 2 * on[x]]);  // elsewhere a unit's last alone
           }
           __syncwarp();
         };
@@ -613,61 +639,121 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           __syncwarp();
         };
         bool ok = true;
-        int seq = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // ring stages, units and tiles so far
         const volatile PromptCta* w;
         while (ok && next_unit(&w)) {
           const int nt[2] = {w->nt[0], w->nt[1]};
           unit_read();
           const int n_tiles = max(nt[0], nt[1]);
           if (n_tiles == 0) continue;
-          ok = wait(&full[seq % S], (seq / S) & 1);
+          if constexpr (C::kRing) {
+            // Steps (tile x, key tile j) in turn, each: P V, then Q K^T of the third
+            // step after it, into the buffer just read. Stages and parities are kept
+            // as running values: this warp's instructions are between one step's
+            // MMAs and the next one's.
+            auto bump = [&](int& st, uint32_t& par) {
+              st += 2;
+              if (st >= S) st -= S, par ^= 1;
+            };
+            auto step_scores = [&](int x) {  // of tile x, K in stage kst, S to buffer sbuf
+              scores(x, kst, sbuf, &sfull[x * 3 + sn[x]]);
+              sn[x] = sn[x] == 2 ? 0 : sn[x] + 1;
+              sbuf = sbuf == 2 ? 0 : sbuf + 1;
+            };
+            auto step_values = [&](int x, int j) {  // of tile x, V in stage vst, P in buffer pbuf
+              ok = wait(&pfull[pbuf], ppar);
+              if (!ok) return;
+              tc_fence_after();
+              values(x, vst, pbuf, j > 0);
+              on[x] ^= 1;
+              if (++pbuf == 3) pbuf = 0, ppar ^= 1;
+            };
+            int qj = 0, j = 0;  // key tiles of the next scores and P V
+            bool q1 = false;    // the next scores are tile 1's
+            auto next_scores = [&]() {  // wherever they are
+              if (qj >= n_tiles || !ok) return;
+              if (!q1 && qj >= nt[0]) q1 = true;
+              if (q1 && qj >= nt[1]) {
+                q1 = qj + 1 >= nt[0];
+                ++qj;
+                bump(kst, kpar);
+              }
+              if (qj >= n_tiles) return;
+              const int x = q1;
+              if (qj == 0) ok = wait(&qfull[x], x == 0 ? nq[0]++ & 1 : nq[1]++ & 1);
+              ok = ok && wait(&full[kst], kpar);
+              if (!ok) return;
+              if (x == 0)
+                step_scores(0);
+              else
+                step_scores(1);
+              if (qj + 1 == (x == 0 ? nt[0] : nt[1])) release(&qempty[x]);  // the unit's last use of this query tile
+              if (q1) {
+                ++qj;
+                bump(kst, kpar);
+              }
+              q1 = !q1;
+            };
+            for (int i = 0; i < 3; ++i) next_scores();
+            while (j < n_tiles && ok) {
+              ok = wait(&full[vst], vpar);
+              if (j + 3 < min(nt[0], nt[1])) {  // both tiles go on: scores of (1, j + 1) and (0, j + 2)
+                if (ok) step_values(0, j);
+                if (ok) step_scores(1);
+                bump(kst, kpar);
+                ok = ok && wait(&full[kst], kpar);
+                if (ok) step_values(1, j);
+                if (ok) step_scores(0);
+                ++qj;
+              } else {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (nt[x] == 0 || !ok) continue;
-            ok = wait(&qfull[x], nq[x]++ & 1);
-            if (ok) scores(x, seq % S);
-            if (nt[x] == 1) release(&qempty[x]);
-          }
-          int vst = (seq + 1) % S, kst = (seq + 2) % S;
-          uint32_t vpar = ((seq + 1) / S) & 1, kpar = ((seq + 2) / S) & 1;
-          ok = ok && wait(&full[vst], vpar);
-          for (int j = 0; j < n_tiles && ok; ++j) {
-            const uint32_t vd = mnmajor_lo(kv0 + vst * C::kTileBytes);
-            bool have_k = false;
+                for (int x = 0; x < 2; ++x) {
+                  if (j >= nt[x] || !ok) continue;
+                  step_values(x, j);
+                  next_scores();
+                }
+              }
+              ++j;
+              bump(vst, vpar);
+            }
+            // kst has passed, or passes, the unit's last K
+            for (; qj < n_tiles; ++qj) bump(kst, kpar);
+          } else {
+            ok = wait(&full[seq % S], (seq / S) & 1);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (j >= nt[x]) continue;
-              if (C::kOwnP && !have_k && j + 1 < nt[x]) {  // mostly there already: not left until P is
-                ok = ok && wait(&full[kst], kpar);
-                have_k = true;
-              }
-              ok = ok && wait(&pfull[x], np[x]++ & 1);
-              if (!ok) break;
-              tc_fence_after();
-              auto next_scores = [&]() {
-                if (j + 1 >= nt[x]) return;
+              if (nt[x] == 0 || !ok) continue;
+              ok = wait(&qfull[x], nq[x]++ & 1);
+              if (ok) scores(x, seq % S, x, &sfull[x]);
+              if (nt[x] == 1) release(&qempty[x]);
+            }
+            vst = (seq + 1) % S, kst = (seq + 2) % S;
+            vpar = ((seq + 1) / S) & 1, kpar = ((seq + 2) / S) & 1;
+            ok = ok && wait(&full[vst], vpar);
+            for (int j = 0; j < n_tiles && ok; ++j) {
+              bool have_k = false;
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                if (j >= nt[x]) continue;
+                ok = ok && wait(&pfull[x], np[x]++ & 1);
+                if (!ok) break;
+                tc_fence_after();
+                values(x, vst, x, j > 0);
+                if (j == nt[x] - 1) {
+                  release(&ofull[x + 2 * on[x]]);
+                  on[x] ^= 1;
+                }
+                if (j + 1 >= nt[x]) continue;
                 if (!have_k) ok = wait(&full[kst], kpar);
                 have_k = true;
-                if (ok) scores(x, kst);
+                if (ok) scores(x, kst, x, &sfull[x]);
                 if (j + 2 == nt[x]) release(&qempty[x]);  // the unit's last use of this query tile
-              };
-              if constexpr (C::kOwnP) next_scores();
-              if (!ok) break;
-              if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                  mma_f16_ts(tmem + C::kO + x * D, tmem + C::kP + x * C::kPStep + k * 8, vd + ((k * 16 * 128) >> 4),
-                             kIdO, j > 0 || k > 0);
-                if (C::kOwnP || j == nt[x] - 1) mma_commit(&ofull[x]);
               }
-              __syncwarp();
-              if constexpr (!C::kOwnP) next_scores();
+              for (int i = 0; i < 2; ++i) {
+                if (++vst == S) vst = 0, vpar ^= 1;
+                if (++kst == S) kst = 0, kpar ^= 1;
+              }
+              if (ok && j + 1 < n_tiles) ok = wait(&full[vst], vpar);
             }
-            for (int i = 0; i < 2; ++i) {
-              if (++vst == S) vst = 0, vpar ^= 1;
-              if (++kst == S) kst = 0, kpar ^= 1;
-            }
-            if (ok && j + 1 < n_tiles) ok = wait(&full[vst], vpar);
           }
           seq += 2 * n_tiles;
         }
@@ -687,12 +773,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int x = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + C::kO + x * D;
+    const uint32_t to = tmem + lanes + C::kO + x * D;
     const float NEG = -INFINITY;
     const bool leader = (warp & 3) == 0 && lane == 0;
     bool ok = true;
     int seq = 0;  // ring stages so far
-    int ns = 0, no = 0;  // tiles, and rounds of ofull, so far
+    int ns = 0;         // tiles so far
+    int base = 0, no = 0;  // kRing: both tiles' tiles in the units before; rounds of ofull waited for
     const volatile PromptCta* wp;
     while (ok && next_unit(&wp)) {
       const volatile PromptCta& w = *wp;
@@ -708,13 +795,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                   : max(visible(w.pos0[1], w.tile.keys) / kKeys, other_nt);
       int kst = seq % S, vst = (seq + 1) % S;  // ring stages of tile j
       uint32_t vpar = ((seq + 1) / S) & 1;
-      for (int j = 0; j < my_nt; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[x], ns++ & 1, abort_flag, a.err)) != 0;
+      // O complete up to the unit's tile j, or (not kRing, j = 0) its last
+      const int first_o = C::kRing ? ns : no;
+      auto wait_o = [&](int j) {
+        bool k = true;
+        for (; k && no <= first_o + j; ++no)
+          k = __all_sync(0xffffffffu, mbar_wait(&ofull[x + 2 * (no & 1)], (no >> 1) & 1, abort_flag, a.err)) != 0;
+        tc_fence_after();
+        return k;
+      };
+      for (int j = 0; j < my_nt; ++j, ++ns) {
+        // its step's buffer: the steps before it are the tiles before it, and the other tile's
+        const int buf = C::kRing ? (base + j + min(j + x, other_nt)) % 3 : x;
+        const uint32_t ts = tmem + lanes + buf * kKeys;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[x * C::kBufs + ns % C::kBufs], (ns / C::kBufs) & 1, abort_flag,
+                                               a.err)) != 0;
         if (!ok) break;
         tc_fence_after();
-        if (leader) {  // the scores are complete, and with P in S's columns everything this tile's MMAs read before
+        if (leader) {  // the scores are complete, and with one buffer all that this tile's MMAs read before
           mbar_arrive(&empty[kst]);
-          if (!C::kOwnP && j > 0) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
+          if (!C::kRing && j > 0) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
         }
         const int lim = vis - j * kKeys;  // visible columns
         // The weights by the reference at hand, without looking for the maximum
@@ -749,12 +849,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             M = n;
             L *= f;
             fresh = __any_sync(0xffffffffu, M == NEG);
-            if (j > 0) {  // O is complete up to tile j - 1: without kOwnP its MMAs precede this tile's scores
-              if (C::kOwnP && !__all_sync(0xffffffffu, mbar_wait(&ofull[x], (no + j - 1) & 1, abort_flag, a.err))) {
+            if (j > 0) {
+              if (C::kRing && !wait_o(j - 1)) {  // (with one buffer, its MMAs precede this tile's scores)
                 ok = false;
                 break;
               }
-              tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -774,14 +873,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         if (!ok) break;
         L += add;
-        if (C::kOwnP && j > 0) {  // the previous tile's P V has read P and V
-          ok = mbar_wait(&ofull[x], (no + j - 1) & 1, abort_flag, a.err);
-          tc_fence_after();
-          if (leader) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
-          __syncwarp();
+        if (C::kRing && j > 1) {  // P V of the tile before the previous one: V was read (mostly long ago)
+          ok = wait_o(j - 2);
+          if (leader) mbar_arrive(&empty[kst < 3 ? kst + S - 3 : kst - 3]);
         }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) tmem_st32(tmem + lanes + C::kP + x * C::kPStep + half * 32, p[half]);
+        for (int half = 0; half < 2; ++half) tmem_st32(ts + half * 32, p[half]);
         // V in a tile cut by the causal edge or the sequence's end, before its first use
         if (j >= fix_from) {
           ok = __all_sync(0xffffffffu, mbar_wait(&full[vst], vpar, abort_flag, a.err)) != 0;
@@ -822,7 +919,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[x]);
+        if (lane == 0) mbar_arrive(&pfull[buf]);
         kst += 2;
         if (kst >= S) kst -= S;
         vst += 2;
@@ -830,11 +927,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       // ---- the row's result
       if (ok && my_nt > 0) {
-        ok = mbar_wait(&ofull[x], (C::kOwnP ? no + my_nt - 1 : no) & 1, abort_flag, a.err);
-        no += C::kOwnP ? my_nt : 1;
+        ok = wait_o(C::kRing ? my_nt - 1 : 0);
       }
-      if (leader && ok) {  // the last tile's V, then the stages that only the other tile reads
-        if (my_nt > 0) mbar_arrive(&empty[kst == 0 ? S - 1 : kst - 1]);
+      base += my_nt + other_nt;
+      if (leader && ok) {  // the last V's, then the stages that only the other tile reads
+        for (int i = C::kRing ? 2 : 1; i > 0; --i)
+          if (my_nt >= i) mbar_arrive(&empty[(seq + 2 * (my_nt - i) + 1) % S]);
         for (int i = seq + 2 * my_nt; i < seq + 2 * other_nt && ok; ++i) {
           ok = mbar_wait(&full[i % S], (i / S) & 1, abort_flag, a.err);
           mbar_arrive(&empty[i % S]);
@@ -882,7 +980,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (mine && a.lse != nullptr)
           a.lse[static_cast<int64_t>(my_t0 + r) * a.heads + my_head] = any ? (M + log2f(L)) * 0.6931471805599453f : NEG;
       }
-  unit_read();
+      unit_read();
     }
     tc_fence_before();
   }

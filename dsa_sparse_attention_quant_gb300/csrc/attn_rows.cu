@@ -434,7 +434,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
 #pragma unroll 2
         for (int i = threadIdx.x; i < C::kRows * CH; i += kThreads) {
           const int r = i / CH, c = i % CH;
-          const uint4 v = r < rows ? __ldg(reinterpret_cast<const uint4*>(q + r * a.q_head + c * 8)) : make_uint4(0, 0, 0, 0);
+          const uint4 v =
+              r < rows ? __ldg(reinterpret_cast<const uint4*>(q + r * a.q_head + c * 8)) : make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4*>(qbuf + r * C::kRowBytes + ((c ^ (r & 7)) << 4)) = v;
         }
         __syncthreads();
@@ -607,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
             for (int y = 0; y < D / 8; ++y)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<float2*>(obuf + ((warp - step) * C::kRows + x * 16 + g + 8 * e) * D + (y ^ g) * 8 + c2) =
+                *reinterpret_cast<float2*>(obuf + ((warp - step) * C::kRows + x * 16 + g + 8 * e) * D +
+                                           (y ^ g) * 8 + c2) =
                     make_float2(o[x][y][2 * e], o[x][y][2 * e + 1]);
         }
         __syncthreads();
@@ -644,9 +646,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
               const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
               for (int y = 0; y < D / 8; ++y)
-                *reinterpret_cast<uint32_t*>(out + y * 8 + c2) = E::pack(o[x][y][2 * e] * inv, o[x][y][2 * e + 1] * inv);
+                *reinterpret_cast<uint32_t*>(out + y * 8 + c2) =
+                    E::pack(o[x][y][2 * e] * inv, o[x][y][2 * e + 1] * inv);
               if (a.lse != nullptr && (lane & 3) == 0)
-                a.lse[static_cast<int64_t>(mt.y) * a.heads + head] = L == 0.0f ? NEG : (M + log2f(L)) * 0.6931471805599453f;
+                a.lse[static_cast<int64_t>(mt.y) * a.heads + head] =
+                    L == 0.0f ? NEG : (M + log2f(L)) * 0.6931471805599453f;
             } else {
               float* po = a.part_o + (slot * C::kRows + r) * D;
 #pragma unroll

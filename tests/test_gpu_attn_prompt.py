@@ -191,7 +191,8 @@ def test_prompt_rows_of_nothing_but_nan_or_infinity(hq, hkv, dtype):
     clean, _ = p.run()
     p.k[:, 0, 5] = torch.where(torch.arange(2 * n, device=DEV) < 140, math.nan, p.k[:, 0, 5].float()).to(dtype)
     out, lse = p.run()
-    assert bool(torch.isnan(out[:n]).all()) and bool(torch.isnan(lse[:n]).all())   # rows that see NaN scores, or only them
+    # rows that see NaN scores, or nothing else
+    assert bool(torch.isnan(out[:n]).all()) and bool(torch.isnan(lse[:n]).all())
     assert torch.equal(out[n:], clean[n:])
     p.q.abs_()
     p.k[:140] = -math.inf        # the first rows' scores are all -infinity: as if they saw no key
@@ -228,6 +229,22 @@ def test_prompt_bad_metadata_is_flagged():
     out, lse = packed.run(dev_err=err)
     assert int(err.item()) == 16 and bool((lse[100:] == -math.inf).all())
     packed.check(out, lse, only=(0,))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_uneven_pairs_of_tiles(d, dtype):
+    # token tiles in pairs of 2, 1 and unequal numbers of key tiles, several pairs
+    # a CTA; scores that rise over the keys, so that references move in any of them
+    q = [100, 300, 256, 1, 129, 640, 128, 257, 31, 511] * 4
+    k = [m + c for m, c in zip(q, [3000, 0, 700, 1500, 127, 0, 0, 1, 900, 130] * 4)]
+    p = Prompts(19, q, k, 7, 7, d, dtype, False, gap=0)
+    up = torch.cat([torch.arange(n, device=DEV) / 100 for n in k])[:, None, None]
+    p.q[:, 1:4] = p.q[:, 1:4].abs()
+    p.k[:, 1:4] = (p.k[:, 1:4].float() / 4 + up).to(dtype)
+    p.kf = list(p.k.split(k))
+    out, lse = p.run()
+    p.check(out, lse)
 
 
 def test_prompt_many_requests_and_same_bits():
