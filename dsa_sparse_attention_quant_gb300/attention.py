@@ -227,17 +227,21 @@ def attn_prompt(batch, q, k, v, scale: float = 0.0, kv_start=None, out=None, lse
 
 def _caches(caches, num_blocks):
     """The C array for caches whose first axis is the page."""
-    flat = []
+    flat, like, dev, size = [], None, -1, 0
     for t in caches:
-        _here(t, "a cache")
-        if t.dim() < 2 or t.size(0) != num_blocks:
-            raise DsaError(f"a cache must have {num_blocks} pages as its first axis")
-        if t.is_contiguous():
-            size = stride = t.nbytes // num_blocks
-        elif t[0].is_contiguous():
-            size, stride = t[0].nbytes, t.stride(0) * t.element_size() if num_blocks > 1 else t[0].nbytes
-        else:
-            raise DsaError("a cache must have contiguous pages")
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev or dev < 0:
+            dev = _here(t, "a cache").get_device()
+        kind = t.shape, t.dtype
+        if kind != like:   # a model's caches are mostly alike
+            if t.dim() < 2 or t.size(0) != num_blocks:
+                raise DsaError(f"a cache must have {num_blocks} pages as its first axis")
+            like, size = kind, t.nbytes // max(num_blocks, 1)
+        stride = size
+        if not t.is_contiguous():
+            if not t[0].is_contiguous():
+                raise DsaError("a cache must have contiguous pages")
+            if num_blocks > 1:
+                stride = t.stride(0) * t.element_size()
         flat += (t.data_ptr(), size, stride)
     return struct.pack(f"{len(flat)}q", *flat), len(caches)
 
