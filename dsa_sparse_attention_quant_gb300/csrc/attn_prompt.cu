@@ -188,7 +188,7 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// The request and query tile of one CTA, found from the metadata by each warp.
+// The request and query tile of one unit, found from the metadata.
 struct PromptTile {
   int req;
   int t0, ntok;   // first token (row of q) of the CTA's rows, tokens left in the request from there
@@ -198,12 +198,24 @@ struct PromptTile {
   bool found;
 };
 
-__device__ __forceinline__ PromptTile find_tile(const PromptArgs& a, int rank, bool flag) {
+// Where a search ended: 32 requests from the base-th last one, `before` units
+// behind them, and the number of all units once it is known. A CTA's units come
+// in rising order as a rule, so the next search starts there (4096 prompts of
+// 128, 16/2 heads of 128: 1.33 ms; from the last request each time 8.8).
+struct PromptFind {
+  int base = 0, before = 0, end = 0x7FFFFFFF;
+};
+
+__device__ __forceinline__ PromptTile find_tile(const PromptArgs& a, int rank, PromptFind* at) {
   const int lane = threadIdx.x & 31;
   const int unit = a.pair_heads ? kRowsTile : 2 * kRowsTile;
   PromptTile p{};
-  int before = 0;  // units of the requests behind this one
-  for (int base = 0; base < a.num_reqs - a.num_decodes; base += 32) {
+  if (rank >= at->end) return p;
+  if (rank < at->before) at->base = at->before = 0;
+  int before = at->before;  // units of the requests behind this one
+  for (int base = at->base; base < a.num_reqs - a.num_decodes; base += 32) {
+    at->base = base;
+    at->before = before;
     const int r = a.num_reqs - 1 - base - lane;
     int q0 = 0, q1 = 0, sl = 0, s0 = 0;
     bool bad = false;
@@ -220,7 +232,7 @@ __device__ __forceinline__ PromptTile find_tile(const PromptArgs& a, int rank, b
         bad = true;
         sl = 0;
       }
-      if (bad && flag) flag_error(a.err, DSA_DEVERR_SEQ_RANGE);
+      if (bad) flag_error(a.err, DSA_DEVERR_SEQ_RANGE);
     }
     const int units = (q1 - q0 + unit - 1) / unit;
     int incl = units;
@@ -245,6 +257,7 @@ __device__ __forceinline__ PromptTile find_tile(const PromptArgs& a, int rank, b
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
+  at->end = before;
   return p;
 }
 
@@ -461,7 +474,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       int nq[2] = {0, 0};  // units that loaded query tile x
       int item = blockIdx.x;
       int asks = 0;  // answers read
-      bool ok = true, ended = false, pending = false;
+      PromptFind found_at;
+      bool ok = true, pending = false;
       while (ok) {
         const int u = units & 1;
         if (units >= 2)
@@ -470,10 +484,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         PromptCta& c = ctas[u];
         const int hu = item < 0 ? 0 : item % a.head_units;
         PromptTile tile{};
-        // the grid is an upper bound: behind the first unit that is not there, none is
-        if (item >= 0 && !ended) tile = find_tile(a, item / a.head_units, hu == 0);
-        ended = ended || !tile.found;
-        if (item >= 0 && ended) {  // pass over it, and the ones behind it
+        if (item >= 0) tile = find_tile(a, item / a.head_units, &found_at);
+        const bool none = item >= 0 && !tile.found;  // the grid is an upper bound
+        if (none) {  // pass over it
           if (lane == 0) {
             mbar_arrive_expect_tx(asked, 16);
             ask_next(next, asked);
@@ -481,7 +494,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           pending = true;
         }
         int nt[2] = {0, 0};
-        if (!ended && item >= 0) {
+        if (tile.found) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int shift = a.pair_heads ? 0 : x * kRowsTile;
@@ -496,7 +509,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
           }
         }
-        if (!(item >= 0 && ended)) {
+        if (!none) {
           if (lane == 0) {
             c.tile = tile;
             c.bad_lo = 0x7FFFFFFF;

@@ -256,6 +256,24 @@ def test_prompt_many_requests_and_same_bits():
     assert torch.equal(out, again)
 
 
+def test_prompt_requests_beyond_one_search_step_with_bad_ones_between():
+    # 32 requests are searched at a time: units far apart, empty requests and bad ones in between
+    n = [0 if i % 7 == 3 else 1 + (37 * i) % 150 for i in range(1200)]
+    p = Prompts(20, n, n, 2, 1, 64, torch.bfloat16, False)
+    seq = p.batch.seq_lens.clone()
+    bad = list(range(5, 1200, 97))
+    seq[bad] = -1
+    p.batch = dsa.Batch(p.batch.query_start_loc, seq, p.batch.block_table, p.batch.req_id_per_token, 0,
+                        p.batch.num_blocks, max_seq_len=max(n), num_decode_tokens=0)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = p.run(dev_err=err)
+    assert int(err.item()) == 16
+    for r in bad:
+        a = p.qsl[r]
+        assert bool((out[a:a + n[r]] == 0).all()) and bool((lse[a:a + n[r]] == -math.inf).all())
+    p.check(out, lse, only=[r for r in range(1200) if r not in bad])
+
+
 def test_prompt_captured_and_replayed():
     p = Prompts(15, [300, 100], [500, 100], 4, 2, 128, torch.bfloat16, True)
     want, _ = p.run()
