@@ -4,8 +4,9 @@
 //   S = Q K^T,  P = 2^(S scale log2(e) - M),  O = P V,  out = O / sum(P),
 //   lse = ln 2 * (M + log2 sum(P))
 // tile by tile over the keys. Any M gives the same quotient; it only has to
-// keep P in range. So a row's M is its maximum in the first tile, and P of a
-// later tile is computed by the M at hand, without a search for the maximum:
+// keep P in range. So a row's M is the maximum of the first 32 columns it sees
+// (all 128 of the tile: 2000 cycles more per unit; 512 prompts of 128, 16/2 heads
+// of 128, 171 us, so 153), and P of a tile is computed by the M at hand:
 // only when a row's weights come out too large is M raised (its O and sum
 // rescaled) and P computed again. M never sits above a score that was seen, so
 // the weights cannot all underflow. The rescaling of O, a round trip through
@@ -820,10 +821,55 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc_fence_after();
         return k;
       };
+      // V in a tile cut by the causal edge or the sequence's end, before its first
+      // use: D = 128 while the tile's scores are on the way (8 x 2048, 32/8 heads:
+      // 233 -> 228 us); D = 64, whose scores are there by then, behind the weights
+      // (2 x 8192, 32/8 heads: 536 us, in front 562)
+      auto clear_v = [&](int j) {
+        if (j < fix_from) return true;
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[vst], vpar, abort_flag, a.err)) != 0;
+        if (!ok) return false;
+        // thread r: key row r of the tile, which lies at 128-byte row r of each
+        // 64-column block; its 16-byte pieces in another order in each lane, so
+        // that the lanes' banks differ
+        uint8_t* v = kv + vst * C::kTileBytes + r * 128;
+        bool bad = false;
+        if (j * kKeys + r >= w.tile.keys) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<uint4*>(v + (i / 8) * C::kColBytes + ((i ^ r) % 8) * 16) = make_uint4(0, 0, 0, 0);
+        } else {
+          // an exponent of all ones, plus its last bit's weight, carries into the sign's place
+          constexpr uint32_t kOnes = E::kExp * 0x10001u, kOne = (E::kExp & (0u - E::kExp)) * 0x10001u;
+          uint32_t hit = 0;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 u = *reinterpret_cast<const uint4*>(v + (i / 8) * C::kColBytes + ((i ^ r) % 8) * 16);
+            hit |= ((u.x & kOnes) + kOne) | ((u.y & kOnes) + kOne) | ((u.z & kOnes) + kOne) | ((u.w & kOnes) + kOne);
+          }
+          bad = hit & 0x80008000u;
+          if (bad) {
+            for (int i = 0; i < D / 2; ++i) {
+              uint32_t* at = reinterpret_cast<uint32_t*>(v + (i / 32) * C::kColBytes + (i % 32) * 4);
+              const uint32_t e = (*at & kOnes) + kOne;
+              *at &= ((e & 0x8000u) ? 0u : 0xFFFFu) | ((e & 0x80000000u) ? 0u : 0xFFFF0000u);
+            }
+          }
+        }
+        if (bad) {
+          atomicMin(&cta.bad_lo, j);
+          atomicMax(&cta.bad_hi, j);
+        }
+        fence_proxy_async();
+        return true;
+      };
       for (int j = 0; j < my_nt; ++j, ++ns) {
         // its step's buffer: the steps before it are the tiles before it, and the other tile's
         const int buf = C::kRing ? (base + j + min(j + x, other_nt)) % 3 : x;
         const uint32_t ts = tmem + lanes + buf * kKeys;
+        if constexpr (!C::kRing) {  // while its scores are on the way
+          if (!clear_v(j)) break;
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(&sfull[x * C::kBufs + ns % C::kBufs], (ns / C::kBufs) & 1, abort_flag,
                                                a.err)) != 0;
         if (!ok) break;
@@ -835,12 +881,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int lim = vis - j * kKeys;  // visible columns
         // The weights by the reference at hand, without looking for the maximum
         // first: only where a row has none yet, or its weights come out too large
-        // (or not a number), the maximum is taken and the weights once more. A
+        // (or not a number), the tile's is taken and the weights once more. A
         // row's decision is its own: no other row has a part in its bits.
-        bool raise = fresh && M == NEG && lim > 0;
+        if (fresh) {  // a first reference: the maximum of the columns in front
+          uint32_t s[32];
+          tmem_ld32(ts, s);
+          tmem_wait32(s);
+          float mx[4];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float v = i < lim ? __uint_as_float(s[i]) : NEG;
+            mx[i & 3] = i < 4 ? v : fmaxf(mx[i & 3], v);
+          }
+          // (no weight was above 0 so far: nothing to rescale)
+          if (M == NEG) M = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2 - E::kHead;
+          fresh = __any_sync(0xffffffffu, M == NEG);
+        }
+        bool raise = M == NEG && lim > 0;
         uint32_t p[2][32];
         float add;
-        for (int attempt = fresh ? 1 : 0;; ++attempt) {
+        for (int attempt = __any_sync(0xffffffffu, raise) ? 1 : 0;; ++attempt) {
           if (attempt > 0) {
             float top = NEG;
 #pragma unroll 1
@@ -895,42 +955,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) tmem_st32(ts + half * 32, p[half]);
-        // V in a tile cut by the causal edge or the sequence's end, before its first use
-        if (j >= fix_from) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&full[vst], vpar, abort_flag, a.err)) != 0;
-          if (!ok) break;
-          // thread r: key row r of the tile, which lies at 128-byte row r of each
-          // 64-column block; its 16-byte pieces in another order in each lane, so
-          // that the lanes' banks differ
-          uint8_t* v = kv + vst * C::kTileBytes + r * 128;
-          bool bad = false;
-          if (j * kKeys + r >= w.tile.keys) {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              *reinterpret_cast<uint4*>(v + (i / 8) * C::kColBytes + ((i ^ r) % 8) * 16) = make_uint4(0, 0, 0, 0);
-          } else {
-            // an exponent of all ones, plus its last bit's weight, carries into the sign's place
-            constexpr uint32_t kOnes = E::kExp * 0x10001u, kOne = (E::kExp & (0u - E::kExp)) * 0x10001u;
-            uint32_t hit = 0;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              const uint4 u = *reinterpret_cast<const uint4*>(v + (i / 8) * C::kColBytes + ((i ^ r) % 8) * 16);
-              hit |= ((u.x & kOnes) + kOne) | ((u.y & kOnes) + kOne) | ((u.z & kOnes) + kOne) | ((u.w & kOnes) + kOne);
-            }
-            bad = hit & 0x80008000u;
-            if (bad) {
-              for (int i = 0; i < D / 2; ++i) {
-                uint32_t* at = reinterpret_cast<uint32_t*>(v + (i / 32) * C::kColBytes + (i % 32) * 4);
-                const uint32_t e = (*at & kOnes) + kOne;
-                *at &= ((e & 0x8000u) ? 0u : 0xFFFFu) | ((e & 0x80000000u) ? 0u : 0xFFFF0000u);
-              }
-            }
-          }
-          if (bad) {
-            atomicMin(&cta.bad_lo, j);
-            atomicMax(&cta.bad_hi, j);
-          }
-          fence_proxy_async();
+        if constexpr (C::kRing) {
+          if (!clear_v(j)) break;
         }
         tmem_wait_st();
         tc_fence_before();

@@ -204,6 +204,26 @@ def test_prompt_rows_of_nothing_but_nan_or_infinity(hq, hkv, dtype):
         check(out[140:n, e], lse[140:n, e], attend_rows(p.q[140:n, e], k, v, range(1, n - 139), 128 ** -0.5, dtype))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_prompt_first_columns_say_little_of_the_others(d, dtype):
+    # a first reference far below the maximum, at it, or none: -infinity in the first columns
+    n = 500
+    p = Prompts(21, [n] * 3, [n] * 3, 4, 1, d, dtype, False, gap=0)
+    p.q.abs_()
+    p.k[40:n] *= 20.0
+    p.k[n:n + 50] = 4.0
+    p.k[2 * n:2 * n + 60] = -math.inf
+    p.kf = list(p.k.split(n))
+    out, lse = p.run()
+    p.check(out, lse, only=(0, 1))
+    assert bool((out[2 * n:2 * n + 60] == 0).all()) and bool((lse[2 * n:2 * n + 60] == -math.inf).all())
+    k, v = p.k[2 * n + 60:, 0], p.v[2 * n + 60:, 0]
+    for e in range(4):
+        check(out[2 * n + 60:, e], lse[2 * n + 60:, e],
+              attend_rows(p.q[2 * n + 60:, e], k, v, range(1, n - 59), d ** -0.5, dtype))
+
+
 def test_prompt_bad_metadata_is_flagged():
     p = Prompts(12, [100, 200, 90], [100, 200, 90], 4, 2, 64, torch.bfloat16, True)
     err = i32([0])
