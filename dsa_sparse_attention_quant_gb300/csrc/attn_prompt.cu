@@ -16,8 +16,10 @@
 // fp16 rate of the tensor cores, with 128x128 tiles of S needing one exponential
 // per 4*D operations beside it. Measured: 4 x 8192, 64/8 heads of 128, 2.75 to
 // 2.87 ms (1600 to 1530 TFLOP/s, power-capped; 2 x 8192, 32/8 heads: 1640);
-// 2 x 8192, 32/8 heads of 64, 525 us (1045 TFLOP/s): there a tile pair's
+// 2 x 8192, 32/8 heads of 64, 538 us (1020 TFLOP/s): there a tile pair's
 // exponentials and the rest of its softmax, 2300 cycles, outlast its MMAs, 1024.
+// Short prompts are a chain per unit (scores, weights, P V, the store), 9000
+// cycles: 512 prompts of 128, 16/2 heads of 128, 144 us.
 //
 // Mapping: a CTA holds two query tiles of 128 rows that share one stream of
 // K and V tiles (128 keys): two query heads of one KV head where the group is
@@ -35,8 +37,8 @@
 //  * TMEM: O of both tiles (2 x D columns) and buffers of S (128 columns), P over
 //    its S. D = 128: a buffer for each tile. D = 64: room for three that all steps
 //    take in turn, so that a step's Q K^T is issued three steps ahead and the
-//    softmax warps, which bound it there, find their next scores ready (2 x 8192,
-//    32/8 heads: 553 -> 525 us against two buffers and P beside them).
+//    softmax warps, which bound it there, find their next scores ready (5% less
+//    at 2 x 8192, 32/8 heads, than two buffers and P beside them).
 // CTAs are numbered from the last query tile of the last request down, so the
 // longest tiles start first and the short ones fill the tail.
 //
@@ -268,8 +270,9 @@ __device__ __forceinline__ int visible(int pos, int keys) { return min(max(pos +
 // A row's weights of one tile, packed as the A operand, and their sum: S from
 // TMEM, 2^(s * scale + ref); columns from lim on are out (EDGE only). Written as
 // a software pipeline, eight columns' exponentials issued ahead of the previous
-// eight's sums and packing: left to the compiler's order a tile took 1000
-// cycles and more, so 780 (the exponentials alone are 512).
+// eight's sums and packing, 32 columns of S on the way while the previous ones
+// are worked on: left to the compiler's order a tile took 1000 cycles and more,
+// so 780 (the exponentials alone are 512).
 template <typename T, bool EDGE>
 __device__ __forceinline__ float weights(uint32_t ts, int lim, uint64_t sc2, uint64_t ref2, uint32_t (&p)[2][32]) {
   using E = PElem<T>;
@@ -278,15 +281,15 @@ __device__ __forceinline__ float weights(uint32_t ts, int lim, uint64_t sc2, uin
   uint32_t s[4][32];
   tmem_ld32(ts, s[0]);
   tmem_wait32(s[0]);
-#pragma unroll
-  for (int c = 1; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
+  tmem_ld32(ts + 32, s[1]);
   float2 w[2][G];
 #pragma unroll
   for (int g = 0; g <= 64 / G; ++g) {
     if (g < 64 / G) {
-      if (g == 16 / G) {
-#pragma unroll
-        for (int c = 1; c < 4; ++c) tmem_wait32(s[c]);
+      if (g % (16 / G) == 0 && g > 0 && g < 64 / G) {
+        const int c = g * G / 16;
+        tmem_wait32(s[c]);
+        if (c < 3) tmem_ld32(ts + (c + 1) * 32, s[c + 1]);
       }
       float2 x[G];
 #pragma unroll
@@ -317,24 +320,28 @@ __device__ __forceinline__ float weights(uint32_t ts, int lim, uint64_t sc2, uin
   return l.x + l.y;
 }
 
-// Within each four lanes: piece q of lane i goes to piece i of lane q.
-__device__ __forceinline__ void transpose4(uint4 (&u)[4]) {
-  const int lane = threadIdx.x & 31;
+// Between lanes 2n and 2n + 1: lane 2n gets both rows' first halves, 2n + 1 their
+// second ones; in: the lane's own row.
+__device__ __forceinline__ void exchange2(uint32_t (&lo)[8], uint32_t (&hi)[8]) {
+  const bool up = threadIdx.x & 1;
 #pragma unroll
-  for (int bit = 1; bit <= 2; bit <<= 1)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint4& lo = u[bit == 1 ? 2 * k : k];
-      uint4& hi = u[bit == 1 ? 2 * k + 1 : k + 2];
-      const bool up = lane & bit;
-      uint4 v = up ? lo : hi;
-      v.x = __shfl_xor_sync(0xffffffffu, v.x, bit);
-      v.y = __shfl_xor_sync(0xffffffffu, v.y, bit);
-      v.z = __shfl_xor_sync(0xffffffffu, v.z, bit);
-      v.w = __shfl_xor_sync(0xffffffffu, v.w, bit);
-      lo = up ? v : lo;
-      hi = up ? hi : v;
-    }
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t v = __shfl_xor_sync(0xffffffffu, up ? lo[i] : hi[i], 1);
+    lo[i] = up ? v : lo[i];
+    hi[i] = up ? hi[i] : v;
+  }
+}
+
+// 32 bytes: one store where their address allows it.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&u)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                 "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  }
 }
 
 // What a CTA works on: one unit of the grid, its own or a taken-over one.
@@ -990,9 +997,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const bool mine = r < my_rows, any = M != NEG || L != 0.0f;
         const float inv = any ? 1.0f / L : 0.0f;
         const int blo = my_nt > 0 ? w.bad_lo : 0x7FFFFFFF, bhi = my_nt > 0 ? w.bad_hi : -1;
-        // after the exchange below this lane stores 16 bytes of rows r / 4 * 4 + q
-        T* out = static_cast<T*>(a.out) + static_cast<int64_t>(my_t0 + (r & ~3)) * a.out_row + my_head * a.out_head +
-                 (lane & 3) * 8;
+        // after the exchange below this lane stores 32 bytes of rows r / 2 * 2 and the
+        // next (16 bytes of four rows, by two exchanges: 512 prompts of 128 took 152
+        // us, so 146)
+        T* out = static_cast<T*>(a.out) + static_cast<int64_t>(my_t0 + (r & ~1)) * a.out_row + my_head * a.out_head +
+                 (lane & 1) * 16;
+        const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | a.out_row * 2 | a.out_head * 2) & 31) == 0;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c, out += 32) {
           uint32_t o[32];
@@ -1000,20 +1010,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tmem_ld32(to + c * 32, o);
             tmem_wait32(o);
           }
-          uint4 u[4];
-          auto pk = [&](int i) {
-            return any ? E::pack(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv) : 0u;
-          };
+          uint32_t u[2][8];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) u[q] = make_uint4(pk(8 * q), pk(8 * q + 2), pk(8 * q + 4), pk(8 * q + 6));
-          transpose4(u);
-          T* at = out;
-#pragma unroll
-          for (int q = 0; q < 4; ++q, at += a.out_row)
-            if ((r & ~3) + q < my_rows) *reinterpret_cast<uint4*>(at) = u[q];
+          for (int i = 0; i < 16; ++i)
+            u[i / 8][i % 8] = any ? E::pack(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
+          exchange2(u[0], u[1]);
+          if ((r & ~1) < my_rows) store32(out, u[0], wide);
+          if ((r | 1) < my_rows) store32(out + a.out_row, u[1], wide);
         }
         if (blo <= bhi) {
-          __syncwarp();  // the row was stored by four lanes
+          __syncwarp();  // the row was stored by two lanes
           if (mine)
             add_non_finite<D, T>(a, cta, blo * kKeys, min(vis, (bhi + 1) * kKeys),
                                  static_cast<T*>(a.out) + static_cast<int64_t>(my_t0 + r) * a.out_row +
