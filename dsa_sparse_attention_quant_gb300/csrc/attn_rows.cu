@@ -128,6 +128,7 @@ struct RowsCfg {
   static constexpr int kOffScan = kOffQ + (MT == 2 ? kRows * kRowBytes : 0);  // the slice, scan scratch
   static constexpr int kSmemBytes = kOffScan + 48 * 4;
   static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(kOffMeta >= 4096, "find_slice's rounds lie in the ring");
 };
 
 // What a stage holds, written by the loader and read when it is consumed.
@@ -190,58 +191,77 @@ struct Slice {
   int n, req;        // of the first token
 };
 
-// Split mode: slice `part` of the flat tile list. All threads call.
+// Split mode: slice `part` of the flat tile list, many tokens counted in rounds of
+// kPer a thread: their metadata's latency is what a round takes (4096 requests of
+// 300 keys, 32/8 heads of 128: 801 us with rounds of one a thread and a second
+// pass over all of them, so 780). All threads call; rounds[kRounds] is scratch.
+constexpr int kPer = 4, kRounds = 1024;
 template <bool SEL>
-__device__ void find_slice(const RowsArgs& a, int part, bool flag, Slice* s, int* scan) {
+__device__ void find_slice(const RowsArgs& a, int part, bool flag, Slice* s, int* scan, int* rounds) {
   const int T = a.n_tokens, tid = threadIdx.x;
-  int tot, n0 = 0, req0 = 0, first0 = 0;  // of token tid, when all tokens fit in one round
+  int tot, n[kPer], req[kPer], tiles[kPer], first = 0;  // of this thread's tokens of the last counted round
   int64_t total = 0;
+  const int per = T <= kThreads ? 1 : kPer;
+  auto count = [&](int c0, bool f) {
+    int sum = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int t = c0 + tid * per + e;
+      n[e] = req[e] = tiles[e] = 0;
+      if (e < per && t < T) {
+        n[e] = token_keys(a, t, &req[e], f);
+        tiles[e] = tiles_of(n[e]);
+      }
+      sum += tiles[e];
+    }
+    first = block_scan_incl(sum, scan, &tot) - sum;
+  };
+  constexpr int R = kThreads * kPer;
   if (SEL) {
     total = static_cast<int64_t>(T) * tiles_of(a.topk);
   } else {
-    for (int c0 = 0; c0 < T; c0 += kThreads) {
-      const int t = c0 + tid;
-      if (t < T) n0 = token_keys(a, t, &req0, flag);
-      const int tiles = t < T ? tiles_of(n0) : 0;
-      first0 = block_scan_incl(tiles, scan, &tot) - tiles;
+    for (int c0 = 0, i = 0; c0 < T; c0 += R, ++i) {
+      count(c0, flag);
+      if (tid == 0 && i < kRounds) rounds[i] = tot;
       total += tot;
     }
+    __syncthreads();
   }
   const int64_t most = (total + a.min_tiles - 1) / a.min_tiles;
-  const int n = static_cast<int>(most < a.slices ? most : a.slices);
-  const int64_t b0 = part < n ? total * part / n : total, b1 = part < n ? total * (part + 1) / n : total;
+  const int use = static_cast<int>(most < a.slices ? most : a.slices);
+  const int64_t b0 = part < use ? total * part / use : total, b1 = part < use ? total * (part + 1) / use : total;
   if (tid == 0) {
     s->all = total;
     s->end = b1;
     s->left = static_cast<int>(b1 - b0);
-    s->in_use = n;
+    s->in_use = use;
   }
   if (b0 < b1) {
     if (SEL) {
       if (tid == 0) {
-        const int per = tiles_of(a.topk);
-        s->t = static_cast<int>(b0 / per);
-        s->kt = static_cast<int>(b0 % per);
+        const int each = tiles_of(a.topk);
+        s->t = static_cast<int>(b0 / each);
+        s->kt = static_cast<int>(b0 % each);
         s->n = a.topk;
         s->req = 0;
       }
     } else {
       int64_t carry = 0;
-      for (int c0 = 0; c0 < T && carry <= b0; c0 += kThreads) {
-        const int t = c0 + tid;
-        if (T > kThreads) {
-          if (t < T) n0 = token_keys(a, t, &req0, false);
-          const int tiles = t < T ? tiles_of(n0) : 0;
-          first0 = block_scan_incl(tiles, scan, &tot) - tiles;
+      int c0 = 0;
+      for (int i = 0; i < kRounds && c0 < T && carry + rounds[i] <= b0; ++i, c0 += R) carry += rounds[i];
+      for (; c0 < T && carry <= b0; c0 += R) {
+        if (T > R) count(c0, false);
+        int64_t at = carry + first;
+#pragma unroll
+        for (int e = 0; e < kPer; at += tiles[e], ++e) {
+          if (at <= b0 && b0 < at + tiles[e]) {
+            s->t = c0 + tid * per + e;
+            s->kt = static_cast<int>(b0 - at);
+            s->n = n[e];
+            s->req = req[e];
+          }
         }
-        const int64_t at = carry + first0;
-        if (t < T && at <= b0 && b0 < at + tiles_of(n0)) {
-          s->t = t;
-          s->kt = static_cast<int>(b0 - at);
-          s->n = n0;
-          s->req = req0;
-        }
-        carry += T > kThreads ? tot : total;
+        carry += tot;
       }
     }
   }
@@ -280,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
   Cursor cur;
   cur.fresh = true;
   if (a.split) {
-    find_slice<SEL>(a, part, blockIdx.x == 0, slice, reinterpret_cast<int*>(slice + 1));
+    find_slice<SEL>(a, part, blockIdx.x == 0, slice, reinterpret_cast<int*>(slice + 1),
+                    reinterpret_cast<int*>(smem));
     cur.left = slice->left;
     if (cur.left == 0) {  // fewer tiles than slices
       if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int2(-1, 0);

@@ -124,6 +124,30 @@ def test_decode_many_short_requests():
     s.check(out, lse)
 
 
+def test_decode_more_tokens_than_one_count():
+    # tokens are counted 512 at a time: long rows among short and empty ones
+    keys = [(53 * i) % 170 for i in range(900)]
+    keys[17], keys[450], keys[899] = 5000, 0, 2100
+    s = Step(22, keys, [1 + i % 3 for i in range(900)], 2, 1, 64, torch.bfloat16)
+    out, lse = dsa.attn_decode(s.batch, s.q, s.k, s.v)
+    s.check(out, lse)
+
+
+def test_decode_half_a_million_rows():
+    # more than 1024 counts of 512; the last three rows of a request see a key
+    s = Step(23, [3] * 540, [1000] * 540, 1, 1, 64, torch.bfloat16)
+    out, lse = dsa.attn_decode(s.batch, s.q, s.k, s.v)
+    out, lse = out.reshape(540, 1000, 64), lse.reshape(540, 1000)
+    assert bool((out[:, :997] == 0).all()) and bool((lse[:, :997] == -math.inf).all())
+    q, k, v = s.q.reshape(540, 1000, 64)[:, 997:].double(), torch.stack(s.kf)[:, :, 0].double(), \
+        torch.stack(s.vf)[:, :, 0].double()
+    score = (q @ k.transpose(1, 2) / 8).masked_fill(torch.ones(3, 3, device=DEV).triu(1).bool(), -math.inf)
+    want = score.softmax(-1) @ v
+    # weights and result in bf16: 2^-8 of max |v| each, and little else
+    assert bool(((out[:, 997:].double() - want).abs() <= 2.1 * 2.0 ** -8 * v.abs().max()).all())
+    assert bool(((lse[:, 997:].double() - score.logsumexp(-1)).abs() <= 1e-4).all())
+
+
 def test_decode_rows_behind_stay_and_scale():
     s = Step(13, [100, 600], [1, 1], 4, 1, 128, torch.float16)
     q = torch.cat([s.q, s.q])
