@@ -14,10 +14,10 @@
 //
 // What bounds it: 4*D operations per (query head, visible pair), the bf16 /
 // fp16 rate of the tensor cores, with 128x128 tiles of S needing one exponential
-// per 4*D operations beside it. Measured: 4 x 8192, 64/8 heads of 128, 2.75 to
-// 2.87 ms (1600 to 1530 TFLOP/s, power-capped; 2 x 8192, 32/8 heads: 1640);
-// 2 x 8192, 32/8 heads of 64, 538 us (1020 TFLOP/s): there a tile pair's
-// exponentials and the rest of its softmax, 2300 cycles, outlast its MMAs, 1024.
+// per 4*D operations beside it. Measured: 4 x 8192, 64/8 heads of 128, 2.65 to
+// 2.8 ms (1660 to 1570 TFLOP/s, power-capped; 2 x 8192, 32/8 heads: 1730);
+// 2 x 8192, 32/8 heads of 64, 502 us (1094 TFLOP/s): there a tile pair's
+// exponentials and the rest of its softmax, 2200 cycles, outlast its MMAs, 1024.
 // Short prompts are a chain per unit (scores, weights, P V, the store), 9000
 // cycles: 512 prompts of 128, 16/2 heads of 128, 144 us.
 //
@@ -57,13 +57,9 @@ constexpr int kRowsTile = 128;  // query rows per tile
 constexpr int kKeys = 128;      // keys per tile
 constexpr int kSoftWarps = 8;
 // Three warpgroups, the third with two idle warps: registers move between
-// warpgroups. Launched with 168 a thread (384 * 168 = 64512), the softmax
-// warpgroups take 208 (a row of S) and the third keeps 88: 256 * 208 + 128 * 88
-// = 64512.
+// warpgroups (PromptCfg), from 168 a thread at launch (384 * 168 = 64512).
 constexpr int kPromptThreads = 32 * (kSoftWarps + 4);
 constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-constexpr int kSoftRegs = 208, kIssueRegs = 88;
-static_assert(32 * kSoftWarps * kSoftRegs + 128 * kIssueRegs <= kPromptThreads * 168, "register split");
 
 template <int D>
 struct PromptCfg {
@@ -83,6 +79,10 @@ struct PromptCfg {
   static constexpr int kOffNext = (kOffMisc + 16 + 15) / 16 * 16;  // the 16 bytes of a taken-over CTA's index
   static constexpr int kOffCta = kOffNext + 16;
   static constexpr int kSmemBytes = kOffCta + 2 * 96 + 1024;  // + slack to align the base to 1024
+  // Registers of the softmax warps (a row of S) and of the others. D = 64 in 208/88:
+  // 508 us for 501 at 2 x 8192, 32/8 heads; D = 128 in 200/104: 651 us for 638.
+  static constexpr int kSoftRegs = D == 128 ? 208 : 200, kIssueRegs = D == 128 ? 88 : 104;
+  static_assert(32 * kSoftWarps * kSoftRegs + 128 * kIssueRegs <= kPromptThreads * 168, "register split");
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kO = kRing ? 3 * kKeys : 2 * kKeys;  // first column of O
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   };
 
   if (warp >= kSoftWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
     if (warp == kTmaWarp) {
       // --------------------------------------------------------------- TMA
       int seq = 0;       // ring stages filled so far
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     // ------------------------------------------------------------- softmax
     // A row per thread, the row's TMEM lane in the quarter that its warp may read.
     const int x = warp >> 2;
@@ -889,8 +889,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         // The weights by the reference at hand, without looking for the maximum
         // first: only where a row has none yet, or its weights come out too large
         // (or not a number), the tile's is taken and the weights once more. A
-        // row's decision is its own: no other row has a part in its bits.
-        if (fresh) {  // a first reference: the maximum of the columns in front
+        // row's decision is its own: no other row has a part in its bits. The way
+        // of most tiles is short and in one piece, the rest out of its way: with
+        // all in one loop, 2 x 8192, 32/8 heads took 652 us (D = 128) and 538
+        // (D = 64), so 638 and 508.
+        if (__builtin_expect(fresh, 0)) {  // a first reference: the maximum of the columns in front
           uint32_t s[32];
           tmem_ld32(ts, s);
           tmem_wait32(s);
@@ -904,57 +907,65 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (M == NEG) M = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2 - E::kHead;
           fresh = __any_sync(0xffffffffu, M == NEG);
         }
-        bool raise = M == NEG && lim > 0;
         uint32_t p[2][32];
         float add;
-        for (int attempt = __any_sync(0xffffffffu, raise) ? 1 : 0;; ++attempt) {
-          if (attempt > 0) {
-            float top = NEG;
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              uint32_t s[2][32];
-              tmem_ld32(ts + c * 64, s[0]);
-              tmem_ld32(ts + c * 64 + 32, s[1]);
-              tmem_wait32(s[0]);
-              tmem_wait32(s[1]);
-              const int end = j < edge_from ? kKeys : lim - c * 64;
-              float mx[8];
-#pragma unroll
-              for (int i = 0; i < 64; ++i) {
-                const float v = i < end ? __uint_as_float(s[i / 32][i % 32]) : NEG;
-                mx[i & 7] = i < 8 ? v : fmaxf(mx[i & 7], v);
-              }
-              top = fmaxf(top, fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                     fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))));
-            }
-            const float n = raise ? fmaxf(M, top * a.scale_log2 - E::kHead) : M;
-            const float f = !raise ? 1.0f : M == NEG ? 0.0f : pex2(M - n);
-            M = n;
-            L *= f;
-            fresh = __any_sync(0xffffffffu, M == NEG);
-            if (j > 0) {
-              if (C::kRing && !wait_o(j - 1)) {  // (with one buffer, its MMAs precede this tile's scores)
-                ok = false;
-                break;
-              }
-#pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(to + c * 32, o);
-                tmem_wait32(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st32(to + c * 32, o);
-              }
-            }
-          }
-          const float ref = M == NEG ? 0.0f : M;
-          const uint64_t sc2 = pack_f32x2(a.scale_log2, a.scale_log2), ref2 = pack_f32x2(-ref, -ref);
-          add = j >= edge_from ? weights<T, true>(ts, lim, sc2, ref2, p) : weights<T, false>(ts, lim, sc2, ref2, p);
-          raise = !raise && !(add <= E::kMaxSum);
-          if (attempt == 2 || !__any_sync(0xffffffffu, raise)) break;
+        const bool whole = j < edge_from && !fresh;
+        bool done = false;
+        if (__builtin_expect(whole, 1)) {
+          add = weights<T, false>(ts, lim, pack_f32x2(a.scale_log2, a.scale_log2), pack_f32x2(-M, -M), p);
+          done = __all_sync(0xffffffffu, add <= E::kMaxSum);
         }
-        if (!ok) break;
+        if (__builtin_expect(!done, 0)) {
+          bool raise = whole ? !(add <= E::kMaxSum) : M == NEG && lim > 0;
+          for (int attempt = __any_sync(0xffffffffu, raise) ? 1 : 0;; ++attempt) {
+            if (attempt > 0) {
+              float top = NEG;
+#pragma unroll 1
+              for (int c = 0; c < 2; ++c) {
+                uint32_t s[2][32];
+                tmem_ld32(ts + c * 64, s[0]);
+                tmem_ld32(ts + c * 64 + 32, s[1]);
+                tmem_wait32(s[0]);
+                tmem_wait32(s[1]);
+                const int end = j < edge_from ? kKeys : lim - c * 64;
+                float mx[8];
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                  const float v = i < end ? __uint_as_float(s[i / 32][i % 32]) : NEG;
+                  mx[i & 7] = i < 8 ? v : fmaxf(mx[i & 7], v);
+                }
+                top = fmaxf(top, fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                       fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))));
+              }
+              const float n = raise ? fmaxf(M, top * a.scale_log2 - E::kHead) : M;
+              const float f = !raise ? 1.0f : M == NEG ? 0.0f : pex2(M - n);
+              M = n;
+              L *= f;
+              fresh = __any_sync(0xffffffffu, M == NEG);
+              if (j > 0) {
+                if (C::kRing && !wait_o(j - 1)) {  // (with one buffer, its MMAs precede this tile's scores)
+                  ok = false;
+                  break;
+                }
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  uint32_t o[32];
+                  tmem_ld32(to + c * 32, o);
+                  tmem_wait32(o);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st32(to + c * 32, o);
+                }
+              }
+            }
+            const float ref = M == NEG ? 0.0f : M;
+            const uint64_t sc2 = pack_f32x2(a.scale_log2, a.scale_log2), ref2 = pack_f32x2(-ref, -ref);
+            add = weights<T, true>(ts, lim, sc2, ref2, p);
+            raise = !raise && !(add <= E::kMaxSum);
+            if (attempt == 2 || !__any_sync(0xffffffffu, raise)) break;
+          }
+          if (!ok) break;
+        }
         L += add;
         if (C::kRing && j > 1) {  // P V of the tile before the previous one: V was read (mostly long ago)
           ok = wait_o(j - 2);

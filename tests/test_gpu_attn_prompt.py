@@ -253,6 +253,21 @@ def test_prompt_bad_metadata_is_flagged():
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("d", [64, 128])
+def test_prompt_rows_bits_are_their_own(d, dtype):
+    # some rows' weights come out too large in a later tile: the other rows' bits stay
+    p = Prompts(24, [900], [900], 2, 1, d, dtype, False, gap=0)
+    want, wlse = p.run()
+    rows = [500, 577, 700, 899]
+    p.q[rows] *= 60
+    out, lse = p.run()
+    rest = [r for r in range(900) if r not in rows]
+    assert torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], wlse[rest])
+    assert not torch.equal(out[rows], want[rows])
+    p.check(out, lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
 def test_prompt_uneven_pairs_of_tiles(d, dtype):
     # token tiles in pairs of 2, 1 and unequal numbers of key tiles, several pairs
     # a CTA; scores that rise over the keys, so that references move in any of them
