@@ -47,7 +47,7 @@ int check_attn(const DsaAttn* at, const DsaKv& kv, int64_t rows, DsaAttn* out) {
   if (rows == 1) out->q_row_stride = out->out_row_stride = kv.head_dim;
   for (int64_t s : {out->q_row_stride, out->q_head_stride, out->out_row_stride, out->out_head_stride})
     if (!stride_ok(s, kv.head_dim)) return DSA_EINVAL;
-  if (std::isinf(at->scale) && at->scale > 0) return DSA_EINVAL;
+  if (!std::isfinite(at->scale * 1.4426950408889634f) && !(at->scale < 0)) return DSA_EINVAL;
   if (!(at->scale > 0.0f)) out->scale = kv.head_dim == 128 ? 0.08838834764831845f : 0.125f;
   return DSA_OK;
 }
@@ -446,7 +446,7 @@ int dsa_pages_copy(const DsaCacheDesc* caches, int32_t n_caches, int64_t num_blo
                    const int32_t* dst, int32_t n, void* ws, size_t ws_bytes, int32_t* dev_err, dsa_stream_t stream) {
   int st = check_caches(caches, n_caches);
   if (st != DSA_OK) return st;
-  if (num_blocks < 1 || num_blocks > kMaxBlocks || n < 0) return DSA_EINVAL;
+  if (num_blocks < 1 || num_blocks > kMaxBlocks || n < 0 || n > (1 << 30)) return DSA_EINVAL;
   if (n == 0) return DSA_OK;
   if (!src || !dst || !ws || !aligned16(ws)) return DSA_EINVAL;
   const PagesWs w = pages_carve(num_blocks, n, ws);

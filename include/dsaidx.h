@@ -395,7 +395,8 @@ DSA_API int dsa_kv_write(const void *k, int64_t k_row_stride, int64_t k_head_str
  *            least head_dim (that of an axis of one element is not used)
  *   lse      device fp32 [T, num_heads] contiguous, or NULL
  *   num_heads  a multiple of kv->num_kv_heads
- *   scale    <= 0 selects head_dim^-0.5 */
+ *   scale    <= 0 selects head_dim^-0.5; NaN, and a scale that overflows fp32
+ *            when multiplied by log2(e), is refused */
 typedef struct DsaAttn {
   const void *q;
   int64_t q_row_stride, q_head_stride;
@@ -468,7 +469,8 @@ DSA_API int dsa_attn_prompt(const DsaBatch *batch, const DsaKv *kv, const int32_
  *   block_table  device int32 [n_rows, bt_stride]
  *   seq_lens     device int32 [n_rows]: ceil(len/64) entries of a row count
  *   caches       host array [n_caches] (0 to 1024 of them): page p is
- *                page_bytes bytes (a multiple of 16) at base + p*page_stride
+ *                page_bytes bytes (a multiple of 16, at most 2^30) at base +
+ *                p*page_stride
  *                (device, 16-byte aligned; stride a multiple of 16, at least
  *                page_bytes)
  *   ws           device scratch, 16-byte aligned, of dsa_pages_workspace_size()
@@ -491,7 +493,7 @@ typedef struct DsaCacheDesc {
 DSA_API size_t dsa_pages_workspace_size(int64_t num_blocks, int32_t n);
 
 /* Copy page src[i] over page dst[i] in every cache, for i < n (device int32
- * lists). A pair with a -1 is padding. A page may be the source of many pairs
+ * lists, n at most 2^30). A pair with a -1 is padding. A page may be the source of many pairs
  * and the destination of one: of pairs with one destination the first stands,
  * a pair whose destination is also a source is skipped, and both flag
  * DSA_DEVERR_PAGE_STATE; pages outside the pool are skipped and flag

@@ -76,6 +76,12 @@ def test_attention_descriptions_refused(bad):
         assert call(a=attn(**bad)) == EINVAL
 
 
+@pytest.mark.parametrize("scale", [float("nan"), 3e38])
+def test_scales_refused(scale):
+    for call in (decode, prompt, selected):
+        assert call(a=attn(scale=scale)) == EINVAL
+
+
 def test_batches_refused():
     for bad in (dict(num_reqs=-1), dict(num_decodes=4), dict(num_decode_tokens=13), dict(num_tokens=-1),
                 dict(num_reqs=0, num_decodes=0), dict(max_seq_len=-1), dict(query_start_loc=None), dict(seq_lens=None),
