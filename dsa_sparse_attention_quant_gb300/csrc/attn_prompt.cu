@@ -672,8 +672,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if constexpr (C::kRing) {
             // Steps (tile x, key tile j) in turn, each: P V, then Q K^T of the third
             // step after it, into the buffer just read. Stages and parities are kept
-            // as running values: this warp's instructions are between one step's
-            // MMAs and the next one's.
+            // as running values, and a step's MMAs issued in one piece: this warp's
+            // instructions are between a step's weights and the scores that follow
+            // (8 x 2048, 32/8 heads: 172 us with two pieces, so 166; 188 with every
+            // step by next_scores).
             auto bump = [&](int& st, uint32_t& par) {
               st += 2;
               if (st >= S) st -= S, par ^= 1;
@@ -690,6 +692,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               values(x, vst, pbuf, j > 0);
               on[x] ^= 1;
               if (++pbuf == 3) pbuf = 0, ppar ^= 1;
+            };
+            auto step_both = [&](int x, int j) {  // values of (x, j), then scores of the other tile
+              const int y = x ^ 1;
+              ok = ok && wait(&pfull[pbuf], ppar);
+              if (!ok) return;
+              tc_fence_after();
+              const uint32_t vd = mnmajor_lo(kv0 + vst * C::kTileBytes), kd = kmajor_lo(kv0 + kst * C::kTileBytes);
+              const uint32_t sp = tmem + pbuf * kKeys, qy = qd + ((y * C::kTileBytes) >> 4);
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                  mma_f16_ts(tmem + C::kO + x * D, sp + k * 8, vd + ((k * 16 * 128) >> 4), kIdO, j > 0 || k > 0);
+                mma_commit(&ofull[x + 2 * on[x]]);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                  const uint32_t off = ((k / 4) * C::kColBytes + (k % 4) * 32) >> 4;
+                  mma_f16_ss(sp, qy + off, kd + off, kIdS, k > 0);
+                }
+                mma_commit(&sfull[y * 3 + sn[y]]);
+              }
+              __syncwarp();
+              on[x] ^= 1;
+              sn[y] = sn[y] == 2 ? 0 : sn[y] + 1;
+              if (++pbuf == 3) pbuf = 0, ppar ^= 1;
+              sbuf = pbuf;
             };
             int qj = 0, j = 0;  // key tiles of the next scores and P V
             bool q1 = false;    // the next scores are tile 1's
@@ -720,13 +747,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int i = 0; i < 3; ++i) next_scores();
             while (j < n_tiles && ok) {
               ok = wait(&full[vst], vpar);
-              if (j + 3 < min(nt[0], nt[1])) {  // both tiles go on: scores of (1, j + 1) and (0, j + 2)
-                if (ok) step_values(0, j);
-                if (ok) step_scores(1);
+              if (j + 2 < nt[0] && j + 1 < nt[1]) {  // both tiles go on: scores of (1, j + 1) and (0, j + 2)
+                step_both(0, j);
+                if (j + 2 == nt[1]) release(&qempty[1]);
                 bump(kst, kpar);
                 ok = ok && wait(&full[kst], kpar);
-                if (ok) step_values(1, j);
-                if (ok) step_scores(0);
+                step_both(1, j);
+                if (j + 3 == nt[0]) release(&qempty[0]);
                 ++qj;
               } else {
 #pragma unroll
@@ -921,21 +948,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (attempt > 0) {
               float top = NEG;
 #pragma unroll 1
-              for (int c = 0; c < 2; ++c) {
-                uint32_t s[2][32];
-                tmem_ld32(ts + c * 64, s[0]);
-                tmem_ld32(ts + c * 64 + 32, s[1]);
-                tmem_wait32(s[0]);
-                tmem_wait32(s[1]);
-                const int end = j < edge_from ? kKeys : lim - c * 64;
-                float mx[8];
+              for (int c = 0; c < 4; ++c) {
+                uint32_t s[32];
+                tmem_ld32(ts + c * 32, s);
+                tmem_wait32(s);
+                const int end = lim - c * 32;
+                float mx[4];
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                  const float v = i < end ? __uint_as_float(s[i / 32][i % 32]) : NEG;
-                  mx[i & 7] = i < 8 ? v : fmaxf(mx[i & 7], v);
+                for (int i = 0; i < 32; ++i) {
+                  const float v = i < end ? __uint_as_float(s[i]) : NEG;
+                  mx[i & 3] = i < 4 ? v : fmaxf(mx[i & 3], v);
                 }
-                top = fmaxf(top, fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                       fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))));
+                top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
               }
               const float n = raise ? fmaxf(M, top * a.scale_log2 - E::kHead) : M;
               const float f = !raise ? 1.0f : M == NEG ? 0.0f : pex2(M - n);
