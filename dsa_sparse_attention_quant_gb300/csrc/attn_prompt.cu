@@ -14,10 +14,10 @@
 //
 // What bounds it: 4*D operations per (query head, visible pair), the bf16 /
 // fp16 rate of the tensor cores, with 128x128 tiles of S needing one exponential
-// per 4*D operations beside it. Measured: 4 x 8192, 64/8 heads of 128, 2.65 to
-// 2.8 ms (1660 to 1570 TFLOP/s, power-capped; 2 x 8192, 32/8 heads: 1730);
-// 2 x 8192, 32/8 heads of 64, 502 us (1094 TFLOP/s): there a tile pair's
-// exponentials and the rest of its softmax, 2200 cycles, outlast its MMAs, 1024.
+// per 4*D operations beside it. Measured: 4 x 8192, 64/8 heads of 128, 2.58 to
+// 2.79 ms (1705 to 1580 TFLOP/s, power-capped; 2 x 8192, 32/8 heads: 1730);
+// 2 x 8192, 32/8 heads of 64, 493 us (1115 TFLOP/s): there a tile pair's
+// exponentials and the rest of its softmax, 2100 cycles, outlast its MMAs, 1024.
 // Short prompts are a chain per unit (scores, weights, P V, the store), 9000
 // cycles: 512 prompts of 128, 16/2 heads of 128, 144 us.
 //
@@ -79,8 +79,8 @@ struct PromptCfg {
   static constexpr int kOffNext = (kOffMisc + 16 + 15) / 16 * 16;  // the 16 bytes of a taken-over CTA's index
   static constexpr int kOffCta = kOffNext + 16;
   static constexpr int kSmemBytes = kOffCta + 2 * 96 + 1024;  // + slack to align the base to 1024
-  // Registers of the softmax warps (a row of S) and of the others. D = 64 in 208/88:
-  // 508 us for 501 at 2 x 8192, 32/8 heads; D = 128 in 200/104: 651 us for 638.
+  // Registers of the softmax warps (a row of S) and of the others. At 2 x 8192, 32/8
+  // heads: D = 64 with 208/88 508 us, so 501; D = 128 with 200/104 651 us, so 638.
   static constexpr int kSoftRegs = D == 128 ? 208 : 200, kIssueRegs = D == 128 ? 88 : 104;
   static_assert(32 * kSoftWarps * kSoftRegs + 128 * kIssueRegs <= kPromptThreads * 168, "register split");
   static constexpr uint32_t kTmemCols = 512;
