@@ -174,6 +174,7 @@ def attn_decode(batch, q, k_cache, v_cache, scale: float = 0.0, out=None, lse=No
     [tokens, heads, head_dim], over their requests' pages. Returns (out, lse);
     the other rows of a passed ``out`` and ``lse`` stay as they were."""
     kv, kv_heads, d, dtype = _kv(k_cache, v_cache)
+    _here(batch.seq_lens, "the batch")
     at, out, lse, heads = _attn(q, out, lse, kv_heads, d, dtype, scale, 0, batch.num_decode_tokens, stream)
     ws = _scratch(ws, lambda: attn_decode_workspace_size(batch, heads, kv_heads, d), q.device, stream)
     st = load().dsa_attn_decode(ctypes.byref(batch.c), kv, at, ws.data_ptr(), ws.numel(), _err(dev_err), _on(stream))
@@ -212,6 +213,7 @@ def attn_prompt(batch, q, k, v, scale: float = 0.0, kv_start=None, out=None, lse
     where key s of request r is row kv_start[r] + s. Returns (out, lse); the
     other rows of a passed ``out`` and ``lse`` stay as they were."""
     kv, kv_heads, d, dtype = _kv(k, v, packed=kv_start is not None)
+    _here(batch.seq_lens, "the batch")
     start = None
     if kv_start is not None:
         start = _dense(kv_start, "kv_start", torch.int32).data_ptr()

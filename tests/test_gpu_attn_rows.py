@@ -124,6 +124,14 @@ def test_decode_many_short_requests():
     s.check(out, lse)
 
 
+def test_batch_elsewhere_is_refused():
+    s = Step(25, [100], [1], 2, 1, 64, torch.bfloat16)
+    s.batch.seq_lens = s.batch.seq_lens.cpu()
+    for call in (dsa.attn_decode, dsa.attn_prompt):
+        with pytest.raises(dsa.DsaError, match="the batch"):
+            call(s.batch, s.q, s.k, s.v)
+
+
 def test_decode_more_tokens_than_one_count():
     # tokens are counted 512 at a time: long rows among short and empty ones
     keys = [(53 * i) % 170 for i in range(900)]
