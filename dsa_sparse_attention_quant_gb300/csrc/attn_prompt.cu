@@ -459,6 +459,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // launched while the stream's previous kernel drains: nothing is read or written before it has ended
 
   // The next unit for a warp that follows the TMA warp, or false at the end.
   int units = 0;
@@ -1080,8 +1081,8 @@ cudaError_t launch(const PromptArgs& a, const CUtensorMap* mq, const CUtensorMap
   auto* fn = attn_prompt_kernel<D, T>;
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(fn), PromptCfg<D>::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
-  fn<<<a.head_units * a.tile_units, kPromptThreads, PromptCfg<D>::kSmemBytes, stream>>>(*mq, *mk, *mv, a);
-  return cudaGetLastError();
+  return launch_pdl(fn, dim3(a.head_units * a.tile_units), dim3(kPromptThreads), PromptCfg<D>::kSmemBytes, stream, *mq,
+                    *mk, *mv, a);
 }
 
 }  // namespace

@@ -24,6 +24,7 @@ constexpr int kWriteThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_constant__ KvWriteArgs a) {
+  pdl_wait();
   constexpr int CH = D / 8;
   constexpr int U = 4;
   const int lane = threadIdx.x & 31;
@@ -126,6 +127,7 @@ constexpr int kForkThreads = 1024;
 __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_constant__ PagesArgs p) {
   __shared__ int scan[33];
   const int tid = threadIdx.x;
+  pdl_wait();
   const int64_t most = p.bt_stride * kBlock;
   // lengths before any child is written
   for (int i = tid; i < p.n; i += kForkThreads) {
@@ -242,6 +244,7 @@ __global__ void __launch_bounds__(kCopyThreads) fork_move_kernel(const __grid_co
 // A CTA per row. Each table entry is taken by an exchange, so a row named
 // twice gives its pages back once.
 __global__ void __launch_bounds__(256) pages_free_kernel(const __grid_constant__ PagesArgs p) {
+  pdl_wait();
   const int32_t row = p.a[blockIdx.x];
   if (row < 0 || row >= p.n_rows) {
     if (threadIdx.x == 0) flag_error(p.err, DSA_DEVERR_SEQ_RANGE);
@@ -284,6 +287,7 @@ __device__ __forceinline__ uint32_t live_bits(const PagesArgs& p, int64_t at) {
 
 __global__ void __launch_bounds__(kScanThreads) compact_count_kernel(const __grid_constant__ PagesArgs p) {
   __shared__ int scan[33];
+  pdl_wait();
   const uint32_t bits = live_bits(p, static_cast<int64_t>(blockIdx.x) * kPageChunk + threadIdx.x * kPerThread);
   int tot;
   block_scan_incl(__popc(bits), scan, &tot);
@@ -389,10 +393,8 @@ cudaError_t launch_kv_write(const KvWriteArgs& a, int head_dim, int num_sms, cud
   const int64_t cap = static_cast<int64_t>(num_sms) * 64;
   if (grid > cap) grid = cap;
   if (head_dim == 128)
-    kv_write_kernel<128><<<static_cast<unsigned>(grid), kWriteThreads, 0, stream>>>(a);
-  else
-    kv_write_kernel<64><<<static_cast<unsigned>(grid), kWriteThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+    return launch_pdl(kv_write_kernel<128>, dim3(static_cast<unsigned>(grid)), dim3(kWriteThreads), 0, stream, a);
+  return launch_pdl(kv_write_kernel<64>, dim3(static_cast<unsigned>(grid)), dim3(kWriteThreads), 0, stream, a);
 }
 
 cudaError_t launch_pages_copy(const PagesArgs& p, const CacheList* lists, int n_lists, int num_sms,
@@ -413,8 +415,7 @@ cudaError_t launch_pages_copy(const PagesArgs& p, const CacheList* lists, int n_
 
 cudaError_t launch_pages_fork(const PagesArgs& p, const CacheList* lists, int n_lists, int num_sms,
                               cudaStream_t stream) {
-  fork_plan_kernel<<<1, kForkThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kForkThreads), 0, stream, p);
   if (e != cudaSuccess) return e;
   for (int i = 0; i < n_lists; ++i) {
     const int tables = i == 0 ? (p.n < num_sms ? p.n : num_sms) : 0;
@@ -427,15 +428,13 @@ cudaError_t launch_pages_fork(const PagesArgs& p, const CacheList* lists, int n_
 }
 
 cudaError_t launch_pages_free(const PagesArgs& p, cudaStream_t stream) {
-  pages_free_kernel<<<p.n, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(pages_free_kernel, dim3(p.n), dim3(256), 0, stream, p);
 }
 
 cudaError_t launch_pages_compact(const PagesArgs& p, const CacheList* lists, int n_lists, int num_sms,
                                  cudaStream_t stream) {
   const int chunks = static_cast<int>((p.num_blocks + kPageChunk - 1) / kPageChunk);
-  compact_count_kernel<<<chunks, kScanThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_pdl(compact_count_kernel, dim3(chunks), dim3(kScanThreads), 0, stream, p);
   if (e == cudaSuccess) e = launch_pdl(compact_rank_kernel, dim3(chunks), dim3(kScanThreads), 0, stream, p);
   if (e != cudaSuccess) return e;
   const int64_t entries = static_cast<int64_t>(p.n_rows) * p.bt_stride;
