@@ -7,9 +7,11 @@
 // first in the order of the request list, and the k-th page that compaction
 // moves goes to the k-th hole. The byte moves are bound by HBM, one read and
 // one write of every moved page; the bookkeeping by a few dependent reads.
-// Measured: 32768 rows of 8 x 128 written in 43 us (6.25 TB/s, read and write);
-// 0.5 GB of pages moved by a compaction over 8 caches in 175 us (5.7 TB/s with
-// the plan); 64 forks over 16 caches 12 us on the GPU, about 28 us of host time.
+// Measured: 32768 rows of 8 x 128 written in 40 to 42 us (6.5 TB/s, read and
+// write); 0.5 GB of pages moved by a compaction over 8 caches in 171 us (5.8 TB/s
+// with the plan); 64 forks over 16 caches 12 us on the GPU, about 28 us of host
+// time. Each call's first kernel is launched while the stream's previous one
+// drains (rows 44.2 -> 41.6 us).
 #include "attn.h"
 #include "common.cuh"
 
