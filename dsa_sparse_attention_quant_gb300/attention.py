@@ -9,6 +9,7 @@ stream's memory. Every call is asynchronous.
 from __future__ import annotations
 
 import ctypes
+import math
 import struct
 
 import torch
@@ -89,18 +90,21 @@ def _kv(k, v, packed=False):
     return _KV.pack(k.data_ptr(), v.data_ptr(), code, heads, d, n, *ks[:3], *vs[:3]), heads, d, dtype
 
 
-def _made(stream, shape, dtype, device, covered):
-    """A result made here, for the stream it is written on; zeros where the call
-    does not write every row."""
+def _made(stream, shape, dtype, device, rest):
+    """A result made here, for the stream it is written on; ``rest`` fills the
+    rows that the call does not write (None: it writes every row)."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return _made(None, shape, dtype, device, covered)
-    return (torch.empty if covered else torch.zeros)(shape, dtype=dtype, device=device)
+            return _made(None, shape, dtype, device, rest)
+    if rest is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.full(shape, rest, dtype=dtype, device=device)
 
 
-def _attn(q, out, lse, kv_heads, d, dtype, scale, first, rows, stream):
-    """(C description, out, lse, heads) for a call that writes rows [first,
-    rows), allocating what is missing."""
+def _attn(q, out, lse, kv_heads, d, dtype, scale, rows, every, stream):
+    """(C description, out, lse, heads) for a call that reaches rows [0, rows)
+    and writes every row or only some, allocating what is missing: rows that are
+    not written are empty ones (0, -infinity)."""
     shape = _here(q, "q", dtype).shape
     if len(shape) != 3 or shape[2] != d:
         raise DsaError(f"q must be [tokens, heads, {d}]")
@@ -110,13 +114,13 @@ def _attn(q, out, lse, kv_heads, d, dtype, scale, first, rows, stream):
     if heads == 0 or kv_heads == 0 or heads % kv_heads:
         raise DsaError(f"{heads} query heads cannot share {kv_heads} KV heads")
     if out is None:
-        out = _made(stream, shape, dtype, q.device, first == 0 and rows == n)
+        out = _made(stream, shape, dtype, q.device, None if every else 0.0)
     elif not isinstance(out, torch.Tensor) or out.get_device() != q.get_device() or out.dtype is not dtype \
             or out.shape != shape:
         _here(out, "out", dtype)
         raise DsaError("out must have q's shape")
     if lse is None:
-        lse = _made(stream, shape[:2], torch.float32, q.device, first == 0 and rows == n)
+        lse = _made(stream, shape[:2], torch.float32, q.device, None if every else -math.inf)
     elif _dense(lse, "lse", torch.float32).shape != shape[:2]:
         raise DsaError("lse must be [tokens, heads]")
     qs, os = q.stride(), out.stride()
@@ -172,10 +176,12 @@ def attn_decode(batch, q, k_cache, v_cache, scale: float = 0.0, out=None, lse=No
                 stream=None):
     """Attention of the batch's decode tokens, rows [0, num_decode_tokens) of q
     [tokens, heads, head_dim], over their requests' pages. Returns (out, lse);
-    the other rows of a passed ``out`` and ``lse`` stay as they were."""
+    the other rows of a passed ``out`` and ``lse`` stay as they were, of one made
+    here they are 0 and -infinity."""
     kv, kv_heads, d, dtype = _kv(k_cache, v_cache)
     _here(batch.seq_lens, "the batch")
-    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, dtype, scale, 0, batch.num_decode_tokens, stream)
+    n = batch.num_decode_tokens
+    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, dtype, scale, n, n == q.shape[0], stream)
     ws = _scratch(ws, lambda: attn_decode_workspace_size(batch, heads, kv_heads, d), q.device, stream)
     st = load().dsa_attn_decode(ctypes.byref(batch.c), kv, at, ws.data_ptr(), ws.numel(), _err(dev_err), _on(stream))
     _check(st, "dsa_attn_decode")
@@ -196,7 +202,7 @@ def attn_selected(q, k_cache, v_cache, physical, scale: float = 0.0, out=None, l
     if len(shape) != 2 or shape[1] < 1:
         raise DsaError("physical must be [tokens, topk]")
     n, topk = shape
-    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, dtype, scale, 0, n, stream)
+    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, dtype, scale, n, True, stream)
     if q.shape[0] != n:
         raise DsaError(f"q has {q.shape[0]} rows, physical {n}")
     ws = _scratch(ws, lambda: attn_selected_workspace_size(n, topk, heads, kv_heads, d), q.device, stream)
@@ -211,7 +217,10 @@ def attn_prompt(batch, q, k, v, scale: float = 0.0, kv_start=None, out=None, lse
     num_tokens) of q [tokens, heads, head_dim]. k and v are the paged caches, or
     with ``kv_start`` (int32 [num_reqs]) packed rows [rows, heads, head_dim]
     where key s of request r is row kv_start[r] + s. Returns (out, lse); the
-    other rows of a passed ``out`` and ``lse`` stay as they were."""
+    other rows, and those that are no request's (behind query_start_loc's end, of
+    a request that is refused), stay as they were in a passed ``out`` and
+    ``lse``. Which they are is known on the GPU alone, so results made here are
+    filled with 0 and -infinity first: passing both saves that."""
     kv, kv_heads, d, dtype = _kv(k, v, packed=kv_start is not None)
     _here(batch.seq_lens, "the batch")
     start = None
@@ -219,7 +228,7 @@ def attn_prompt(batch, q, k, v, scale: float = 0.0, kv_start=None, out=None, lse
         start = _dense(kv_start, "kv_start", torch.int32).data_ptr()
         if kv_start.numel() < batch.num_reqs:
             raise DsaError("kv_start needs an entry per request")
-    at, out, lse, _ = _attn(q, out, lse, kv_heads, d, dtype, scale, batch.num_decode_tokens, batch.num_tokens, stream)
+    at, out, lse, _ = _attn(q, out, lse, kv_heads, d, dtype, scale, batch.num_tokens, False, stream)
     st = load().dsa_attn_prompt(ctypes.byref(batch.c), kv, start, at, _err(dev_err), _on(stream))
     _check(st, "dsa_attn_prompt")
     return out, lse

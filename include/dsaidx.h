@@ -446,17 +446,20 @@ DSA_API int dsa_attn_selected(const DsaKv *kv, const DsaAttn *attn, const int32_
 /* The prefill tokens of a batch, rows [num_decode_tokens, num_tokens): whole
  * prompts or chunks of them, packed one request after the other. Query token i
  * of request r sees keys [0, seq_lens[r] - q_len[r] + i]. Other rows are left
- * as they were.
+ * as they were: the decode tokens', and those that are no request's because
+ * num_tokens is larger than query_start_loc[num_reqs] (a padded batch, not
+ * flagged) or because their request is refused below.
  *   kv_start  NULL: the keys are in the paged cache, through the block table
  *             (kv->num_blocks must equal batch->num_blocks);
  *             else device int32 [num_reqs]: K and V are packed rows [rows,
  *             heads, head_dim] (kv->num_blocks = rows, the slot stride is the
  *             row stride, no page stride) and key s of request r is row
  *             kv_start[r] + s; the block table is not used
- * Flags: DSA_DEVERR_SEQ_RANGE (negative q_len, seq_len negative or beyond the
- * block-table row, max_seq_len or the packed rows: the request's rows are
- * empty), DSA_DEVERR_BLOCK_RANGE (the rows that see the page are unspecified),
- * DSA_DEVERR_TIMEOUT. No workspace. */
+ * Flags: DSA_DEVERR_SEQ_RANGE (negative q_len, query tokens before
+ * num_decode_tokens or beyond num_tokens: the request is refused, none of its
+ * rows is written; seq_len negative or beyond the block-table row, max_seq_len
+ * or the packed rows: its rows are empty), DSA_DEVERR_BLOCK_RANGE (the rows
+ * that see the page are unspecified), DSA_DEVERR_TIMEOUT. No workspace. */
 DSA_API int dsa_attn_prompt(const DsaBatch *batch, const DsaKv *kv, const int32_t *kv_start,
                     const DsaAttn *attn, int32_t *dev_err, dsa_stream_t stream);
 
