@@ -46,7 +46,8 @@
 // V rows a tile holds but a row may not see meet P = 0 in the MMA, and 0 * NaN
 // is NaN: in the tiles cut by the causal edge or by the sequence's end, the
 // softmax warps first clear the rows behind the sequence and any non-finite V
-// element; rows that do see such an element get it added back at the end.
+// element; rows that do see such an element get it added back at the end, but
+// for rows whose scores are all -infinity.
 #include "attn.h"
 #include "common.cuh"
 
@@ -1057,7 +1058,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         if (blo <= bhi) {
           __syncwarp();  // the row was stored by two lanes
-          if (mine)
+          if (mine && any)
             add_non_finite<D, T>(a, cta, blo * kKeys, min(vis, (bhi + 1) * kKeys),
                                  static_cast<T*>(a.out) + static_cast<int64_t>(my_t0 + r) * a.out_row +
                                      my_head * a.out_head);

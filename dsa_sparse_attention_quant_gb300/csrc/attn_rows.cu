@@ -668,12 +668,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
             if (whole) {
               const int64_t head = static_cast<int64_t>(h) * a.group + head0 + r;
               T* out = static_cast<T*>(a.out) + mt.y * a.out_row + head * a.out_head;
-              // L = 0: no key, or only scores of -infinity; no score but NaN leaves M alone and L NaN
-              const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+              // L = 0: no key, or only scores of -infinity (O is then 0, or NaN by 0 times
+              // a V that is not finite); no score but NaN leaves M alone and L NaN
+              const float inv = 1.0f / L;
 #pragma unroll
               for (int y = 0; y < D / 8; ++y)
                 *reinterpret_cast<uint32_t*>(out + y * 8 + c2) =
-                    E::pack(o[x][y][2 * e] * inv, o[x][y][2 * e + 1] * inv);
+                    L == 0.0f ? 0u : E::pack(o[x][y][2 * e] * inv, o[x][y][2 * e + 1] * inv);
               if (a.lse != nullptr && (lane & 3) == 0)
                 a.lse[static_cast<int64_t>(mt.y) * a.heads + head] =
                     L == 0.0f ? NEG : (M + log2f(L)) * 0.6931471805599453f;
@@ -731,9 +732,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
       float w[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) w[i] = p[i];
-      if (v.y == 0.0f) continue;  // no key in this part
-      const float n = fmaxf(M, v.x);
-      const float f = ex2(M - n), e = ex2(v.x - n);  // M = -inf: 0
+      // a part without a weight adds 0, or NaN where V is not finite: as within a CTA
+      const float n = fmaxf(M, v.x), ref = n == -INFINITY ? 0.0f : n;
+      const float f = ex2(M - ref), e = ex2(v.x - ref);  // -inf: 0
       M = n;
       L = L * f + v.y * e;
 #pragma unroll
@@ -763,10 +764,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
   }
   if (!in) return;
   const int64_t head = static_cast<int64_t>(h) * a.group + head0 + r;
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const float inv = 1.0f / L;
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + d.x * a.out_row + head * a.out_head + lane * V);
 #pragma unroll
-  for (int i = 0; i < V; i += 2) out[i / 2] = Elem<T>::pack(o[i] * inv, o[i + 1] * inv);
+  for (int i = 0; i < V; i += 2) out[i / 2] = L == 0.0f ? 0u : Elem<T>::pack(o[i] * inv, o[i + 1] * inv);
   if (a.lse != nullptr && lane == 0)
     a.lse[static_cast<int64_t>(d.x) * a.heads + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }

@@ -387,9 +387,11 @@ DSA_API int dsa_kv_write(const void *k, int64_t k_row_stride, int64_t k_head_str
  * Scores, sums and the running maximum are fp32; the weights e^(s_j - max) are
  * rounded to the inputs' type for the product with V, the result once more
  * when it is stored. A token that sees no key, or whose scores are all
- * -infinity, gets out = 0, lse = -infinity.
+ * -infinity, gets out = 0, lse = -infinity, whatever V holds.
  * Keys that a token does not see have no influence on its row, whatever bits
- * they hold (NaN and infinities included); a visible NaN gives NaN.
+ * they hold (NaN and infinities included). For other rows a visible NaN score
+ * gives NaN, a visible NaN in V gives NaN in its column, even where its weight
+ * is 0, and a visible infinity in V gives an infinity or NaN there.
  *   q, out   device [T, num_heads, head_dim] of the cache's type, 16-byte
  *            aligned; row and head strides in elements, multiples of 8, at
  *            least head_dim (that of an axis of one element is not used)

@@ -1,5 +1,6 @@
 """Attention at its edges, against plain attention in 64 bits: rows that no
-request owns."""
+request owns, rows whose scores are all -infinity over values that are not
+finite."""
 import math
 
 import pytest
@@ -8,6 +9,7 @@ import torch
 import dsa_sparse_attention_quant_gb300 as dsa
 from tests.attn_ref import attend, check
 from tests.test_gpu_attn_prompt import Prompts
+from tests.test_gpu_attn_rows import Step
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -81,3 +83,48 @@ def test_rows_of_the_other_half_of_a_mixed_step():
         for e in range(4):
             check(out[t, e], lse[t, e], attend(p.q[t, e], p.kf[t][:, e // 2], p.vf[t][:, e // 2], 128 ** -0.5, p.dtype))
     assert empty(out[2:], lse[2:])
+
+
+# ------------------------------------- scores of -infinity, values not finite
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("keys", [40, 3000])
+@pytest.mark.parametrize("group", [2, 20])
+def test_rows_of_minus_infinity_over_values_that_are_not_finite(dtype, keys, group):
+    s = Step(41, [keys, keys, 5], [1] * 3, 2 * group, 2, 64, dtype)
+    at = s.batch.block_table.long()
+    s.q.abs_()
+    for r, n in ((0, keys), (1, keys - 5)):     # request 0: every score, request 1: all but the last five
+        for j in range(0, n, 64):
+            s.k[at[r, j // 64], :min(64, n - j), 0] = -math.inf
+        s.v[at[r, 0], 7, 0, 3], s.v[at[r, 0], 11, 0, 4] = math.nan, math.inf
+    phys = torch.full((3, keys), -1, dtype=torch.int32, device=DEV)
+    for r, n in enumerate([keys, keys, 5]):
+        j = torch.arange(n, device=DEV)
+        phys[r, :n] = (at[r][j // 64] * 64 + j % 64).to(torch.int32)
+    for out, lse in (dsa.attn_decode(s.batch, s.q, s.k, s.v), dsa.attn_selected(s.q, s.k, s.v, phys)):
+        assert empty(out[0, :group], lse[0, :group])
+        # a visible NaN gives NaN, a visible infinity an infinity or NaN, however the keys are cut
+        assert bool(torch.isnan(out[1, :group, 3]).all()) and not bool(torch.isfinite(out[1, :group, 4]).any())
+        keep = [i for i in range(64) if i not in (3, 4)]
+        for e in range(group):
+            ref = attend(s.q[1, e], s.kf[1][-5:, 0], s.vf[1][-5:, 0], s.scale, dtype)
+            check(out[1, e, keep], lse[1, e], (ref[0][keep], ref[1], ref[2][keep], ref[3]))
+        assert bool(torch.isfinite(out[:, group:]).all()) and bool(torch.isfinite(out[2]).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [2, 3])
+def test_prompt_of_minus_infinity_over_values_that_are_not_finite(dtype, d, hq):
+    n = 400
+    p = Prompts(42, [n], [n], hq, 1, d, dtype, False, gap=0)
+    p.q.abs_()
+    p.k[:150] = -math.inf
+    p.v[5, 0, 3], p.v[140, 0, 4], p.v[200, 0, 5] = math.nan, math.inf, math.inf
+    out, lse = p.run()
+    assert empty(out[:150], lse[:150])
+    assert bool(torch.isnan(out[150:, :, 3]).all())
+    assert not bool(torch.isfinite(out[150:, :, 4]).any()) and not bool(torch.isfinite(out[200:, :, 5]).any())
+    keep = [i for i in range(d) if i not in (3, 4, 5)]
+    assert bool(torch.isfinite(out[150:][..., keep]).all()) and bool(torch.isfinite(out[150:200, :, 5]).all())
