@@ -123,9 +123,11 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pairs_kernel(const __grid_c
 
 // ----------------------------------------------------------------------- fork
 constexpr int kForkThreads = 1024;
+constexpr int kForkUnclaim = 2;  // an entry's state until its child is empty again
 
 // One CTA: checks the list, takes the fresh pages. entry[i] = {parent's last
-// page, fresh page, parent's length, state}; state 0 = skipped.
+// page, fresh page, parent's length, state}; state 0 = skipped. A child that was
+// claimed and then skipped is empty again.
 __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_constant__ PagesArgs p) {
   __shared__ int scan[33];
   const int tid = threadIdx.x;
@@ -161,8 +163,14 @@ __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_co
       if (*reinterpret_cast<volatile int32_t*>(p.seq_lens + p.b[i]) != i - p.n) {
         p.entry[i].w = 0;
         flag_error(p.err, DSA_DEVERR_PAGE_STATE);
-      } else {
-        part = p.entry[i].z % kBlock != 0;
+      } else if (p.entry[i].z % kBlock != 0) {
+        const int32_t src = p.block_table[p.a[i] * p.bt_stride + p.entry[i].z / kBlock];
+        part = src >= 0 && src < p.num_blocks;
+        p.entry[i].x = src;
+        if (!part) {  // nothing to copy
+          p.entry[i].w = kForkUnclaim;
+          flag_error(p.err, DSA_DEVERR_BLOCK_RANGE);
+        }
       }
     }
     const int incl = block_scan_incl(part, scan, &tot);
@@ -189,21 +197,20 @@ __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_co
   for (int i = tid; i < p.n; i += kForkThreads) {
     int4 e = p.entry[i];
     if (!e.w) continue;
-    const int32_t a = p.a[i], b = p.b[i];
-    const int full = e.z / kBlock;
+    const int32_t b = p.b[i];
     if (e.z % kBlock != 0) {
-      if (e.y >= found) {  // no page left: the child stays empty
+      if (e.w != kForkUnclaim && e.y >= found) {  // no page left
         flag_error(p.err, DSA_DEVERR_NO_PAGE);
+        e.w = kForkUnclaim;
+      }
+      if (e.w == kForkUnclaim) {
         p.seq_lens[b] = 0;
         p.entry[i].w = 0;
         continue;
       }
-      const int32_t src = p.block_table[a * p.bt_stride + full], dst = p.fresh[e.y];
-      const bool in = src >= 0 && src < p.num_blocks;
-      if (!in) flag_error(p.err, DSA_DEVERR_BLOCK_RANGE);
+      const int32_t dst = p.fresh[e.y];
       p.refs[dst] = 1;
-      p.block_table[b * p.bt_stride + full] = dst;
-      e.x = in ? src : -1;
+      p.block_table[b * p.bt_stride + e.z / kBlock] = dst;
       e.y = dst;
     }
     p.seq_lens[b] = e.z;
