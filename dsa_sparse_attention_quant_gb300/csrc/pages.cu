@@ -165,11 +165,12 @@ __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_co
         flag_error(p.err, DSA_DEVERR_PAGE_STATE);
       } else if (p.entry[i].z % kBlock != 0) {
         const int32_t src = p.block_table[p.a[i] * p.bt_stride + p.entry[i].z / kBlock];
-        part = src >= 0 && src < p.num_blocks;
+        const bool in = src >= 0 && src < p.num_blocks;
+        part = in && p.refs[src] > 0;
         p.entry[i].x = src;
-        if (!part) {  // nothing to copy
+        if (!part) {  // nothing to copy, or a page that may be another child's fresh one
           p.entry[i].w = kForkUnclaim;
-          flag_error(p.err, DSA_DEVERR_BLOCK_RANGE);
+          flag_error(p.err, in ? DSA_DEVERR_PAGE_STATE : DSA_DEVERR_BLOCK_RANGE);
         }
       }
     }

@@ -1,15 +1,20 @@
-"""The page calls over pools that are not in order: entries outside the pool.
-Whole numbers, entry by entry."""
+"""The page calls over pools that are not in order: entries outside the pool,
+pages whose count does not fit. Whole numbers, entry by entry."""
+import numpy as np
 import pytest
 
 import dsa_sparse_attention_quant_gb300 as dsa
-from tests.test_gpu_pages import BLOCK, Pool, i32
+from tests.test_gpu_pages import BLOCK, STATE, Pool, i32
 
 pytestmark = pytest.mark.gpu
 
 
 def fork(p, parents, children):
     dsa.pages_fork(p.d_refs, p.d_bt, p.d_seq, i32(parents), i32(children), p.dev, dev_err=p.err)
+
+
+def lowest_free(p, n):
+    return [int(x) for x in np.nonzero(p.refs == 0)[0][:n]]
 
 
 @pytest.mark.parametrize("entry", [30, 2 ** 31 - 1, -1, -5])
@@ -22,3 +27,19 @@ def test_fork_of_a_part_filled_page_outside_the_pool(entry):
     p.fork([1, 2], [4, 6], run=False)
     p.same(BLOCK)
     assert p.seq[3] == 0 and p.seq[5] == 0 and p.seq[4] == 200
+
+
+def test_fork_of_a_part_filled_page_without_users():
+    # its bytes are anybody's: the page may be taken for another child of the same call
+    for low in (False, True):
+        p = Pool(22, 30, 7, [200, 200, 130])
+        p.refs[p.bt[0, 3]] = 0
+        if low:   # the lowest page of the pool that is free
+            free = [b for b in lowest_free(p, 30) if b < p.bt[0, 3]]
+            p.refs[free] = 1
+        p.up()
+        fork(p, [0, 1, 0, 2], [3, 4, 5, 6])
+        p.fork([1, 2], [4, 6], run=False)
+        p.same(STATE)
+        if low:
+            assert p.bt[4, 3] == p.bt[0, 3]
