@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_co
     for (; bits != 0 && k < need; bits &= bits - 1) p.fresh[k++] = static_cast<int32_t>(at + __ffs(bits) - 1);
     found += tot;
   }
+  if (tid == 0) p.counts[0] = found < need ? found : need;  // fresh pages taken
   __syncthreads();
   for (int i = tid; i < p.n; i += kForkThreads) {
     int4 e = p.entry[i];
@@ -211,6 +212,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_co
       }
       const int32_t dst = p.fresh[e.y];
       p.refs[dst] = 1;
+      p.w0[dst] = e.y;
       p.block_table[b * p.bt_stride + e.z / kBlock] = dst;
       e.y = dst;
     }
@@ -220,11 +222,14 @@ __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_co
 }
 
 // The children's shared pages (CTAs [0, n), first launch only) and the copies
-// of the part-filled last pages.
+// of the part-filled last pages. A shared page whose count was not positive is
+// flagged; one that the plan took has count 1 by now, and is known as taken by its
+// rank: w0 may hold anything for other pages, but then the rank's page is another.
 __global__ void __launch_bounds__(kCopyThreads) fork_move_kernel(const __grid_constant__ PagesArgs p,
                                                                  const __grid_constant__ CacheList cl, int tables) {
   pdl_wait();
   if (static_cast<int>(blockIdx.x) < tables) {
+    const int taken = p.counts[0];
     for (int i = blockIdx.x; i < p.n; i += tables) {
       const int4 e = p.entry[i];
       if (!e.w) continue;
@@ -233,10 +238,13 @@ __global__ void __launch_bounds__(kCopyThreads) fork_move_kernel(const __grid_co
       for (int j = threadIdx.x; j < e.z / kBlock; j += kCopyThreads) {
         const int32_t id = from[j];
         to[j] = id;
-        if (id >= 0 && id < p.num_blocks)
-          atomicAdd(p.refs + id, 1);
-        else
+        if (id < 0 || id >= p.num_blocks) {
           flag_error(p.err, DSA_DEVERR_BLOCK_RANGE);
+          continue;
+        }
+        const int k = p.w0[id];
+        if (atomicAdd(p.refs + id, 1) <= 0 || (k >= 0 && k < taken && p.fresh[k] == id))
+          flag_error(p.err, DSA_DEVERR_PAGE_STATE);
       }
     }
     return;

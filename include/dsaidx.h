@@ -516,8 +516,9 @@ DSA_API int dsa_pages_copy(const DsaCacheDesc *caches, int32_t n_caches, int64_t
  * (DSA_DEVERR_NO_PAGE). Rows outside [0, n_rows) and parents whose length is
  * negative or beyond the row flag DSA_DEVERR_SEQ_RANGE, table entries outside
  * the pool DSA_DEVERR_BLOCK_RANGE: a part-filled page's leaves the child empty, a
- * full page's is the child's as well. A part-filled page whose count is not
- * positive leaves the child empty too and flags DSA_DEVERR_PAGE_STATE. */
+ * full page's is the child's as well. A page of the parent's whose count is not
+ * positive flags DSA_DEVERR_PAGE_STATE: a part-filled one leaves the child empty
+ * too, a full one is shared all the same (and may be a fresh page of this call). */
 DSA_API int dsa_pages_fork(const DsaPages *pages, const int32_t *parents, const int32_t *children, int32_t n,
                    const DsaCacheDesc *caches, int32_t n_caches, void *ws, size_t ws_bytes,
                    int32_t *dev_err, dsa_stream_t stream);

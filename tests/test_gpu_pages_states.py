@@ -2,6 +2,7 @@
 pages whose count does not fit. Whole numbers, entry by entry."""
 import numpy as np
 import pytest
+import torch
 
 import dsa_sparse_attention_quant_gb300 as dsa
 from tests.test_gpu_pages import BLOCK, STATE, Pool, i32
@@ -43,3 +44,43 @@ def test_fork_of_a_part_filled_page_without_users():
         p.same(STATE)
         if low:
             assert p.bt[4, 3] == p.bt[0, 3]
+
+
+@pytest.mark.parametrize("count", [0, -2])
+def test_fork_shares_a_page_without_users(count):
+    p = Pool(23, 30, 6, [256, 200])
+    page = int(p.bt[0, 1])
+    free = [b for b in lowest_free(p, 30) if b < page]
+    p.refs[free] = 1       # were its count 0, it would be the lowest free page
+    p.refs[page] = count
+    p.up()
+    fork(p, [0], [3])      # whole pages alone: none is taken
+    p.fork([0], [3], run=False)
+    p.same(STATE)
+
+
+@pytest.mark.parametrize("order", [[0, 1], [1, 0]])
+def test_fork_shares_a_page_that_it_takes(order):
+    # a full page of row 0 has count 0 and is the lowest free one: row 1's child takes it
+    p = Pool(24, 30, 6, [256, 200])
+    page = int(p.bt[0, 1])
+    p.refs[[b for b in lowest_free(p, 30) if b < page]] = 1
+    p.refs[page] = 0
+    p.up()
+    fork(p, order, [3, 4])
+    child = 3 + order.index(1)
+    assert int(p.d_bt[child, 3]) == page and int(p.d_refs[page]) == 2
+    assert int(p.err.item()) == STATE
+
+
+def test_fork_of_a_sound_pool_flags_nothing():
+    # scratch from an earlier call says nothing of this one
+    p = Pool(25, 300, 40, [64 * 5 + 3, 640, 64 * 2 + 1])
+    ws = torch.zeros(dsa.pages_workspace_size(300, 12), dtype=torch.uint8, device="cuda")
+    for at in (4, 16):
+        par = [0, 1, 2] * 4
+        dsa.pages_fork(p.d_refs, p.d_bt, p.d_seq, i32(par), i32(list(range(at, at + 12))), p.dev, ws=ws, dev_err=p.err)
+        assert p.fork(par, list(range(at, at + 12)), run=False) == 0
+        p.same()
+        assert p.free([at + 1, at + 2, 0 if at == 16 else at + 3]) == 0
+        p.same()
