@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const __grid_constant__
   const int pages = (len + kBlock - 1) / kBlock;
   for (int j = threadIdx.x; j < pages; j += 256) {
     const int32_t id = atomicExch(bt + j, -1);
-    if (id < 0) continue;  // taken by the row's other entry
-    if (id >= p.num_blocks) {
+    if (id == -1) continue;  // taken by the row's other entry
+    if (id < 0 || id >= p.num_blocks) {
       flag_error(p.err, DSA_DEVERR_BLOCK_RANGE);
     } else if (atomicSub(p.refs + id, 1) <= 0) {
       atomicAdd(p.refs + id, 1);

@@ -525,7 +525,9 @@ DSA_API int dsa_pages_fork(const DsaPages *pages, const int32_t *parents, const 
 
 /* End sequences: the counts of the rows' pages go down by one, their entries
  * become -1 and their lengths 0. A row named twice ends once. A page whose
- * count is 0 already flags DSA_DEVERR_PAGE_STATE. No workspace. */
+ * count is 0 already flags DSA_DEVERR_PAGE_STATE; an entry outside the pool,
+ * other than -1, DSA_DEVERR_BLOCK_RANGE; a row outside [0, n_rows) or a length
+ * that is negative or beyond the row DSA_DEVERR_SEQ_RANGE. No workspace. */
 DSA_API int dsa_pages_free(const DsaPages *pages, const int32_t *rows, int32_t n, int32_t *dev_err,
                    dsa_stream_t stream);
 

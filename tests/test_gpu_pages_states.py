@@ -84,3 +84,18 @@ def test_fork_of_a_sound_pool_flags_nothing():
         p.same()
         assert p.free([at + 1, at + 2, 0 if at == 16 else at + 3]) == 0
         p.same()
+
+
+def test_free_flags_entries_that_are_no_pages():
+    p = Pool(26, 40, 6, [300, 200, 64])
+    pages = [int(b) for b in p.bt[0, :5]]
+    p.bt[0, 1], p.bt[0, 3] = -2, -2 ** 31
+    p.up()
+    dsa.pages_free(p.d_refs, p.d_bt, p.d_seq, i32([0, 2]), dev_err=p.err)
+    p.refs[[pages[0], pages[2], pages[4], int(p.bt[2, 0])]] -= 1
+    p.bt[0, :5] = p.bt[2, :1] = -1
+    p.seq[[0, 2]] = 0
+    p.same(BLOCK)
+    # -1 inside the length is an entry that another naming of the row has taken
+    assert p.free([1, 1]) == 0
+    p.same()
