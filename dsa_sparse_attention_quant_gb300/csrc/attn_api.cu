@@ -52,14 +52,15 @@ int check_attn(const DsaAttn* at, const DsaKv& kv, int64_t rows, DsaAttn* out) {
   return DSA_OK;
 }
 
-int check_step(const DsaBatch* b) {
+// pages: the call reads the block table.
+int check_step(const DsaBatch* b, bool pages) {
   if (b == nullptr) return DSA_EINVAL;
   if (b->num_reqs < 0 || b->num_decodes < 0 || b->num_decodes > b->num_reqs || b->num_tokens < 0) return DSA_EINVAL;
   if (b->num_decode_tokens < 0 || b->num_decode_tokens > b->num_tokens) return DSA_EINVAL;
   if (b->num_tokens > 0 && b->num_reqs == 0) return DSA_EINVAL;
   if (b->max_seq_len < 0) return DSA_EINVAL;
-  if (b->num_reqs > 0 && (!b->query_start_loc || !b->seq_lens || !b->block_table || b->bt_stride < 1))
-    return DSA_EINVAL;
+  if (b->num_reqs > 0 && (!b->query_start_loc || !b->seq_lens)) return DSA_EINVAL;
+  if (b->num_reqs > 0 && pages && (!b->block_table || b->bt_stride < 1)) return DSA_EINVAL;
   if (b->num_tokens > 0 && b->req_id_per_token == nullptr) return DSA_EINVAL;
   return DSA_OK;
 }
@@ -332,7 +333,7 @@ int dsa_kv_write(const void* k, int64_t k_row_stride, int64_t k_head_stride, con
 
 size_t dsa_attn_decode_workspace_size(const DsaBatch* batch, int32_t num_heads, int32_t num_kv_heads,
                                       int32_t head_dim) {
-  if (check_step(batch) != DSA_OK || !heads_ok(num_heads, num_kv_heads, head_dim)) return 0;
+  if (check_step(batch, true) != DSA_OK || !heads_ok(num_heads, num_kv_heads, head_dim)) return 0;
   return rows_plan(batch->num_decode_tokens, batch->num_reqs > 0 ? max_keys(batch) : 0, num_heads, num_kv_heads,
                    head_dim, kRowsCtas)
       .bytes;
@@ -342,7 +343,7 @@ int dsa_attn_decode(const DsaBatch* batch, const DsaKv* kv, const DsaAttn* attn,
                     int32_t* dev_err, dsa_stream_t stream) {
   DsaKv c;
   DsaAttn at;
-  int st = check_step(batch);
+  int st = check_step(batch, true);
   if (st != DSA_OK) return st;
   if (batch->num_decode_tokens == 0) return DSA_OK;
   if ((st = check_kv(kv, false, &c)) != DSA_OK ||
@@ -387,12 +388,12 @@ int dsa_attn_prompt(const DsaBatch* batch, const DsaKv* kv, const int32_t* kv_st
                     int32_t* dev_err, dsa_stream_t stream) {
   DsaKv c;
   DsaAttn at;
-  int st = check_step(batch);
+  const bool packed = kv_start != nullptr;
+  int st = check_step(batch, !packed);
   if (st != DSA_OK) return st;
   const int reqs = batch->num_reqs - batch->num_decodes;
   const int64_t rows = batch->num_tokens - batch->num_decode_tokens;
   if (rows == 0) return DSA_OK;
-  const bool packed = kv_start != nullptr;
   if ((st = check_kv(kv, packed, &c)) != DSA_OK ||
       (st = check_attn(attn, c, batch->num_tokens, &at)) != DSA_OK)
     return st;

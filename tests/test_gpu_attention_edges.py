@@ -128,3 +128,13 @@ def test_prompt_of_minus_infinity_over_values_that_are_not_finite(dtype, d, hq):
     assert not bool(torch.isfinite(out[150:, :, 4]).any()) and not bool(torch.isfinite(out[200:, :, 5]).any())
     keep = [i for i in range(d) if i not in (3, 4, 5)]
     assert bool(torch.isfinite(out[150:][..., keep]).all()) and bool(torch.isfinite(out[150:200, :, 5]).all())
+
+
+# ------------------------------------------------------------- unused metadata
+
+def test_packed_prompts_without_a_block_table():
+    p = Prompts(34, [300, 65], [300, 100], 4, 2, 64, torch.bfloat16, False)
+    want, wlse = p.run()
+    p.batch.c.block_table, p.batch.c.bt_stride = None, 0
+    out, lse = p.run()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
