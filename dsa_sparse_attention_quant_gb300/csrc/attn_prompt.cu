@@ -225,10 +225,10 @@ __device__ __forceinline__ PromptTile find_tile(const PromptArgs& a, int rank, P
     int q0 = 0, q1 = 0, sl = 0, s0 = 0;
     bool bad = false;
     if (r >= a.num_decodes) {
-      q0 = __ldg(a.qsl + r);
-      q1 = __ldg(a.qsl + r + 1);
-      sl = __ldg(a.seq_lens + r);
-      if (a.kv_start != nullptr) s0 = __ldg(a.kv_start + r);
+      q0 = a.qsl[r];
+      q1 = a.qsl[r + 1];
+      sl = a.seq_lens[r];
+      if (a.kv_start != nullptr) s0 = a.kv_start[r];
       if (q1 < q0 || q0 < a.first_token || q1 > a.num_tokens) {
         bad = true;
         q1 = q0;  // no rows of its own to write
@@ -389,7 +389,7 @@ __device__ __forceinline__ void add_non_finite(const PromptArgs& a, const Prompt
   for (int k = k0; k < k1; ++k) {
     int64_t at;
     if (a.kv_start == nullptr) {
-      const int id = __ldg(a.block_table + static_cast<int64_t>(cta.tile.req) * a.bt_stride + k / kBlock);
+      const int id = a.block_table[static_cast<int64_t>(cta.tile.req) * a.bt_stride + k / kBlock];
       if (id < 0 || id >= a.num_blocks) continue;
       at = id * a.v_page + static_cast<int64_t>(k % kBlock) * a.v_slot;
     } else {
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (a.kv_start == nullptr) {
               if ((j & 15) == 0) {  // the next 32 pages
                 const int pg = 2 * j + lane;
-                ids = pg < n_pages ? __ldg(a.block_table + static_cast<int64_t>(tile.req) * a.bt_stride + pg) : 0;
+                ids = pg < n_pages ? a.block_table[static_cast<int64_t>(tile.req) * a.bt_stride + pg] : 0;
                 if (ids < 0 || ids >= a.num_blocks) {
                   flag_error(a.err, DSA_DEVERR_BLOCK_RANGE);
                   ids = 0;

@@ -138,9 +138,9 @@ enum : int { kFirst = 1, kLast = 2, kStartsItem = 4, kEndsItem = 8 };
 // its request's block-table row.
 __device__ __forceinline__ int token_keys(const RowsArgs& a, int t, int* req, bool flag) {
   // token t mostly belongs to request t: that one's metadata is read beside its id, not after it
-  const int r = __ldg(a.req_id + t);
+  const int r = a.req_id[t];
   const bool guess = t < a.num_reqs;
-  int q0 = guess ? __ldg(a.qsl + t) : 0, q1 = guess ? __ldg(a.qsl + t + 1) : 0, sl = guess ? __ldg(a.seq_lens + t) : 0;
+  int q0 = guess ? a.qsl[t] : 0, q1 = guess ? a.qsl[t + 1] : 0, sl = guess ? a.seq_lens[t] : 0;
   *req = 0;
   if (r < 0 || r >= a.num_reqs) {
     if (flag) flag_error(a.err, DSA_DEVERR_SEQ_RANGE);
@@ -148,9 +148,9 @@ __device__ __forceinline__ int token_keys(const RowsArgs& a, int t, int* req, bo
   }
   *req = r;
   if (r != t) {
-    q0 = __ldg(a.qsl + r);
-    q1 = __ldg(a.qsl + r + 1);
-    sl = __ldg(a.seq_lens + r);
+    q0 = a.qsl[r];
+    q1 = a.qsl[r + 1];
+    sl = a.seq_lens[r];
   }
   if (t < q0 || t >= q1 || sl < 0 || sl > a.max_keys) {
     if (flag) flag_error(a.err, DSA_DEVERR_SEQ_RANGE);
@@ -335,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
     if (cur.left <= 0) return;
     if (SEL) {
       const int j = cur.kt * kTile + warp * kWarpKeys + (lane & 15);
-      if (j < a.topk) nid = __ldg(a.physical + static_cast<int64_t>(cur.t) * a.topk + j);
+      if (j < a.topk) nid = a.physical[static_cast<int64_t>(cur.t) * a.topk + j];
     } else if (cur.n > 0) {
-      nid = __ldg(a.block_table + static_cast<int64_t>(cur.req) * a.bt_stride + cur.kt);
+      nid = a.block_table[static_cast<int64_t>(cur.req) * a.bt_stride + cur.kt];
     }
   };
   auto issue = [&](int stage) {
@@ -450,10 +450,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
         const T* q1 = q + (v1 ? g + 8 : 0) * a.q_head + c2;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          qf[k][0] = v0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16)) : 0u;
-          qf[k][1] = v1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 16)) : 0u;
-          qf[k][2] = v0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16 + 8)) : 0u;
-          qf[k][3] = v1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 16 + 8)) : 0u;
+          qf[k][0] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + k * 16) : 0u;
+          qf[k][1] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + k * 16) : 0u;
+          qf[k][2] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + k * 16 + 8) : 0u;
+          qf[k][3] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + k * 16 + 8) : 0u;
         }
       } else {
         // (no warp reads the previous item's rows any more: all have met at its end)
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
         for (int i = threadIdx.x; i < C::kRows * CH; i += kThreads) {
           const int r = i / CH, c = i % CH;
           const uint4 v =
-              r < rows ? __ldg(reinterpret_cast<const uint4*>(q + r * a.q_head + c * 8)) : make_uint4(0, 0, 0, 0);
+              r < rows ? *reinterpret_cast<const uint4*>(q + r * a.q_head + c * 8) : make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4*>(qbuf + r * C::kRowBytes + ((c ^ (r & 7)) << 4)) = v;
         }
         __syncthreads();

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_co
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kWriteThreads / 32);
   const int chunks = a.hkv * CH;
   for (int64_t t = warp; t < a.n_tokens; t += warps) {
-    const int64_t slot = __ldg(a.slot_mapping + t);
+    const int64_t slot = a.slot_mapping[t];
     if (slot < 0 || slot >= a.num_slots) {
       if (slot != -1 && lane == 0) flag_error(a.err, DSA_DEVERR_SLOT_RANGE);
       continue;
@@ -48,8 +48,8 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_co
       for (int u = 0; u < U; ++u) {
         const int c = c0 + 32 * u;
         if (c < chunks) {
-          kx[u] = __ldg(reinterpret_cast<const uint4*>(ks + (c / CH) * a.k_rhead + (c % CH) * 8));
-          vx[u] = __ldg(reinterpret_cast<const uint4*>(vs + (c / CH) * a.v_rhead + (c % CH) * 8));
+          kx[u] = *reinterpret_cast<const uint4*>(ks + (c / CH) * a.k_rhead + (c % CH) * 8);
+          vx[u] = *reinterpret_cast<const uint4*>(vs + (c / CH) * a.v_rhead + (c % CH) * 8);
         }
       }
 #pragma unroll

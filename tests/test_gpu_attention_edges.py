@@ -130,6 +130,23 @@ def test_prompt_of_minus_infinity_over_values_that_are_not_finite(dtype, d, hq):
     assert bool(torch.isfinite(out[150:][..., keep]).all()) and bool(torch.isfinite(out[150:200, :, 5]).all())
 
 
+# ----------------------------------------------------------- results over q
+
+@pytest.mark.parametrize("keys", [[100, 300], [5000, 1200]])
+def test_results_over_the_queries(keys):
+    # out may be q's own memory
+    s = Step(54, keys, [1, 1], 8, 2, 128, torch.bfloat16)
+    want, wlse = dsa.attn_decode(s.batch, s.q, s.k, s.v)
+    q = s.q.clone()
+    out, lse = dsa.attn_decode(s.batch, q, s.k, s.v, out=q)
+    assert out is q and torch.equal(q, want) and torch.equal(lse, wlse)
+    for hq, hkv in ((4, 2), (3, 1)):
+        p = Prompts(55, [300, 700], [400, 700], hq, hkv, 64, torch.float16, True)
+        want, wlse = p.run()
+        out, lse = p.run(out=p.q)
+        assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
 # ------------------------------------------------------------- unused metadata
 
 def test_packed_prompts_without_a_block_table():
