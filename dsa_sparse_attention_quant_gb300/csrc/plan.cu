@@ -160,7 +160,8 @@ __device__ void plan_batch(const PlanArgs& p, PlanSmem& S) {
 // per stack61 F layer.
 // Launched as a programmatic dependent of the previous layer's top-k (pdl), it
 // quantises while that top-k's last CTAs run, and waits for it only before
-// clearing the decode rows' histograms and counters, which the top-k reads.
+// clearing the decode rows' histograms and counters, which the top-k reads, or
+// before its own end.
 constexpr int kPrologueThreads = 256;
 constexpr int kPrologueMinCtas = 4;
 
@@ -251,6 +252,10 @@ __global__ void __launch_bounds__(kPrologueThreads, kPrologueMinCtas) prologue_k
       if (lane == 0) reinterpret_cast<uint4*>(a.counters)[t] = make_uint4(0, 0, 0, 0);
     }
   }
+  // A step without decode rows clears nothing. This kernel still may not end
+  // before that top-k: the score kernel waits for this one alone, and writes the
+  // score rows that the top-k reads. One CTA holds the end up, the others make room.
+  if (z_rows == 0 && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // Prologue CTAs resident on one SM (the occupancy of the instance, with the

@@ -206,3 +206,31 @@ def test_stack_without_consumer(work):
     topk = topk.cpu().numpy()
     assert not compare.check_topk(topk, scores, lens, hb.topk)
     assert np.array_equal(valid.cpu().numpy(), (topk >= 0).sum(axis=1))
+
+
+def test_prefill_stack_without_consumer():
+    # prefill rows alone, every F layer: the next layer's prologue and scores are
+    # launched while the previous layer's top-k still reads the score rows; each
+    # layer's ids (in no particular order) against the same layer run alone
+    n_layers = 4
+    fs, _ = dsa.schedule_build(n_layers, pattern="F" * n_layers)
+    hb = synth.make_batch(77, [], [(2600, 2600), (900, 700)], 64)
+    batch = dsa.Batch.from_host(hb, DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    cache = dsa.new_k_cache(hb.num_blocks, device=DEV)
+    dsa.indexer_k_quant_write(bf16_tensor(hb.ctx_k), torch.from_numpy(hb.ctx_slots).to(DEV), cache, err)
+    slots = torch.from_numpy(hb.slot_mapping).to(DEV)
+    layers = [dict(q=torch.randn((hb.num_tokens, 64, 128), generator=g, device=DEV).to(torch.bfloat16),
+                   w=torch.rand((hb.num_tokens, 64), generator=g, device=DEV),
+                   k_new=torch.randn((hb.num_tokens, 128), generator=g, device=DEV).to(torch.bfloat16),
+                   k_cache=cache.clone()) for _ in range(n_layers)]
+    alone = []
+    for layer in layers:
+        one = dict(layer, k_cache=layer["k_cache"].clone())
+        alone.append(dsa.layer_stack_run(batch, "F", [one], hb.topk, slot_mapping=slots, dev_err=err)[0].sort(1).values)
+    for first in range(n_layers):    # stacks that end with each layer: the last one's ids stay in the buffers
+        topk = dsa.layer_stack_run(batch, fs[:first + 1], layers[:first + 1], hb.topk, slot_mapping=slots,
+                                   dev_err=err)[0]
+        assert torch.equal(topk.sort(1).values, alone[first]), f"layer {first}"
+    assert dsa.check_device_error(err) == 0

@@ -23,3 +23,38 @@ def test_nothing_is_read_as_read_only(name):
     assert "launch_pdl(" in text and "pdl_wait();" in text
     for word in ("__ldg", "__restrict__", "ld.global.nc"):
         assert word not in text, word
+
+
+def bodies():
+    """Name and body of every kernel of the library."""
+    for name in sorted(os.listdir(CSRC)):
+        if not name.endswith(".cu"):
+            continue
+        text = source(name)
+        for m in re.finditer(r"__global__ void (?:__launch_bounds__\((?:[^()]|\([^()]*\))*\)\s*)?(\w+)\(", text):
+            i = text.index("{", m.end())
+            end, depth = i + 1, 1
+            while depth:
+                depth += (text[end] == "{") - (text[end] == "}")
+                end += 1
+            yield m.group(1), text[i + 1:end - 1]
+
+
+def test_kernels_launched_early_wait_whatever_they_have_to_do():
+    # a kernel that ends without having waited lets the next one begin, and write,
+    # while the one before it still reads. The score kernel's two forms wait in
+    # branches that are decided when it is compiled.
+    launched = set()
+    for name in os.listdir(CSRC):
+        launched |= set(re.findall(r"launch_pdl\((\w+)", source(name) if name.endswith(".cu") else ""))
+    seen = {}
+    for name, body in bodies():
+        depth = 0
+        for word in re.findall(r"[{}]|pdl_wait\(\);", body):
+            depth += (word == "{") - (word == "}")
+            if word.startswith("pdl_wait") and depth == 0:
+                seen[name] = True
+        seen.setdefault(name, False)
+    assert {"prologue_kernel", "topk_kernel", "resolve_kernel", "kv_write_kernel", "attn_join_kernel"} <= launched
+    for name in (launched & set(seen)) | {"attn_rows_kernel", "attn_prompt_kernel"}:
+        assert seen[name] or name == "logits_kernel", name
