@@ -94,7 +94,7 @@ struct RowCfg {
 // choice is made per row, so the short prefill rows of a batch whose score
 // rows are long (decode requests at long context) still stage.
 template <int NT>
-__global__ void __launch_bounds__(NT, NT == 1024 ? 1 : 4) topk_kernel(const float* __restrict__ logits, int64_t ld,
+__global__ void __launch_bounds__(NT, NT == 1024 ? 1 : 4) topk_kernel(const float* logits, int64_t ld,
                                                                       const int32_t* qsl, const int32_t* seq_lens,
                                                                       const int32_t* req_id, int num_reqs,
                                                                       int row_begin, int topk,

@@ -58,3 +58,14 @@ def test_kernels_launched_early_wait_whatever_they_have_to_do():
     assert {"prologue_kernel", "topk_kernel", "resolve_kernel", "kv_write_kernel", "attn_join_kernel"} <= launched
     for name in (launched & set(seen)) | {"attn_rows_kernel", "attn_prompt_kernel"}:
         assert seen[name] or name == "logits_kernel", name
+
+
+def test_no_input_is_declared_read_only():
+    text = "".join(source(name) for name in os.listdir(CSRC) if name.endswith(".cu"))
+    launched = set(re.findall(r"launch_pdl\((\w+)", text)) | {"attn_rows_kernel", "attn_prompt_kernel"}
+    found = set()
+    for m in re.finditer(r"__global__ void (?:__launch_bounds__\((?:[^()]|\([^()]*\))*\)\s*)?(\w+)\(([^)]*)\)", text):
+        if m.group(1) in launched:
+            found.add(m.group(1))
+            assert not re.search(r"const \w+\s*\*\s*__restrict__", m.group(2)), m.group(1)
+    assert {"topk_kernel", "prologue_kernel", "attn_rows_kernel", "fork_move_kernel"} <= found
