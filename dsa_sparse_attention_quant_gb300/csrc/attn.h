@@ -55,6 +55,7 @@ cudaError_t launch_kv_write(const KvWriteArgs& a, int head_dim, int num_sms, cud
 
 // Page moves (pages.cu).
 constexpr int kMaxCaches = 64;  // caches per copy launch
+constexpr int kPartBytes = 32768;  // a CTA's piece of a page: what the lists count and the copies step by
 struct CacheList {
   uint8_t* base[kMaxCaches];
   int64_t page_bytes[kMaxCaches];

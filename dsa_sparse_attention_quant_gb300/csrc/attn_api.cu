@@ -263,7 +263,6 @@ int check_pages(const DsaPages* g, bool lens) {
 // Calls f(lists, n) with the caches in lists of kMaxCaches; one empty list without caches.
 template <typename F>
 int with_lists(const DsaCacheDesc* caches, int32_t n, F f) {
-  constexpr int64_t part = 32768;
   CacheList lists[kMaxLists];
   int m = 0;
   for (int32_t i = 0; i < n || m == 0; ++m) {
@@ -273,7 +272,7 @@ int with_lists(const DsaCacheDesc* caches, int32_t n, F f) {
       l.base[l.n] = static_cast<uint8_t*>(caches[i].base);
       l.page_bytes[l.n] = caches[i].page_bytes;
       l.page_stride[l.n] = caches[i].page_stride;
-      l.parts += static_cast<int>((caches[i].page_bytes + part - 1) / part);
+      l.parts += static_cast<int>((caches[i].page_bytes + kPartBytes - 1) / kPartBytes);
       l.parts_end[l.n] = l.parts;
     }
   }

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_co
 // per thread in flight; parts are numbered pair-major over all caches.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;
-constexpr int kPartBytes = kCopyThreads * kCopyUnroll * 16;
+static_assert(kPartBytes == kCopyThreads * kCopyUnroll * 16, "a CTA copies a whole part");
 
 __device__ __forceinline__ void copy_part(const CacheList& cl, int part, int64_t src, int64_t dst) {
   int c = 0;
