@@ -96,7 +96,8 @@ struct PElem;
 template <>
 struct PElem<__nv_bfloat16> {
   static constexpr uint32_t kFmt = 1;
-  // bf16 has fp32's exponents: weights may reach 2^30 before the reference moves.
+  // bf16 has fp32's exponents: a tile's weights may sum to 2^30 before the reference
+  // moves. O is their product with V, not yet divided: |v| < 2^98 / tiles stays finite.
   static constexpr float kHead = 0.0f, kMaxSum = 1073741824.0f;
   static constexpr uint32_t kExp = 0x7F80u;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {

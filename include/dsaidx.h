@@ -373,7 +373,8 @@ typedef struct DsaKv {
  *                 of 8 (column views of a fused projection go in as they are)
  *   slot_mapping  device int64 [n_tokens]; -1 = padding token, skipped
  *   kv            the cache, written in place
- * Slots must be distinct: of two tokens with one slot either may remain.
+ * Slots must be distinct: of two tokens with one slot, parts of either may
+ * remain.
  * Other slots outside the cache are skipped and flag DSA_DEVERR_SLOT_RANGE. */
 DSA_API int dsa_kv_write(const void *k, int64_t k_row_stride, int64_t k_head_stride, const void *v,
                  int64_t v_row_stride, int64_t v_head_stride, int64_t n_tokens,
@@ -384,9 +385,15 @@ DSA_API int dsa_kv_write(const void *k, int64_t k_row_stride, int64_t k_head_str
  * num_kv_heads), and the keys j that the token sees:
  *   s_j = scale * q[t,e].k[j,h]
  *   out[t,e] = sum_j e^(s_j) v[j,h] / sum_j e^(s_j),  lse[t,e] = ln sum_j e^(s_j).
- * Scores, sums and the running maximum are fp32; the weights e^(s_j - max) are
- * rounded to the inputs' type for the product with V, the result once more
- * when it is stored. A token that sees no key, or whose scores are all
+ * Scores, sums and a row's reference M are fp32. The weights 2^(s_j log2(e) - M)
+ * are rounded to the inputs' type for the product with V, the result once more
+ * when it is stored. M follows the largest score seen loosely, so weights may
+ * exceed 1: in bf16 by 2^8 each for single rows and by 2^30 in sum over 128 keys
+ * for prompts. They multiply V before the division by their sum: over n keys,
+ * bf16 elements of V below 2^98 / ceil(n / 128) in magnitude cannot overflow
+ * there, larger ones may give an infinity (fp16 elements never do). fp16 weights
+ * are multiples of 2^-28 of the row's largest, or finer.
+ * A token that sees no key, or whose scores are all
  * -infinity, gets out = 0, lse = -infinity, whatever V holds.
  * Keys that a token does not see have no influence on its row, whatever bits
  * they hold (NaN and infinities included). For other rows a visible NaN score
@@ -395,6 +402,8 @@ DSA_API int dsa_kv_write(const void *k, int64_t k_row_stride, int64_t k_head_str
  *   q, out   device [T, num_heads, head_dim] of the cache's type, 16-byte
  *            aligned; row and head strides in elements, multiples of 8, at
  *            least head_dim (that of an axis of one element is not used)
+ *            out may be q itself (one base, the same strides); otherwise out's
+ *            rows overlap neither each other nor q
  *   lse      device fp32 [T, num_heads] contiguous, or NULL
  *   num_heads  a multiple of kv->num_kv_heads
  *   scale    <= 0 selects head_dim^-0.5; NaN, and a scale that overflows fp32

@@ -1,6 +1,6 @@
 """Attention at its edges, against plain attention in 64 bits: rows that no
 request owns, rows whose scores are all -infinity over values that are not
-finite."""
+finite, sizes far from the usual ones."""
 import math
 
 import pytest
@@ -9,7 +9,7 @@ import torch
 import dsa_sparse_attention_quant_gb300 as dsa
 from tests.attn_ref import attend, check
 from tests.test_gpu_attn_prompt import Prompts
-from tests.test_gpu_attn_rows import Step
+from tests.test_gpu_attn_rows import Step, check_selected, selected_case
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -155,3 +155,62 @@ def test_packed_prompts_without_a_block_table():
     p.batch.c.block_table, p.batch.c.bt_stride = None, 0
     out, lse = p.run()
     assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+# --------------------------------------------------------------------- sizes
+
+@pytest.mark.parametrize("hq,hkv", [(72, 1), (128, 1), (256, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_many_heads(hq, hkv, d):
+    # more than two passes over the keys, short rows and cut ones
+    for keys in ([90, 0, 130], [2500, 1, 700]):
+        s = Step(hq + d, keys, [1] * 3, hq, hkv, d, torch.bfloat16)
+        out, lse = dsa.attn_decode(s.batch, s.q, s.k, s.v)
+        s.check(out, lse)
+    q, k, v, phys = selected_case(hq, 4, 900, hq, hkv, d, torch.float16)
+    out, lse = dsa.attn_selected(q, k, v, phys)
+    check_selected(q, k, v, phys, out, lse, torch.float16)
+
+
+@pytest.mark.parametrize("hq,hkv", [(6, 2), (24, 1), (40, 1)])
+def test_decode_several_long_tokens_per_request(hq, hkv):
+    s = Step(51, [3000, 700, 1900], [4, 1, 7], hq, hkv, 64, torch.bfloat16)
+    out, lse = dsa.attn_decode(s.batch, s.q, s.k, s.v)
+    s.check(out, lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_selected_for_the_tokens_of_a_prompt(dtype):
+    # a row per prompt token; rows sampled over the whole length
+    tokens, topk = 4099, 520
+    q, k, v, phys = selected_case(52, tokens, topk, 8, 2, 128, dtype)
+    phys[tokens - 1] = -1
+    err = i32([0])
+    out, lse = dsa.attn_selected(q, k, v, phys, dev_err=err)
+    assert int(err.item()) == 0 and bool(torch.isfinite(out).all())
+    rows = [0, 1, 303, 304, 1023, 2048, 2049, 3333, 4097, 4098]
+    check_selected(q[rows], k, v, phys[rows], out[rows], lse[rows], dtype)
+    again, _ = dsa.attn_selected(q, k, v, phys)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_values(d):
+    # O is summed before it is divided: with bf16, |v| < 2^98 / ceil(keys / 128) is
+    # finite (here 2^96). The scores rise by 20 powers of two, so that weights get large.
+    n = 500
+    p = Prompts(53, [n], [n], 2, 1, d, torch.bfloat16, True)
+    top = 20 * math.log(2) * d ** 0.5 / d
+    p.q = torch.ones_like(p.q)
+    up = (torch.arange(n, device=DEV) / n * top)[:, None, None].expand(n, 1, d).to(p.dtype)
+    big = (p.vf[0].float().clamp(-2, 2) * 2.0 ** 94).to(p.dtype)
+    for j in range(0, n, 64):
+        page = p.bt[0][j // 64]
+        p.k[page, :min(64, n - j)], p.v[page, :min(64, n - j)] = up[j:j + 64], big[j:j + 64]
+    p.kf[0], p.vf[0] = up, big
+    out, lse = p.run()
+    p.check(out, lse)
+    b = dsa.Batch(i32([0, 1]), i32([n]), i32(p.bt), i32([0]), 1, p.batch.num_blocks)
+    rows, rlse = dsa.attn_decode(b, p.q[-1:].contiguous(), p.k, p.v)
+    for e in range(2):
+        check(rows[0, e], rlse[0, e], attend(p.q[-1, e], up[:, 0], big[:, 0], d ** -0.5, p.dtype))
