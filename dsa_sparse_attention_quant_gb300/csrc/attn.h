@@ -9,6 +9,11 @@
 
 namespace dsa {
 
+// All but the page copies' kernels are launched while the stream's previous kernel
+// runs, and wait for it before they read anything. What they read behind that wait
+// is read with plain loads: __ldg and const __restrict__ are for what nobody writes
+// as long as the kernel lives, and such loads may move ahead of the wait.
+
 // Single query rows over the paged cache (attn_rows.cu). Strides in elements.
 struct RowsArgs {
   const void *q, *k, *v;

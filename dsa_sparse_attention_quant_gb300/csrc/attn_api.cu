@@ -82,14 +82,20 @@ struct RowsPlan {
 
 // Two CTAs per SM on a part of up to 160 SMs.
 constexpr int kRowsCtas = 320;
-// Tokens of up to this many tiles are not cut while a CTA for each fits on the
-// GPU at once: it streams such a row in about the time that the join's launch
-// takes. More CTAs than that run as slices, whose loads go on across tokens.
+// Tokens of up to this many tiles are not cut while the CTAs are few: one streams
+// such a row in about the time that the join's launch takes. GPU time, 32/8 heads
+// of 128: one request of 256 keys 5.7 us (cut from 2 tiles on: 7.1), of 768 7.9 (cut
+// from 16 on: 11.5); one of 512 takes 8.5, cut 7.5.
 constexpr int kDirectTiles = 8;
-// The least slice: shorter ones pay more for their partials than they save.
-constexpr int kMinTiles = 2;
-
+// More CTAs than this run as slices, whose loads go on across tokens: two on each of
+// a GB300's 152 SMs. It is a number, not the device's, so that the scratch's size
+// and the run decide alike. 32 requests of 512 keys, 32/8 heads: 10.6 us (with 152:
+// 15.2); 64 of them 29.3 (with 608: 26.5).
 constexpr int kDirectCtas = 304;
+// The least slice, in tiles: shorter ones pay more for their partials than they save
+// (2 requests of 4096 keys, 40/1 heads: 14.3 us, with 1 tile 18.5; one of 768,
+// 32/8: 7.9, with 4 tiles 9.1).
+constexpr int kMinTiles = 2;
 
 // One slice per CTA place: cut two or four times finer, so that CTAs that stream
 // slower take less, the partials and the CTAs' starts cost more than that gains

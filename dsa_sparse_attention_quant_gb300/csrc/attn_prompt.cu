@@ -14,13 +14,17 @@
 //
 // What bounds it: 4*D operations per (query head, visible pair), the bf16 /
 // fp16 rate of the tensor cores, with 128x128 tiles of S needing one exponential
-// per 4*D operations beside it. Measured: 4 x 8192, 64/8 heads of 128, 2.58 to
-// 2.79 ms (1705 to 1580 TFLOP/s, power-capped; 2 x 8192, 32/8 heads: 1730);
-// 2 x 8192, 32/8 heads of 64, 493 us (1115 TFLOP/s): there a tile pair's
+// per 4*D operations beside it. Measured: 4 x 8192, 64/8 heads of 128, 2.54 ms in
+// single calls at 2070 MHz (1730 TFLOP/s), 2.75 ms one call after the other under the
+// power cap, at 1840 MHz in the median (1600);
+// 2 x 8192, 32/8 heads of 64, 497 us (1105 TFLOP/s): there a tile pair's
 // exponentials and the rest of its softmax, 2100 cycles, outlast its MMAs, 1024.
 // Short prompts are a chain per unit (scores, weights, P V, the store), 9000
-// cycles: 512 prompts of 128, 16/2 heads of 128, 144 us; one of 509, 11.6 us
+// cycles: 512 prompts of 128, 16/2 heads of 128, 144 us; one of 509, 11.4 us
 // (14.4 when it did not start while the previous kernel drained).
+// A unit's keys are not split: few query rows behind many keys are as many chains
+// as there are units (128 tokens behind 128K keys, 32/8 heads: 16 units, 1.33 ms for
+// 0.14 of operations; 8 tokens the same, 0.08 of bytes).
 //
 // Mapping: a CTA holds two query tiles of 128 rows that share one stream of
 // K and V tiles (128 keys): two query heads of one KV head where the group is

@@ -14,15 +14,19 @@
 //
 // What bounds it: one read of the K and V rows, 4*D bytes per (key, KV head)
 // for 4*G*D operations: HBM for the usual G. Measured, 64/8 heads of 128: 8
-// requests of 128K keys 606 us (7.06 TB/s), 32 of 4K to 8K keys 125 us
-// (6.5 TB/s), 64 tokens of 2048 selected slots 101 us (5.4 TB/s: single 256-byte
-// rows); one request of 300 keys 9 us, the host's time for the call. 64/1 heads,
-// 8 requests of 32K keys, 60 us: there the MMAs and their fragments bound it.
+// requests of 128K keys 606 us (7.06 TB/s), 32 of 4K to 8K keys 127 us
+// (6.4 TB/s), 64 tokens of 2048 selected slots 100 us (5.4 TB/s: single 256-byte
+// rows); one request of 300 keys 9 to 10 us, the host's time for the call. 8 requests
+// of 32K keys: 64/1 heads 64 us, 128/1 101, the keys alone 20: there the MMAs and
+// their fragments bound it. 4096 tokens of one request, 2048 of 32K slots each,
+// 64/8 heads: 4.5 ms, every row fetched through L2 for each token (34 GB, 7.5 TB/s).
 // The G query heads of a KV head
 // form one 16-row MMA tile, so K and V are read once for all of them; G > 16
 // takes 32-row tiles (two 16-row MMA tiles on the same K and V fragments) and
 // one pass over the keys per 32 heads, the passes' CTAs next to each other so
-// that the later pass finds K and V in L2.
+// that the later pass finds K and V in L2. Tokens of one request share nothing: n
+// decode tokens read its pages n times (8 requests of 128K, 32/8 heads: one token
+// each 0.62 ms, four 2.36).
 //
 // Mapping: the (token, 64-key tile) pairs form one flat list, cut into equally
 // long slices whatever the mix of lengths; a slice is run by one CTA per KV
@@ -701,8 +705,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
 // The tokens cut by slice boundaries: for the token and head that main CTA b
 // began, CTA (b, y) adds the partials of rows y * 8 / WAYS and following. WAYS
 // warps share a row, taking its slices in turn, each in order; their sums are
-// added in warp order. Many slices per token want all eight warps on a row (1
-// token of 131072 keys: 38 partials a row), few want a warp per row.
+// added in warp order. More than four slices per token want all eight warps on a
+// row (one of 131072 keys, 32/8 heads: 38 partials a row, 83 us, with a warp per row
+// 93), fewer a warp per row (32 of 2048, 64/8: 48.4 us, with eight 50.4).
 constexpr int kJoinWarps = 8;
 
 template <int D, typename T, int WAYS>

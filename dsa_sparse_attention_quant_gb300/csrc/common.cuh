@@ -29,9 +29,7 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 
 // Launch `kernel` so that it may start while the previous kernel of the
 // stream is still running; the kernel calls pdl_wait() before it reads that
-// kernel's results, and with plain loads: __ldg and const __restrict__ are for what
-// nobody writes as long as the kernel lives, and such loads may move ahead of the
-// wait. Stream capture keeps the relation as a programmatic edge.
+// kernel's results. Stream capture keeps the relation as a programmatic edge.
 template <typename... Params, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                        Args&&... args) {

@@ -7,11 +7,12 @@
 // first in the order of the request list, and the k-th page that compaction
 // moves goes to the k-th hole. The byte moves are bound by HBM, one read and
 // one write of every moved page; the bookkeeping by a few dependent reads.
-// Measured: 32768 rows of 8 x 128 written in 40 to 42 us (6.5 TB/s, read and
-// write); 0.5 GB of pages moved by a compaction over 8 caches in 171 us (5.8 TB/s
-// with the plan); 64 forks over 16 caches 12 us on the GPU, about 28 us of host
-// time. Each call's first kernel is launched while the stream's previous one
-// drains (rows 44.2 -> 41.6 us).
+// Measured: 32768 rows of 8 x 128 written in 40 us (6.7 TB/s, read and write);
+// 0.5 GB of pages moved by a compaction over 8 caches in 170 to 174 us (5.8 TB/s with
+// the plan); 1024 pages copied over 4 caches in 180 us (6.0 TB/s with the claims), 64
+// over 16 in 54; 64 forks over 16 caches 12 us on the GPU, about 30 us of host time.
+// Each call's first kernel is launched while the stream's previous one drains (rows
+// 44.2 -> 41.6 us), but for the page copies, whose claims begin with memsets.
 #include "attn.h"
 #include "common.cuh"
 
