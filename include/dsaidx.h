@@ -466,6 +466,7 @@ DSA_API int dsa_attn_selected(const DsaKv *kv, const DsaAttn *attn, const int32_
  *             heads, head_dim] (kv->num_blocks = rows, the slot stride is the
  *             row stride, no page stride) and key s of request r is row
  *             kv_start[r] + s; the block table is not used and may be NULL
+ * batch->req_id_per_token is not read, but may not be NULL.
  * Flags: DSA_DEVERR_SEQ_RANGE (negative q_len, query tokens before
  * num_decode_tokens or beyond num_tokens: the request is refused, none of its
  * rows is written; seq_len negative or beyond the block-table row, max_seq_len
