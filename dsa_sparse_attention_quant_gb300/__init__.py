@@ -30,12 +30,20 @@ from .binding import (  # noqa: F401
 )
 from .attention import (  # noqa: F401
     attn_decode,
+    attn_decode8,
+    attn_decode8_workspace_size,
     attn_decode_workspace_size,
     attn_prompt,
     attn_selected,
+    attn_selected8,
+    attn_selected8_workspace_size,
     attn_selected_workspace_size,
+    kv_read8,
     kv_write,
+    kv_write8,
+    kv_write8_workspace_size,
     new_kv_cache,
+    new_kv_cache8,
     pages_compact,
     pages_copy,
     pages_fork,

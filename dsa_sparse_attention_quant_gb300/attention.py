@@ -1,6 +1,6 @@
-"""The attention that reads the paged KV cache, the cache's writer and its page
-calls: argument marshalling for the entry points of ``include/dsaidx.h`` that
-take a ``DsaKv`` or ``DsaPages``.
+"""The attention that reads the paged KV cache, in 16 or in 8 bits, the cache's
+writers and its page calls: argument marshalling for the entry points of
+``include/dsaidx.h`` that take a ``DsaKv``, ``DsaKv8`` or ``DsaPages``.
 
 Tensors are on the current CUDA device. Results and scratch are allocated with
 torch when the caller does not pass them, with ``stream`` given as that
@@ -14,9 +14,10 @@ import struct
 
 import torch
 
-from .binding import DsaAttnC, DsaCacheDescC, DsaError, DsaKvC, DsaPagesC, _check, load
+from .binding import DsaAttnC, DsaCacheDescC, DsaError, DsaKv8C, DsaKvC, DsaPagesC, _check, load
 
 BLOCK_SIZE = 64
+SCALE_BLOCK = 16  # slots of a page that share a scale in an 8-bit cache
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 # torch.cuda.current_device() without its check that CUDA is up: asked only once a CUDA tensor is at hand
 _device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
@@ -31,15 +32,30 @@ def new_kv_cache(num_blocks: int, num_kv_heads: int, head_dim: int, dtype=torch.
     return torch.zeros(shape, dtype=dtype, device=dev), torch.zeros(shape, dtype=dtype, device=dev)
 
 
+def new_kv_cache8(num_blocks: int, num_kv_heads: int, head_dim: int, device=None):
+    """A zeroed 8-bit cache: K and V codes [num_blocks, 64, num_kv_heads, head_dim]
+    (float8_e4m3fn) and their scales [num_blocks, 4, num_kv_heads, 2] (float32; K's
+    and V's of each 16 slots and head). A row's values are codes * scale."""
+    if head_dim not in (64, 128) or num_blocks < 1 or num_kv_heads < 1:
+        raise DsaError("an 8-bit KV cache has rows of 64 or 128, at least one page and one head")
+    dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
+    n, heads = int(num_blocks), int(num_kv_heads)
+    codes = [torch.zeros((n, BLOCK_SIZE, heads, int(head_dim)), dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+             for _ in range(2)]
+    return (*codes, torch.zeros((n, BLOCK_SIZE // SCALE_BLOCK, heads, 2), dtype=torch.float32, device=dev))
+
+
 # ---------------------------------------------------------------- arguments
 # A decode step makes these calls once per layer, so their host time counts: the
 # C structs are packed with ``struct`` (their layout is checked against ctypes
 # below) and every check is one or two cheap tensor queries.
 
 _KV = struct.Struct("PPiii4xq6q")         # DsaKv
+_KV8 = struct.Struct("PPPiii4xq9q")       # DsaKv8
 _ATTN = struct.Struct("PqqPqqPif")        # DsaAttn
 _PAGES = struct.Struct("PqPqi4xP")        # DsaPages
-assert (_KV.size, _ATTN.size, _PAGES.size) == tuple(ctypes.sizeof(c) for c in (DsaKvC, DsaAttnC, DsaPagesC))
+assert (_KV.size, _KV8.size, _ATTN.size, _PAGES.size) == tuple(ctypes.sizeof(c) for c in (DsaKvC, DsaKv8C, DsaAttnC,
+                                                                                          DsaPagesC))
 
 
 def _here(t, what, dtype=None):
@@ -88,6 +104,31 @@ def _kv(k, v, packed=False):
         raise DsaError("k and v must be [num_blocks, 64, heads, head_dim]")
     n, _, heads, d = shape
     return _KV.pack(k.data_ptr(), v.data_ptr(), code, heads, d, n, *ks[:3], *vs[:3]), heads, d, dtype
+
+
+def _kv8(k, v, scale, rows, what):
+    """(C description, heads, head_dim, dtype) of an 8-bit cache's codes
+    [num_blocks, 64, heads, head_dim] and scales [num_blocks, 4, heads, 2], for
+    rows (``what``) in 16 bits; any strides with a contiguous last axis."""
+    _here(k, "k_cache", torch.float8_e4m3fn)
+    shape, dev = k.shape, k.get_device()
+    if not isinstance(v, torch.Tensor) or v.get_device() != dev or v.dtype is not k.dtype or v.shape != shape:
+        _here(v, "v_cache", torch.float8_e4m3fn)
+        raise DsaError("k_cache and v_cache must have one shape")
+    if len(shape) != 4 or shape[1] != BLOCK_SIZE:
+        raise DsaError("k_cache and v_cache must be [num_blocks, 64, heads, head_dim]")
+    n, _, heads, d = shape
+    if _here(scale, "kv_scale", torch.float32).shape != (n, BLOCK_SIZE // SCALE_BLOCK, heads, 2):
+        raise DsaError("kv_scale must be [num_blocks, 4, heads, 2]")
+    ks, vs, ss = k.stride(), v.stride(), scale.stride()
+    if ks[3] != 1 or vs[3] != 1 or ss[3] != 1:
+        raise DsaError("k_cache, v_cache and kv_scale must have a contiguous last axis")
+    dtype = _here(rows, what).dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise DsaError(f"{what} must be bf16 or fp16, got {dtype}")
+    return (_KV8.pack(k.data_ptr(), v.data_ptr(), scale.data_ptr(), code, heads, d, n, *ks[:3], *vs[:3], *ss[:3]), heads,
+            d, dtype)
 
 
 def _made(stream, shape, dtype, device, rest):
@@ -231,6 +272,95 @@ def attn_prompt(batch, q, k, v, scale: float = 0.0, kv_start=None, out=None, lse
     at, out, lse, _ = _attn(q, out, lse, kv_heads, d, dtype, scale, batch.num_tokens, False, stream)
     st = load().dsa_attn_prompt(ctypes.byref(batch.c), kv, start, at, _err(dev_err), _on(stream))
     _check(st, "dsa_attn_prompt")
+    return out, lse
+
+
+# ---------------------------------------------------------------- 8-bit cache
+
+def kv_write8_workspace_size(n_tokens: int, num_blocks: int) -> int:
+    return int(load().dsa_kv_write8_workspace_size(int(n_tokens), int(num_blocks)))
+
+
+def kv_write8(k, v, slot_mapping, k_cache, v_cache, kv_scale, ws=None, dev_err=None, stream=None):
+    """Quantise the rows k and v [tokens, heads, head_dim] (bf16 or fp16) into the
+    8-bit cache (``new_kv_cache8``) at their slots (int64, -1 = padding). A block's
+    scale is made anew when its first slot is written and may rise after that, which
+    rounds the rows that are there to the raised one."""
+    kv, heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, k, "k rows")
+    n = _dense(slot_mapping, "slot_mapping", torch.int64).numel()
+    want = (n, heads, d)
+    for t, what in ((k, "k rows"), (v, "v rows")):
+        if _here(t, what, dtype).shape != want:
+            raise DsaError(f"{what} must be [{n}, {heads}, {d}]")
+        if t.stride(2) != 1:
+            raise DsaError(f"{what} must have a contiguous last axis")
+    if n == 0:
+        return
+    ws = _scratch(ws, lambda: kv_write8_workspace_size(n, k_cache.shape[0]), k.device, stream)
+    st = load().dsa_kv_write8(k.data_ptr(), *k.stride()[:2], v.data_ptr(), *v.stride()[:2], n, slot_mapping.data_ptr(),
+                              kv, ws.data_ptr(), ws.numel(), _err(dev_err), _on(stream))
+    _check(st, "dsa_kv_write8")
+
+
+def kv_read8(batch, k_cache, v_cache, kv_scale, kv_start, k, v, past: bool = False, dev_err=None, stream=None):
+    """Read sequences back from the 8-bit cache: key s of each request r with
+    kv_start[r] >= 0 (int32 [num_reqs]) into row kv_start[r] + s of k and v [rows,
+    heads, head_dim] (bf16 or fp16), as ``attn_prompt`` takes packed keys; with
+    ``past`` without the request's own query tokens. Other rows stay as they were.
+    Returns (k, v)."""
+    kv, heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, k, "k rows")
+    rows, rheads, rd, _ = _kv(k, v, packed=True)
+    if (rheads, rd) != (heads, d):
+        raise DsaError(f"k and v rows must be [rows, {heads}, {d}]")
+    _here(batch.seq_lens, "the batch")
+    if _dense(kv_start, "kv_start", torch.int32).numel() < batch.num_reqs:
+        raise DsaError("kv_start needs an entry per request")
+    if k.shape[0] == 0:
+        return k, v
+    st = load().dsa_kv_read8(ctypes.byref(batch.c), kv, kv_start.data_ptr(), rows, 1 if past else 0, _err(dev_err),
+                             _on(stream))
+    _check(st, "dsa_kv_read8")
+    return k, v
+
+
+def attn_decode8_workspace_size(batch, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(load().dsa_attn_decode8_workspace_size(ctypes.byref(batch.c), int(num_heads), int(num_kv_heads),
+                                                      int(head_dim)))
+
+
+def attn_decode8(batch, q, k_cache, v_cache, kv_scale, scale: float = 0.0, out=None, lse=None, ws=None, dev_err=None,
+                 stream=None):
+    """``attn_decode`` over an 8-bit cache (``new_kv_cache8``); q is bf16 or fp16."""
+    kv, kv_heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, q, "q")
+    _here(batch.seq_lens, "the batch")
+    n = batch.num_decode_tokens
+    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, dtype, scale, n, n == q.shape[0], stream)
+    ws = _scratch(ws, lambda: attn_decode8_workspace_size(batch, heads, kv_heads, d), q.device, stream)
+    st = load().dsa_attn_decode8(ctypes.byref(batch.c), kv, at, ws.data_ptr(), ws.numel(), _err(dev_err), _on(stream))
+    _check(st, "dsa_attn_decode8")
+    return out, lse
+
+
+def attn_selected8_workspace_size(n_tokens: int, topk: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(load().dsa_attn_selected8_workspace_size(int(n_tokens), int(topk), int(num_heads), int(num_kv_heads),
+                                                        int(head_dim)))
+
+
+def attn_selected8(q, k_cache, v_cache, kv_scale, physical, scale: float = 0.0, out=None, lse=None, ws=None,
+                   dev_err=None, stream=None):
+    """``attn_selected`` over an 8-bit cache (``new_kv_cache8``); q is bf16 or fp16."""
+    kv, kv_heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, q, "q")
+    shape = _dense(physical, "physical", torch.int32).shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise DsaError("physical must be [tokens, topk]")
+    n, topk = shape
+    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, dtype, scale, n, True, stream)
+    if q.shape[0] != n:
+        raise DsaError(f"q has {q.shape[0]} rows, physical {n}")
+    ws = _scratch(ws, lambda: attn_selected8_workspace_size(n, topk, heads, kv_heads, d), q.device, stream)
+    st = load().dsa_attn_selected8(kv, at, physical.data_ptr(), n, topk, ws.data_ptr(), ws.numel(), _err(dev_err),
+                                   _on(stream))
+    _check(st, "dsa_attn_selected8")
     return out, lse
 
 

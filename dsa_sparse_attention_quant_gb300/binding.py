@@ -49,6 +49,8 @@ SYMBOLS = [
     "dsa_kv_write", "dsa_attn_decode_workspace_size", "dsa_attn_decode", "dsa_attn_selected_workspace_size",
     "dsa_attn_selected", "dsa_attn_prompt", "dsa_pages_workspace_size", "dsa_pages_copy", "dsa_pages_fork",
     "dsa_pages_free", "dsa_pages_compact",
+    "dsa_kv_write8_workspace_size", "dsa_kv_write8", "dsa_kv_read8", "dsa_attn_decode8_workspace_size",
+    "dsa_attn_decode8", "dsa_attn_selected8_workspace_size", "dsa_attn_selected8",
 ]
 STATIC_WORKSPACE_BYTES = 32 << 20
 
@@ -120,6 +122,27 @@ class DsaKvC(ctypes.Structure):
         ("v_page_stride", ctypes.c_int64),
         ("v_slot_stride", ctypes.c_int64),
         ("v_head_stride", ctypes.c_int64),
+    ]
+
+
+class DsaKv8C(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int64),
+        ("k_page_stride", ctypes.c_int64),
+        ("k_slot_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_page_stride", ctypes.c_int64),
+        ("v_slot_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("s_page_stride", ctypes.c_int64),
+        ("s_block_stride", ctypes.c_int64),
+        ("s_head_stride", ctypes.c_int64),
     ]
 
 
@@ -201,6 +224,13 @@ def load(build_if_missing: bool = True):
             "dsa_attn_selected_workspace_size": (SZ, [I64, I32, I32, I32, I32]),
             "dsa_attn_selected": (ctypes.c_int, [P, P, P, I64, I32, P, SZ, P, P]),
             "dsa_attn_prompt": (ctypes.c_int, [P, P, P, P, P, P]),
+            "dsa_kv_write8_workspace_size": (SZ, [I64, I64]),
+            "dsa_kv_write8": (ctypes.c_int, [P, I64, I64, P, I64, I64, I64, P, P, P, SZ, P, P]),
+            "dsa_kv_read8": (ctypes.c_int, [P, P, P, P, I32, P, P]),
+            "dsa_attn_decode8_workspace_size": (SZ, [P, I32, I32, I32]),
+            "dsa_attn_decode8": (ctypes.c_int, [P, P, P, P, SZ, P, P]),
+            "dsa_attn_selected8_workspace_size": (SZ, [I64, I32, I32, I32, I32]),
+            "dsa_attn_selected8": (ctypes.c_int, [P, P, P, I64, I32, P, SZ, P, P]),
             "dsa_pages_workspace_size": (SZ, [I64, I32]),
             "dsa_pages_copy": (ctypes.c_int, [P, I32, I64, P, P, I32, P, SZ, P, P]),
             "dsa_pages_fork": (ctypes.c_int, [P, P, P, I32, P, I32, P, SZ, P, P]),

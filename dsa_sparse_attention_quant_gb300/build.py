@@ -19,8 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libdsaidx.so")
 SOURCES = ["api.cu", "quant.cu", "plan.cu", "logits.cu", "topk.cu", "noalloc.cu", "gather.cu",
-           "attn_rows.cu", "attn_prompt.cu", "pages.cu", "attn_api.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "kernels.h", "host.h", "attn.h")] + [os.path.join(ROOT, "include", "dsaidx.h")]
+           "attn_rows.cu", "attn_rows8.cu", "attn_prompt.cu", "kv8.cu", "pages.cu", "attn_api.cu"]
+HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "kernels.h", "host.h", "attn.h", "attn_rows.cuh")] + [os.path.join(ROOT, "include", "dsaidx.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

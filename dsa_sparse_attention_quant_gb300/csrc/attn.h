@@ -45,6 +45,52 @@ struct RowsArgs {
 };
 cudaError_t launch_attn_rows(const RowsArgs& a, int head_dim, int dtype, bool selected, cudaStream_t stream);
 
+// The parts that the main kernel's slices left, added (attn_rows.cu): grid main CTAs,
+// krows rows of the workspace each.
+cudaError_t launch_attn_join(const RowsArgs& a, int head_dim, int dtype, int grid, int krows, cudaStream_t stream);
+
+// The same rows over a cache of E4M3 codes (attn_rows8.cu): k, v and their strides
+// count bytes, the scales' strides count fp32 numbers.
+struct Rows8Args : RowsArgs {
+  const float* scale;  // [pages, 4, heads, 2]: a block of 16 slots' K and V scale
+  int64_t s_page, s_block, s_head;
+};
+cudaError_t launch_attn_rows8(const Rows8Args& a, int head_dim, int dtype, bool selected, cudaStream_t stream);
+
+// The cache of E4M3 codes, written and read back (kv8.cu). Strides as in Rows8Args;
+// those of 16-bit rows in elements of 2 bytes.
+struct Cache8Args {
+  uint8_t *k, *v;
+  float* scale;
+  int64_t k_page, k_slot, k_head, v_page, v_slot, v_head, s_page, s_block, s_head;
+  int hkv;
+  int64_t num_blocks;
+};
+struct Write8Args {
+  Cache8Args c;
+  const uint16_t *k, *v;
+  int64_t k_row, k_rhead, v_row, v_rhead;
+  int64_t n_tokens;
+  const int64_t* slot_mapping;
+  int32_t* token_of;  // [slots]: the last token with that slot, or anything; nullptr: few tokens
+  int32_t* err;
+};
+constexpr int kWrite8Few = 512;  // up to this many tokens: one launch, without token_of
+cudaError_t launch_kv_write8(const Write8Args& a, int head_dim, int dtype, cudaStream_t stream);
+
+struct Read8Args {
+  Cache8Args c;
+  uint16_t *k, *v;
+  int64_t k_row, k_rhead, v_row, v_rhead;
+  int64_t rows;  // of k and v
+  const int32_t *qsl, *seq_lens, *block_table, *kv_start;
+  int64_t bt_stride;
+  int num_reqs, max_keys;
+  bool past;  // without the requests' own query tokens
+  int32_t* err;
+};
+cudaError_t launch_kv_read8(const Read8Args& a, int head_dim, int dtype, int num_sms, cudaStream_t stream);
+
 // K and V rows into the paged cache (pages.cu). Strides in elements of 2 bytes.
 struct KvWriteArgs {
   const uint16_t *k, *v;

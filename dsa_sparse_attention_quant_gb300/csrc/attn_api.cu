@@ -52,6 +52,39 @@ int check_attn(const DsaAttn* at, const DsaKv& kv, int64_t rows, DsaAttn* out) {
   return DSA_OK;
 }
 
+// The 8-bit cache's description with the strides of one-element axes made valid;
+// sizes: heads, head_dim, pages and type as DsaKv has them.
+int check_kv8(const DsaKv8* kv, DsaKv8* out, DsaKv* sizes) {
+  if (kv == nullptr) return DSA_EINVAL;
+  *out = *kv;
+  if (kv->dtype != DSA_BF16 && kv->dtype != DSA_FP16) return DSA_EINVAL;
+  if (kv->num_kv_heads < 1 || kv->num_kv_heads > 65535 || (kv->head_dim != 64 && kv->head_dim != 128))
+    return DSA_EINVAL;
+  if (kv->num_blocks < 1 || kv->num_blocks > INT_MAX / kBlock) return DSA_EINVAL;
+  if (!kv->k || !kv->v || !kv->scale || !aligned16(kv->k) || !aligned16(kv->v) || !aligned16(kv->scale))
+    return DSA_EINVAL;
+  const int d = kv->head_dim;
+  if (kv->num_kv_heads == 1) {
+    out->k_head_stride = out->v_head_stride = d;
+    out->s_head_stride = 2;
+  }
+  if (kv->num_blocks == 1) {
+    out->k_page_stride = out->v_page_stride = d;
+    out->s_page_stride = 2;
+  }
+  for (int64_t s : {out->k_page_stride, out->k_slot_stride, out->k_head_stride, out->v_page_stride,
+                    out->v_slot_stride, out->v_head_stride})
+    if (!stride_ok(s, d) || s % 16 != 0) return DSA_EINVAL;
+  for (int64_t s : {out->s_page_stride, out->s_block_stride, out->s_head_stride})
+    if (s < 2 || s % 2 != 0 || s >= kMaxStride) return DSA_EINVAL;
+  *sizes = DsaKv{};
+  sizes->dtype = kv->dtype;
+  sizes->num_kv_heads = kv->num_kv_heads;
+  sizes->head_dim = d;
+  sizes->num_blocks = kv->num_blocks;
+  return DSA_OK;
+}
+
 // pages: the call reads the block table.
 int check_step(const DsaBatch* b, bool pages) {
   if (b == nullptr) return DSA_EINVAL;
@@ -100,10 +133,12 @@ constexpr int kMinTiles = 2;
 // One slice per CTA place: cut two or four times finer, so that CTAs that stream
 // slower take less, the partials and the CTAs' starts cost more than that gains
 // (32 requests of 4K to 8K keys: 130.8, 134.4, 145.0 us).
-RowsPlan rows_plan(int64_t tokens, int64_t keys, int heads, int hkv, int head_dim, int ctas) {
+// least: the query heads of the kernel's smallest tile.
+RowsPlan rows_plan(int64_t tokens, int64_t keys, int heads, int hkv, int head_dim, int least, int ctas) {
   RowsPlan p{};
   const int group = heads / hkv;
-  p.rows = group <= 16 ? 16 : 32;
+  p.rows = least;
+  while (p.rows < 32 && p.rows < group) p.rows *= 2;
   p.passes = (group + p.rows - 1) / p.rows;
   const int64_t tiles = keys > 0 ? (keys + kBlock - 1) / kBlock : 1;
   p.split = tiles > kDirectTiles || tokens * hkv * p.passes > kDirectCtas;
@@ -123,6 +158,8 @@ RowsPlan rows_plan(int64_t tokens, int64_t keys, int heads, int hkv, int head_di
   }
   return p;
 }
+
+constexpr int kLeast16 = 16, kLeast8 = 8;  // of attn_rows.cu and attn_rows8.cu
 
 bool heads_ok(int32_t heads, int32_t hkv, int32_t head_dim) {
   return hkv >= 1 && heads >= 1 && heads <= 65535 && heads % hkv == 0 && (head_dim == 64 || head_dim == 128);
@@ -155,16 +192,52 @@ RowsArgs rows_args(const DsaKv& kv, const DsaAttn& at) {
   return a;
 }
 
-int run_rows(RowsArgs& a, int64_t tokens, int64_t keys, const DsaKv& kv, bool selected, void* ws, size_t ws_bytes,
-             cudaStream_t stream) {
-  RowsPlan need = rows_plan(tokens, keys, a.heads, a.hkv, kv.head_dim, kRowsCtas);
+Rows8Args rows8_args(const DsaKv8& kv, const DsaKv& sizes, const DsaAttn& at) {
+  Rows8Args a{};
+  static_cast<RowsArgs&>(a) = rows_args(sizes, at);
+  a.k = kv.k;
+  a.v = kv.v;
+  a.k_page = kv.k_page_stride;
+  a.k_slot = kv.k_slot_stride;
+  a.k_head = kv.k_head_stride;
+  a.v_page = kv.v_page_stride;
+  a.v_slot = kv.v_slot_stride;
+  a.v_head = kv.v_head_stride;
+  a.scale = kv.scale;
+  a.s_page = kv.s_page_stride;
+  a.s_block = kv.s_block_stride;
+  a.s_head = kv.s_head_stride;
+  return a;
+}
+
+Cache8Args cache8_args(const DsaKv8& kv) {
+  return Cache8Args{kv.k,
+                    kv.v,
+                    kv.scale,
+                    kv.k_page_stride,
+                    kv.k_slot_stride,
+                    kv.k_head_stride,
+                    kv.v_page_stride,
+                    kv.v_slot_stride,
+                    kv.v_head_stride,
+                    kv.s_page_stride,
+                    kv.s_block_stride,
+                    kv.s_head_stride,
+                    kv.num_kv_heads,
+                    kv.num_blocks};
+}
+
+// launch(): the kernels with the finished arguments.
+template <typename F>
+int run_rows(RowsArgs& a, int64_t tokens, int64_t keys, int head_dim, int least, void* ws, size_t ws_bytes, F launch) {
+  RowsPlan need = rows_plan(tokens, keys, a.heads, a.hkv, head_dim, least, kRowsCtas);
   if (need.ctas > INT_MAX) return DSA_EINVAL;
   if (need.bytes > 0 && (ws == nullptr || !aligned16(ws))) return DSA_EINVAL;
   if (ws_bytes < need.bytes) return DSA_ENOSPACE;
   int sms;
   int st = device_sms(&sms);
   if (st != DSA_OK) return st;
-  const RowsPlan p = rows_plan(tokens, keys, a.heads, a.hkv, kv.head_dim, 2 * sms < kRowsCtas ? 2 * sms : kRowsCtas);
+  const RowsPlan p = rows_plan(tokens, keys, a.heads, a.hkv, head_dim, least, 2 * sms < kRowsCtas ? 2 * sms : kRowsCtas);
   a.n_tokens = static_cast<int>(tokens);
   a.passes = p.passes;
   a.slices = static_cast<int>(p.slices);
@@ -175,7 +248,19 @@ int run_rows(RowsArgs& a, int64_t tokens, int64_t keys, const DsaKv& kv, bool se
     a.part_ml = reinterpret_cast<float2*>(base + p.off_ml);
     a.part_o = reinterpret_cast<float*>(base + p.off_o);
   }
-  return from_cuda(launch_attn_rows(a, kv.head_dim, kv.dtype, selected, stream));
+  return from_cuda(launch());
+}
+
+// What a batch's decode tokens read.
+void set_decode(RowsArgs& a, const DsaBatch* batch, int32_t* dev_err) {
+  a.qsl = batch->query_start_loc;
+  a.seq_lens = batch->seq_lens;
+  a.req_id = batch->req_id_per_token;
+  a.block_table = batch->block_table;
+  a.bt_stride = batch->bt_stride;
+  a.num_reqs = batch->num_decodes;
+  a.max_keys = max_keys(batch);
+  a.err = dev_err;
 }
 
 // K or V as a 4-D tensor {head_dim, heads, slots, pages} (packed: {head_dim,
@@ -340,7 +425,7 @@ size_t dsa_attn_decode_workspace_size(const DsaBatch* batch, int32_t num_heads, 
                                       int32_t head_dim) {
   if (check_step(batch, true) != DSA_OK || !heads_ok(num_heads, num_kv_heads, head_dim)) return 0;
   return rows_plan(batch->num_decode_tokens, batch->num_reqs > 0 ? max_keys(batch) : 0, num_heads, num_kv_heads,
-                   head_dim, kRowsCtas)
+                   head_dim, kLeast16, kRowsCtas)
       .bytes;
 }
 
@@ -356,21 +441,15 @@ int dsa_attn_decode(const DsaBatch* batch, const DsaKv* kv, const DsaAttn* attn,
     return st;
   if (batch->num_blocks != c.num_blocks || batch->num_decodes < 1) return DSA_EINVAL;
   RowsArgs a = rows_args(c, at);
-  a.qsl = batch->query_start_loc;
-  a.seq_lens = batch->seq_lens;
-  a.req_id = batch->req_id_per_token;
-  a.block_table = batch->block_table;
-  a.bt_stride = batch->bt_stride;
-  a.num_reqs = batch->num_decodes;
-  a.max_keys = max_keys(batch);
-  a.err = dev_err;
-  return run_rows(a, batch->num_decode_tokens, a.max_keys, c, false, ws, ws_bytes, stream);
+  set_decode(a, batch, dev_err);
+  return run_rows(a, batch->num_decode_tokens, a.max_keys, c.head_dim, kLeast16, ws, ws_bytes,
+                  [&] { return launch_attn_rows(a, c.head_dim, c.dtype, false, stream); });
 }
 
 size_t dsa_attn_selected_workspace_size(int64_t n_tokens, int32_t topk, int32_t num_heads, int32_t num_kv_heads,
                                         int32_t head_dim) {
   if (n_tokens < 0 || n_tokens > INT_MAX || topk < 1 || !heads_ok(num_heads, num_kv_heads, head_dim)) return 0;
-  return rows_plan(n_tokens, topk, num_heads, num_kv_heads, head_dim, kRowsCtas).bytes;
+  return rows_plan(n_tokens, topk, num_heads, num_kv_heads, head_dim, kLeast16, kRowsCtas).bytes;
 }
 
 int dsa_attn_selected(const DsaKv* kv, const DsaAttn* attn, const int32_t* physical, int64_t n_tokens, int32_t topk,
@@ -386,7 +465,8 @@ int dsa_attn_selected(const DsaKv* kv, const DsaAttn* attn, const int32_t* physi
   a.physical = physical;
   a.topk = topk;
   a.err = dev_err;
-  return run_rows(a, n_tokens, topk, c, true, ws, ws_bytes, stream);
+  return run_rows(a, n_tokens, topk, c.head_dim, kLeast16, ws, ws_bytes,
+                  [&] { return launch_attn_rows(a, c.head_dim, c.dtype, true, stream); });
 }
 
 int dsa_attn_prompt(const DsaBatch* batch, const DsaKv* kv, const int32_t* kv_start, const DsaAttn* attn,
@@ -441,6 +521,109 @@ int dsa_attn_prompt(const DsaBatch* batch, const DsaKv* kv, const int32_t* kv_st
   a.tile_units = static_cast<int>(units);
   a.err = dev_err;
   return from_cuda(launch_attn_prompt(a, &mq, &mk, &mv, c.head_dim, c.dtype, stream));
+}
+
+size_t dsa_kv_write8_workspace_size(int64_t n_tokens, int64_t num_blocks) {
+  if (n_tokens <= kWrite8Few || n_tokens > INT_MAX || num_blocks < 1 || num_blocks > INT_MAX / kBlock) return 0;
+  return static_cast<size_t>(num_blocks) * kBlock * sizeof(int32_t);
+}
+
+int dsa_kv_write8(const void* k, int64_t k_row_stride, int64_t k_head_stride, const void* v, int64_t v_row_stride,
+                  int64_t v_head_stride, int64_t n_tokens, const int64_t* slot_mapping, const DsaKv8* kv, void* ws,
+                  size_t ws_bytes, int32_t* dev_err, dsa_stream_t stream) {
+  DsaKv8 c;
+  DsaKv sizes;
+  int st = check_kv8(kv, &c, &sizes);
+  if (st != DSA_OK) return st;
+  if (n_tokens < 0 || n_tokens > INT_MAX) return DSA_EINVAL;
+  if (c.num_kv_heads == 1) k_head_stride = v_head_stride = c.head_dim;
+  if (n_tokens <= 1) k_row_stride = v_row_stride = c.head_dim;
+  for (int64_t s : {k_row_stride, k_head_stride, v_row_stride, v_head_stride})
+    if (!stride_ok(s, c.head_dim)) return DSA_EINVAL;
+  if (n_tokens == 0) return DSA_OK;
+  if (!k || !v || !slot_mapping || !aligned16(k) || !aligned16(v)) return DSA_EINVAL;
+  const size_t need = dsa_kv_write8_workspace_size(n_tokens, c.num_blocks);
+  if (need > 0 && (ws == nullptr || !aligned16(ws))) return DSA_EINVAL;
+  if (ws_bytes < need) return DSA_ENOSPACE;
+  int sms;
+  if ((st = device_sms(&sms)) != DSA_OK) return st;
+  const Write8Args a{cache8_args(c), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
+                     k_row_stride, k_head_stride, v_row_stride, v_head_stride,
+                     n_tokens, slot_mapping, need > 0 ? static_cast<int32_t*>(ws) : nullptr, dev_err};
+  return from_cuda(launch_kv_write8(a, c.head_dim, c.dtype, stream));
+}
+
+int dsa_kv_read8(const DsaBatch* batch, const DsaKv8* kv, const int32_t* kv_start, const DsaKv* rows, int32_t past,
+                 int32_t* dev_err, dsa_stream_t stream) {
+  DsaKv8 c;
+  DsaKv sizes, out;
+  if (batch == nullptr || batch->num_reqs < 0 || batch->max_seq_len < 0) return DSA_EINVAL;
+  if (batch->num_reqs == 0) return DSA_OK;
+  int st = check_kv8(kv, &c, &sizes);
+  if (st != DSA_OK || (st = check_kv(rows, true, &out)) != DSA_OK) return st;
+  if (out.dtype != c.dtype || out.num_kv_heads != c.num_kv_heads || out.head_dim != c.head_dim) return DSA_EINVAL;
+  if (!batch->seq_lens || !batch->block_table || batch->bt_stride < 1 || batch->num_blocks != c.num_blocks ||
+      !kv_start || (past && !batch->query_start_loc))
+    return DSA_EINVAL;
+  const int keys = max_keys(batch);
+  if (keys > (1 << 27) - kBlock) return DSA_EINVAL;  // the blocks of 256 requests are counted in 32 bits
+  int sms;
+  if ((st = device_sms(&sms)) != DSA_OK) return st;
+  const Read8Args a{cache8_args(c), static_cast<uint16_t*>(out.k), static_cast<uint16_t*>(out.v),
+                    out.k_slot_stride, out.k_head_stride, out.v_slot_stride, out.v_head_stride,
+                    out.num_blocks, batch->query_start_loc, batch->seq_lens, batch->block_table, kv_start,
+                    batch->bt_stride, batch->num_reqs, keys, past != 0, dev_err};
+  return from_cuda(launch_kv_read8(a, c.head_dim, c.dtype, sms, stream));
+}
+
+size_t dsa_attn_decode8_workspace_size(const DsaBatch* batch, int32_t num_heads, int32_t num_kv_heads,
+                                       int32_t head_dim) {
+  if (check_step(batch, true) != DSA_OK || !heads_ok(num_heads, num_kv_heads, head_dim)) return 0;
+  return rows_plan(batch->num_decode_tokens, batch->num_reqs > 0 ? max_keys(batch) : 0, num_heads, num_kv_heads,
+                   head_dim, kLeast8, kRowsCtas)
+      .bytes;
+}
+
+int dsa_attn_decode8(const DsaBatch* batch, const DsaKv8* kv, const DsaAttn* attn, void* ws, size_t ws_bytes,
+                     int32_t* dev_err, dsa_stream_t stream) {
+  DsaKv8 c;
+  DsaKv sizes;
+  DsaAttn at;
+  int st = check_step(batch, true);
+  if (st != DSA_OK) return st;
+  if (batch->num_decode_tokens == 0) return DSA_OK;
+  if ((st = check_kv8(kv, &c, &sizes)) != DSA_OK ||
+      (st = check_attn(attn, sizes, batch->num_decode_tokens, &at)) != DSA_OK)
+    return st;
+  if (batch->num_blocks != c.num_blocks || batch->num_decodes < 1) return DSA_EINVAL;
+  Rows8Args a = rows8_args(c, sizes, at);
+  set_decode(a, batch, dev_err);
+  return run_rows(a, batch->num_decode_tokens, a.max_keys, c.head_dim, kLeast8, ws, ws_bytes,
+                  [&] { return launch_attn_rows8(a, c.head_dim, c.dtype, false, stream); });
+}
+
+size_t dsa_attn_selected8_workspace_size(int64_t n_tokens, int32_t topk, int32_t num_heads, int32_t num_kv_heads,
+                                         int32_t head_dim) {
+  if (n_tokens < 0 || n_tokens > INT_MAX || topk < 1 || !heads_ok(num_heads, num_kv_heads, head_dim)) return 0;
+  return rows_plan(n_tokens, topk, num_heads, num_kv_heads, head_dim, kLeast8, kRowsCtas).bytes;
+}
+
+int dsa_attn_selected8(const DsaKv8* kv, const DsaAttn* attn, const int32_t* physical, int64_t n_tokens, int32_t topk,
+                       void* ws, size_t ws_bytes, int32_t* dev_err, dsa_stream_t stream) {
+  DsaKv8 c;
+  DsaKv sizes;
+  DsaAttn at;
+  if (n_tokens < 0 || n_tokens > INT_MAX || topk < 1) return DSA_EINVAL;
+  if (n_tokens == 0) return DSA_OK;
+  int st = check_kv8(kv, &c, &sizes);
+  if (st != DSA_OK || (st = check_attn(attn, sizes, n_tokens, &at)) != DSA_OK) return st;
+  if (physical == nullptr) return DSA_EINVAL;
+  Rows8Args a = rows8_args(c, sizes, at);
+  a.physical = physical;
+  a.topk = topk;
+  a.err = dev_err;
+  return run_rows(a, n_tokens, topk, c.head_dim, kLeast8, ws, ws_bytes,
+                  [&] { return launch_attn_rows8(a, c.head_dim, c.dtype, true, stream); });
 }
 
 size_t dsa_pages_workspace_size(int64_t num_blocks, int32_t n) {

@@ -1,0 +1,333 @@
+// kv8.cu — the paged KV cache in 8 bits (sm_103a): rows quantised as they are
+// written, and sequences' rows read back in 16 bits.
+//
+// A block is 16 slots of a page and one KV head, K and V apart; its scale is a power
+// of two 2^e, a row's values are codes * 2^e. For the rows that a call writes into a
+// block, with amax their largest finite magnitude,
+//   need = the least 2^e, e >= -64, with amax / 2^e <= 448 (E4M3's largest code),
+//   scale = need if the block's first slot is written, else max(need, old scale),
+//   code = RN(x / scale), and RN(code * old / scale) for the block's other slots
+//   where the scale rises.
+// Powers of two make x / scale exact, so each value is rounded once, and a code that
+// moves to a higher scale is rounded again only where it falls below 2^-6. All of it
+// depends on the call's rows and the block alone, not on the order of the list or of
+// the threads.
+//
+// What bounds both: HBM, 4*D bytes of rows and 2*D of codes a (token, head).
+#include "attn.h"
+#include "common.cuh"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kScaleBlock = DSA_SCALE_BLOCK;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// The least power of two 2^e, e >= -64, with amax <= 448 * 2^e: amax = m*2^E (1 <= m
+// < 2) and 448 = 1.75*2^8, so e = E - 8, plus one when m > 1.75.
+__device__ __forceinline__ float scale_of(float amax) {
+  const uint32_t u = __float_as_uint(fmaxf(amax, 0x1p-64f));
+  return fmaxf(__uint_as_float(((u >> 23) - 8u + ((u & 0x7FFFFFu) > 0x600000u ? 1u : 0u)) << 23), 0x1p-64f);
+}
+
+// Two 16-bit values as fp32.
+__device__ __forceinline__ float2 wide(uint32_t x, __nv_bfloat16) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 wide(uint32_t x, __half) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+__device__ __forceinline__ uint32_t narrow(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t narrow(float a, float b, __half) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Bits of the type's infinity: magnitudes at or above it are not finite.
+__device__ __forceinline__ uint32_t inf_bits(__nv_bfloat16) { return 0x7F80u; }
+__device__ __forceinline__ uint32_t inf_bits(__half) { return 0x7C00u; }
+
+// Four codes as fp32.
+__device__ __forceinline__ void values(uint32_t codes, float2* lo, float2* hi) {
+  uint32_t a, b;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(codes));
+  *lo = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  *hi = __half22float2(*reinterpret_cast<const __half2*>(&b));
+}
+__device__ __forceinline__ uint32_t rescaled(uint32_t codes, float f) {
+  float2 lo, hi;
+  values(codes, &lo, &hi);
+  return e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
+}
+
+// ---------------------------------------------------------------------- write
+// Who writes a block: the call's tokens of a block are found by its slots, whatever
+// their places in the list. With few tokens a warp looks the list through; with many
+// a first kernel leaves each slot's last token in token_of, which needs no clearing:
+// an entry counts only if it names a token whose slot this is. Either way the token
+// at the block's lowest written slot takes the whole block.
+__global__ void __launch_bounds__(kThreads) write8_claim_kernel(const __grid_constant__ Write8Args a) {
+  pdl_wait();
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (t >= a.n_tokens) return;
+  const int64_t slot = a.slot_mapping[t], slots = a.c.num_blocks * kBlock;
+  if (slot < 0 || slot >= slots) return;
+  int32_t* at = a.token_of + slot;
+  int32_t seen = *reinterpret_cast<volatile int32_t*>(at);
+  while (true) {
+    // an entry of this call that is later in the list stands; each exchange that fails meets another token's
+    if (seen >= static_cast<int32_t>(t) && seen < a.n_tokens && a.slot_mapping[seen] == slot) return;
+    const int32_t was = atomicCAS(at, seen, static_cast<int32_t>(t));
+    if (was == seen) return;
+    seen = was;
+  }
+}
+
+// A warp: the rows of one block and head, K or V; src[r] = the token of slot r, or -1.
+template <int D, typename T>
+__device__ __forceinline__ void write_block(const Write8Args& a, int64_t block, const int32_t* src, int h, bool isv) {
+  constexpr int CH = D / 8;                  // 16-byte chunks of a new row
+  constexpr int RPI = 32 / CH;               // rows per load of the warp
+  constexpr int N = kScaleBlock / RPI;       // loads
+  const int lane = threadIdx.x & 31, ch = lane % CH, r0 = lane / CH;
+  const uint16_t* rows = (isv ? a.v : a.k) + h * (isv ? a.v_rhead : a.k_rhead);
+  const int64_t row = isv ? a.v_row : a.k_row;
+  const int64_t page = block / (kBlock / kScaleBlock), part = block % (kBlock / kScaleBlock);
+  const int64_t slot = isv ? a.c.v_slot : a.c.k_slot;
+  uint8_t* codes = (isv ? a.c.v + page * a.c.v_page + h * a.c.v_head : a.c.k + page * a.c.k_page + h * a.c.k_head) +
+                   part * kScaleBlock * slot;
+  float* scale = a.c.scale + page * a.c.s_page + part * a.c.s_block + h * a.c.s_head + (isv ? 1 : 0);
+
+  uint4 x[N];
+  bool in[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int32_t t = src[i * RPI + r0];
+    in[i] = t >= 0;
+    x[i] = in[i] ? *reinterpret_cast<const uint4*>(rows + t * row + ch * 8) : make_uint4(0, 0, 0, 0);
+  }
+  const bool opened = src[0] >= 0;
+  float old = opened ? 0.0f : *scale;
+  if (!(old > 0.0f && old < INFINITY)) old = 0.0f;  // nothing was written here
+  // the largest magnitude, by its bits; values that are not finite do not count
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (uint32_t w : {x[i].x, x[i].y, x[i].z, x[i].w}) most = __vmaxu2(most, w & 0x7FFF7FFFu);
+  const uint32_t inf = inf_bits(T());
+  if ((most & 0xFFFFu) >= inf || (most >> 16) >= inf) {
+    most = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (uint32_t w : {x[i].x, x[i].y, x[i].z, x[i].w}) {
+        const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
+        most = __vmaxu2(most, (lo < inf ? lo : 0u) | (hi < inf ? hi << 16 : 0u));
+      }
+  }
+  most = max(most & 0xFFFFu, most >> 16);
+  most = __reduce_max_sync(0xffffffffu, most);
+  const float s = fmaxf(scale_of(wide(most, T()).x), old);
+  const float inv = 1.0f / s;
+  if (old > 0.0f && s > old) {
+    // the rows that are there move to the higher scale
+    const float f = old * inv;
+    constexpr int CC = D / 16, RC = 32 / CC;
+    const int cc = lane % CC, q0 = lane / CC;
+#pragma unroll
+    for (int i = 0; i < kScaleBlock / RC; ++i) {
+      const int r = i * RC + q0;
+      if (src[r] >= 0) continue;
+      uint4* at = reinterpret_cast<uint4*>(codes + r * slot + cc * 16);
+      uint4 v = *at;
+      v = make_uint4(rescaled(v.x, f), rescaled(v.y, f), rescaled(v.z, f), rescaled(v.w, f));
+      *at = v;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (!in[i]) continue;
+    float2 f[4] = {wide(x[i].x, T()), wide(x[i].y, T()), wide(x[i].z, T()), wide(x[i].w, T())};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      // x - x: 0, or NaN for what is not finite, which has NaN as its code
+      f[k].x = fmaf(f[k].x, inv, f[k].x - f[k].x);
+      f[k].y = fmaf(f[k].y, inv, f[k].y - f[k].y);
+    }
+    *reinterpret_cast<uint2*>(codes + (i * RPI + r0) * slot + ch * 8) =
+        make_uint2(e4m3x4(f[0].x, f[0].y, f[1].x, f[1].y), e4m3x4(f[2].x, f[2].y, f[3].x, f[3].y));
+  }
+  __syncwarp();  // all have read the old scale
+  if (lane == 0) *scale = s;
+}
+
+// A CTA takes PER tokens of the list: a warp each finds its token's block, then all
+// warps share the blocks' heads.
+template <int D, typename T, int PER>
+__global__ void __launch_bounds__(kThreads) write8_kernel(const __grid_constant__ Write8Args a) {
+  __shared__ int32_t src[PER][kScaleBlock];
+  __shared__ int64_t block[PER];
+  __shared__ int lead[PER];
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t slots = a.c.num_blocks * kBlock;
+  for (int i = warp; i < PER; i += kWarps) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * PER + i;
+    const int64_t slot = t < a.n_tokens ? a.slot_mapping[t] : -1;
+    const bool ok = slot >= 0 && slot < slots;
+    if (slot != -1 && !ok && lane == 0) flag_error(a.err, DSA_DEVERR_SLOT_RANGE);
+    const int64_t b = slot / kScaleBlock;
+    int32_t mine = -1;  // lane r < 16: the token of the block's slot r
+    if (ok) {
+      if (a.token_of != nullptr) {
+        if (lane < kScaleBlock) {
+          const int32_t v = a.token_of[b * kScaleBlock + lane];
+          if (v >= 0 && v < a.n_tokens && a.slot_mapping[v] == b * kScaleBlock + lane) mine = v;
+        }
+      } else {
+        if (lane < kScaleBlock) src[i][lane] = -1;
+        __syncwarp();
+        for (int j = lane; j < a.n_tokens; j += 32) {
+          const int64_t other = a.slot_mapping[j];
+          if (other >= 0 && other / kScaleBlock == b) atomicMax(&src[i][other % kScaleBlock], j);
+        }
+        __syncwarp();
+        if (lane < kScaleBlock) mine = src[i][lane];
+      }
+    }
+    const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0);
+    const int32_t first = there ? __shfl_sync(0xffffffffu, mine, __ffs(there) - 1) : -1;
+    if (lane < kScaleBlock) src[i][lane] = mine;
+    if (lane == 0) {
+      block[i] = b;
+      lead[i] = ok && first == t;
+    }
+  }
+  __syncthreads();
+  const int each = 2 * a.c.hkv;
+  int at = warp;  // this warp's unit, counted over the blocks taken here
+#pragma unroll 1
+  for (int i = 0; i < PER; ++i) {
+    if (!lead[i]) continue;
+    for (; at < each; at += kWarps) write_block<D, T>(a, block[i], src[i], at >> 1, at & 1);
+    at -= each;
+  }
+}
+
+// ----------------------------------------------------------------------- read
+// A warp per (block of a request, head, K or V), in order; lengths are counted in
+// rounds of kThreads requests.
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__ Read8Args a) {
+  constexpr int CH = D / 8;             // 8-byte chunks of a row of codes: 16 bytes of a row read
+  constexpr int RPI = 32 / CH;
+  constexpr int N = kScaleBlock / RPI;
+  __shared__ int scan[33];
+  __shared__ int ends[kThreads], keys[kThreads];
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ch = lane % CH, r0 = lane / CH;
+  const int each = 2 * a.c.hkv;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+  int64_t at = static_cast<int64_t>(blockIdx.x) * kWarps + warp;  // this warp's unit, from the round's first one
+  for (int q0 = 0; q0 < a.num_reqs; q0 += kThreads) {
+    int n = 0;
+    if (q0 + tid < a.num_reqs) {
+      const int r = q0 + tid;
+      const int64_t start = a.kv_start[r];
+      if (start >= 0) {  // below 0: this request is not read
+        const int sl = a.seq_lens[r];
+        n = sl;
+        if (a.past) n -= a.qsl[r + 1] - a.qsl[r];
+        if (sl < 0 || n < 0 || n > a.max_keys || start + n > a.rows) {
+          if (blockIdx.x == 0) flag_error(a.err, DSA_DEVERR_SEQ_RANGE);
+          n = 0;
+        }
+      }
+    }
+    int tot;
+    const int incl = block_scan_incl((n + kScaleBlock - 1) / kScaleBlock, scan, &tot);
+    ends[tid] = incl;
+    keys[tid] = n;
+    __syncthreads();
+    const int64_t units = static_cast<int64_t>(tot) * each;
+    int i = 0;
+    for (; at < units; at += warps) {
+      const int b = static_cast<int>(at / each), hv = static_cast<int>(at - static_cast<int64_t>(b) * each);
+      while (ends[i] <= b) ++i;
+      const int first = (b - (i > 0 ? ends[i - 1] : 0)) * kScaleBlock, have = min(kScaleBlock, keys[i] - first);
+      const int64_t page = a.block_table[static_cast<int64_t>(q0 + i) * a.bt_stride + first / kBlock];
+      if (page < 0 || page >= a.c.num_blocks) {
+        if (lane == 0) flag_error(a.err, DSA_DEVERR_BLOCK_RANGE);
+        continue;
+      }
+      const int h = hv >> 1, part = first % kBlock / kScaleBlock;
+      const bool isv = hv & 1;
+      const int64_t slot = isv ? a.c.v_slot : a.c.k_slot, row = isv ? a.v_row : a.k_row;
+      const uint8_t* codes = (isv ? a.c.v + page * a.c.v_page + h * a.c.v_head : a.c.k + page * a.c.k_page + h * a.c.k_head) +
+                             (part * kScaleBlock + r0) * slot + ch * 8;
+      uint16_t* out = (isv ? a.v + h * a.v_rhead : a.k + h * a.k_rhead) +
+                      (static_cast<int64_t>(a.kv_start[q0 + i]) + first + r0) * row + ch * 8;
+      uint2 x[N];
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+        if (u * RPI + r0 < have) x[u] = *reinterpret_cast<const uint2*>(codes + u * RPI * slot);
+      const float s = a.c.scale[page * a.c.s_page + part * a.c.s_block + h * a.c.s_head + (isv ? 1 : 0)];
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        if (u * RPI + r0 >= have) continue;
+        float2 f[4];
+        values(x[u].x, &f[0], &f[1]);
+        values(x[u].y, &f[2], &f[3]);
+        *reinterpret_cast<uint4*>(out + u * RPI * row) =
+            make_uint4(narrow(f[0].x * s, f[0].y * s, T()), narrow(f[1].x * s, f[1].y * s, T()),
+                       narrow(f[2].x * s, f[2].y * s, T()), narrow(f[3].x * s, f[3].y * s, T()));
+      }
+    }
+    at -= units;
+    __syncthreads();  // the round's lengths are read
+  }
+}
+
+template <int D, typename T>
+cudaError_t write8(const Write8Args& a, cudaStream_t stream) {
+  if (a.token_of == nullptr)
+    return launch_pdl(write8_kernel<D, T, 1>, dim3(static_cast<unsigned>(a.n_tokens)), dim3(kThreads), 0, stream, a);
+  cudaError_t e = launch_pdl(write8_claim_kernel, dim3(static_cast<unsigned>((a.n_tokens + kThreads - 1) / kThreads)),
+                             dim3(kThreads), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  constexpr int PER = 16;
+  return launch_pdl(write8_kernel<D, T, PER>, dim3(static_cast<unsigned>((a.n_tokens + PER - 1) / PER)),
+                    dim3(kThreads), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write8(const Write8Args& a, int head_dim, int dtype, cudaStream_t stream) {
+  if (dtype == DSA_BF16)
+    return head_dim == 128 ? write8<128, __nv_bfloat16>(a, stream) : write8<64, __nv_bfloat16>(a, stream);
+  return head_dim == 128 ? write8<128, __half>(a, stream) : write8<64, __half>(a, stream);
+}
+
+cudaError_t launch_kv_read8(const Read8Args& a, int head_dim, int dtype, int num_sms, cudaStream_t stream) {
+  // at most so many blocks are read, whatever the lengths
+  const int64_t blocks = static_cast<int64_t>(a.num_reqs) * ((a.max_keys + kScaleBlock - 1) / kScaleBlock);
+  int64_t grid = (blocks * 2 * a.c.hkv + kWarps - 1) / kWarps;
+  const int64_t cap = static_cast<int64_t>(num_sms) * 8;
+  if (grid > cap) grid = cap;
+  if (grid < 1) grid = 1;
+  const dim3 g(static_cast<unsigned>(grid)), b(kThreads);
+  if (dtype == DSA_BF16)
+    return head_dim == 128 ? launch_pdl(read8_kernel<128, __nv_bfloat16>, g, b, 0, stream, a)
+                           : launch_pdl(read8_kernel<64, __nv_bfloat16>, g, b, 0, stream, a);
+  return head_dim == 128 ? launch_pdl(read8_kernel<128, __half>, g, b, 0, stream, a)
+                         : launch_pdl(read8_kernel<64, __half>, g, b, 0, stream, a);
+}
+
+}  // namespace dsa

@@ -475,6 +475,98 @@ DSA_API int dsa_attn_selected(const DsaKv *kv, const DsaAttn *attn, const int32_
 DSA_API int dsa_attn_prompt(const DsaBatch *batch, const DsaKv *kv, const int32_t *kv_start,
                     const DsaAttn *attn, int32_t *dev_err, dsa_stream_t stream);
 
+/* ------------------------------------------- the KV cache in 8 bits */
+/* The same cache with rows held as E4M3 codes and a scale for each block of 16
+ * slots of a page and KV head, K's and V's apart: a row's values are codes *
+ * scale. Half the bytes of a 16-bit cache for the calls that are bound by them.
+ * Codes have the shape and the freedom of strides of DsaKv (a code is a byte);
+ * scales are fp32 [num_blocks, 4, num_kv_heads, 2], the last axis (K's, V's)
+ * contiguous. For the page calls codes and scales are caches like any other,
+ * and have to move together.
+ *   k, v        device, 16-byte aligned; page, slot and head strides in bytes,
+ *               multiples of 16, at least head_dim, below 2^39; that of an axis
+ *               of one element (one page, one head) is not used
+ *   scale       device, 16-byte aligned; page, block and head strides in
+ *               fp32 numbers, even, at least 2, below 2^39
+ *   dtype       DSA_BF16 or DSA_FP16: of the rows that a call takes and gives
+ *   num_kv_heads, head_dim, num_blocks  as in DsaKv
+ * dsa_kv_write8 makes scales that are powers of two from 2^-64 to 2^120. The
+ * readers take any finite scales from 2^-64 to 2^120 (a smaller one of V's, 0
+ * among them, counts as 2^-64); others give unspecified rows. */
+#define DSA_SCALE_BLOCK 16
+typedef struct DsaKv8 {
+  uint8_t *k;
+  uint8_t *v;
+  float *scale;
+  int32_t dtype;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int64_t num_blocks;
+  int64_t k_page_stride, k_slot_stride, k_head_stride;
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+  int64_t s_page_stride, s_block_stride, s_head_stride;
+} DsaKv8;
+
+/* A step's K and V rows quantised into the cache at their slots. In each block
+ * that the call writes, per head and K and V apart, with amax the largest finite
+ * magnitude of the rows that it writes there:
+ *   need  = the least power of two 2^e, e >= -64, with amax / 2^e <= 448
+ *   scale = need if the call writes the block's first slot (which opens the
+ *           block: its other slots' codes keep their bits and stand for nothing
+ *           until they are written), else the larger of need and the block's
+ *           scale (one that is not positive and finite counts as none)
+ *   code  = x / scale rounded to the nearest code; where the block's scale rises,
+ *           its other slots' codes are rounded to it
+ * so a sequence that grows slot by slot keeps each row within one step of its
+ * block's largest, however it is cut into calls. NaN and infinities become NaN.
+ * Of tokens with one slot the last of the list is written. Results do not depend
+ * on timing, nor on the order of the list but for that.
+ *   k, v, slot_mapping  as for dsa_kv_write; n_tokens at most 2^31 - 1
+ *   ws, ws_bytes        device scratch, 16-byte aligned, of
+ *                       dsa_kv_write8_workspace_size() bytes (0 for few tokens,
+ *                       else 4 a slot of the cache), as for dsa_attn_decode
+ * Slots outside the cache, other than -1, are skipped and flag
+ * DSA_DEVERR_SLOT_RANGE. */
+DSA_API size_t dsa_kv_write8_workspace_size(int64_t n_tokens, int64_t num_blocks);
+DSA_API int dsa_kv_write8(const void *k, int64_t k_row_stride, int64_t k_head_stride, const void *v,
+                  int64_t v_row_stride, int64_t v_head_stride, int64_t n_tokens,
+                  const int64_t *slot_mapping, const DsaKv8 *kv, void *ws, size_t ws_bytes,
+                  int32_t *dev_err, dsa_stream_t stream);
+
+/* Sequences' rows back in 16 bits: keys [0, seq_lens[r]) of each request r with
+ * kv_start[r] >= 0 into the packed rows kv_start[r] + s of `rows`, described as
+ * dsa_attn_prompt takes them (dtype and sizes as kv's). With past != 0 without
+ * the request's own query tokens, keys [0, seq_lens[r] - q_len[r]): what a prompt
+ * that brings its own K and V in 16 bits attends to besides. Other rows are left
+ * as they were. Values are codes * scale, rounded once to the type (a power of
+ * two scale leaves nothing to round within the type's range).
+ *   kv_start  device int32 [num_reqs]; below 0: the request is not read
+ * batch->num_blocks must equal kv->num_blocks; keys that a block-table row and
+ * max_seq_len allow are at most 2^27 - 64; query_start_loc may be NULL without
+ * past, req_id_per_token is not used.
+ * Flags: DSA_DEVERR_SEQ_RANGE (seq_len negative, below q_len with past, or
+ * beyond the block-table row, max_seq_len or the packed rows: the request is not
+ * read), DSA_DEVERR_BLOCK_RANGE (the block's rows are left as they were). */
+DSA_API int dsa_kv_read8(const DsaBatch *batch, const DsaKv8 *kv, const int32_t *kv_start, const DsaKv *rows,
+                 int32_t past, int32_t *dev_err, dsa_stream_t stream);
+
+/* dsa_attn_decode and dsa_attn_selected over this cache: arguments, rows, flags
+ * and the treatment of what a row does not see as there, q and out of type
+ * kv->dtype. Scores and sums are fp32; the weights, with V's scales in them, are
+ * rounded to fp16 for the product with V's codes (2^-11 of each, or 2^-30 of the
+ * row's largest, whichever is more), the result to the type when it is stored.
+ * q's elements below 2^-38 of their row's largest may count as 0 (bf16). V's
+ * scales that one row sees may lie up to 2^100 apart. */
+DSA_API size_t dsa_attn_decode8_workspace_size(const DsaBatch *batch, int32_t num_heads,
+                                       int32_t num_kv_heads, int32_t head_dim);
+DSA_API int dsa_attn_decode8(const DsaBatch *batch, const DsaKv8 *kv, const DsaAttn *attn, void *ws,
+                     size_t ws_bytes, int32_t *dev_err, dsa_stream_t stream);
+DSA_API size_t dsa_attn_selected8_workspace_size(int64_t n_tokens, int32_t topk, int32_t num_heads,
+                                         int32_t num_kv_heads, int32_t head_dim);
+DSA_API int dsa_attn_selected8(const DsaKv8 *kv, const DsaAttn *attn, const int32_t *physical,
+                       int64_t n_tokens, int32_t topk, void *ws, size_t ws_bytes, int32_t *dev_err,
+                       dsa_stream_t stream);
+
 /* ------------------------------------------------------ pages of a cache */
 /* Upkeep of sequences' pages: a pool of num_blocks pages with a reference
  * count each (0 = free), and per sequence a block-table row and a length. The
