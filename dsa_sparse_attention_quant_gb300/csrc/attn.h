@@ -35,27 +35,32 @@ struct RowsArgs {
   int topk;
   int64_t num_slots;
   // work: split: slices of at least min_tiles tiles of the flat tile list, else
-  // a token per slice; a CTA per slice, KV head and pass
+  // a token per slice; a CTA per slice, `joint` KV heads and pass
   int slices, min_tiles;
+  int joint;
   bool split;
   int2* desc;       // [CTAs]: {token begun here and continued, its last slice}
-  float2* part_ml;  // [2 * CTAs][rows of a pass]
-  float* part_o;    // [2 * CTAs][rows of a pass][D]
+  float2* part_ml;  // [2 * CTAs][joint][rows of a pass]
+  float* part_o;    // [2 * CTAs][joint][rows of a pass][D]
   int32_t* err;
 };
 cudaError_t launch_attn_rows(const RowsArgs& a, int head_dim, int dtype, bool selected, cudaStream_t stream);
 
-// The parts that the main kernel's slices left, added (attn_rows.cu): grid main CTAs,
-// krows rows of the workspace each.
-cudaError_t launch_attn_join(const RowsArgs& a, int head_dim, int dtype, int grid, int krows, cudaStream_t stream);
+// The parts that the main kernel's slices left, added (attn_rows.cu): krows rows of the
+// workspace a CTA and KV head; early: the stream's next kernel may begin meanwhile.
+cudaError_t launch_attn_join(const RowsArgs& a, int head_dim, int dtype, int krows, bool early, cudaStream_t stream);
 
 // The same rows over a cache of E4M3 codes (attn_rows8.cu): k, v and their strides
 // count bytes, the scales' strides count fp32 numbers.
 struct Rows8Args : RowsArgs {
   const float* scale;  // [pages, 4, heads, 2]: a block of 16 slots' K and V scale
   int64_t s_page, s_block, s_head;
+  bool bf16;   // of q and out; else fp16
+  bool pairs;  // heads of 64 side by side, an even number of them
 };
-cudaError_t launch_attn_rows8(const Rows8Args& a, int head_dim, int dtype, bool selected, cudaStream_t stream);
+// maps: K and V as {row, rows of heads, 64 slots, pages}; not used for selected slots.
+cudaError_t launch_attn_rows8(const Rows8Args& a, int head_dim, bool selected, const CUtensorMap* maps,
+                              cudaStream_t stream);
 
 // The cache of E4M3 codes, written and read back (kv8.cu). Strides as in Rows8Args;
 // those of 16-bit rows in elements of 2 bytes.

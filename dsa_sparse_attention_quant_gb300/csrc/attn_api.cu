@@ -105,6 +105,7 @@ int max_keys(const DsaBatch* b) {
 }
 
 // ---- single rows: how the work is cut, from the host's bounds alone.
+enum Cache { kIn16, kIn8 };
 struct RowsPlan {
   int passes, rows;  // passes over the keys, rows of the workspace per pass
   int64_t slices;    // split: slices of the tile list, else the tokens
@@ -113,18 +114,18 @@ struct RowsPlan {
   size_t off_ml, off_o, bytes;
 };
 
-// Two CTAs per SM on a part of up to 160 SMs.
-constexpr int kRowsCtas = 320;
+// The scratch is sized for parts of up to 160 SMs.
+constexpr int kMostSms = 160;
 // Tokens of up to this many tiles are not cut while the CTAs are few: one streams
 // such a row in about the time that the join's launch takes. GPU time, 32/8 heads
 // of 128: one request of 256 keys 5.7 us (cut from 2 tiles on: 7.1), of 768 7.9 (cut
 // from 16 on: 11.5); one of 512 takes 8.5, cut 7.5.
 constexpr int kDirectTiles = 8;
-// More CTAs than this run as slices, whose loads go on across tokens: two on each of
-// a GB300's 152 SMs. It is a number, not the device's, so that the scratch's size
-// and the run decide alike. 32 requests of 512 keys, 32/8 heads: 10.6 us (with 152:
-// 15.2); 64 of them 29.3 (with 608: 26.5).
-constexpr int kDirectCtas = 304;
+// More CTAs than there are places on a GB300's 152 SMs run as slices, whose loads go on
+// across tokens. It is a number, not the device's, so that the scratch's size
+// and the run decide alike. 16 bits, two places an SM: 32 requests of 512 keys, 32/8
+// heads: 10.6 us (with 152: 15.2); 64 of them 29.3 (with 608: 26.5).
+constexpr int kDirectSms = 152;
 // The least slice, in tiles: shorter ones pay more for their partials than they save
 // (2 requests of 4096 keys, 40/1 heads: 14.3 us, with 1 tile 18.5; one of 768,
 // 32/8: 7.9, with 4 tiles 9.1).
@@ -133,33 +134,36 @@ constexpr int kMinTiles = 2;
 // One slice per CTA place: cut two or four times finer, so that CTAs that stream
 // slower take less, the partials and the CTAs' starts cost more than that gains
 // (32 requests of 4K to 8K keys: 130.8, 134.4, 145.0 us).
-// least: the query heads of the kernel's smallest tile.
-RowsPlan rows_plan(int64_t tokens, int64_t keys, int heads, int hkv, int head_dim, int least, int ctas) {
+// joint: KV heads a CTA takes.
+RowsPlan rows_plan(int64_t tokens, int64_t keys, int heads, int hkv, int head_dim, Cache cache, int joint,
+                   int sms) {
   RowsPlan p{};
   const int group = heads / hkv;
-  p.rows = least;
+  // the kernels' tiles of query heads, and their CTAs per SM (RowsCfg, Rows8Cfg)
+  p.rows = cache == kIn8 ? 8 : 16;
   while (p.rows < 32 && p.rows < group) p.rows *= 2;
+  const int row = cache == kIn8 && joint > 1 ? 128 : head_dim;
+  const int per_sm = cache == kIn8 && p.rows * row <= 8 * 128 ? 3 : 2;
   p.passes = (group + p.rows - 1) / p.rows;
+  const int64_t across = static_cast<int64_t>(hkv / joint) * p.passes;  // CTAs a slice
   const int64_t tiles = keys > 0 ? (keys + kBlock - 1) / kBlock : 1;
-  p.split = tiles > kDirectTiles || tokens * hkv * p.passes > kDirectCtas;
+  p.split = tiles > kDirectTiles || tokens * across > per_sm * kDirectSms;
   p.slices = tokens;
   if (p.split) {
     const int64_t most = (tokens * tiles + kMinTiles - 1) / kMinTiles;
-    int64_t s = ctas / (static_cast<int64_t>(hkv) * p.passes);
+    int64_t s = per_sm * (sms < kMostSms ? sms : kMostSms) / across;
     if (s < 1) s = 1;
     p.slices = s < most ? s : most;
   }
-  p.ctas = p.slices * hkv * p.passes;
+  p.ctas = p.slices * across;
   if (p.split) {
-    const size_t n = static_cast<size_t>(p.ctas);
-    p.off_ml = align_up(n * sizeof(int2), 256);
+    const size_t n = static_cast<size_t>(p.ctas) * joint;
+    p.off_ml = align_up(static_cast<size_t>(p.ctas) * sizeof(int2), 256);
     p.off_o = p.off_ml + align_up(2 * n * p.rows * sizeof(float2), 256);
     p.bytes = p.off_o + 2 * n * p.rows * head_dim * sizeof(float);
   }
   return p;
 }
-
-constexpr int kLeast16 = 16, kLeast8 = 8;  // of attn_rows.cu and attn_rows8.cu
 
 bool heads_ok(int32_t heads, int32_t hkv, int32_t head_dim) {
   return hkv >= 1 && heads >= 1 && heads <= 65535 && heads % hkv == 0 && (head_dim == 64 || head_dim == 128);
@@ -189,7 +193,33 @@ RowsArgs rows_args(const DsaKv& kv, const DsaAttn& at) {
   a.num_blocks = kv.num_blocks;
   a.num_slots = kv.num_blocks * kBlock;
   a.min_tiles = kMinTiles;
+  a.joint = 1;
   return a;
+}
+
+// Heads of 64 that lie side by side, two to a row of 128 bytes.
+bool pairs_of_64(const DsaKv8& kv) {
+  return kv.head_dim == 64 && kv.num_kv_heads % 2 == 0 && kv.k_head_stride == 64 && kv.v_head_stride == 64;
+}
+
+// Codes of K or V as a 4-D tensor {row, rows of heads, slots, pages} with `pair` heads a
+// row: one box is 16 slots of a row.
+int make_kv8_map(CUtensorMap* m, const DsaKv8& kv, int pair, const void* base, int64_t page, int64_t slot, int64_t head) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  int st = tensor_map_encoder(&enc);
+  if (st != DSA_OK) return st;
+  const int row = pair * kv.head_dim;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(kv.num_kv_heads / pair), kBlock,
+                        static_cast<cuuint64_t>(kv.num_blocks)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(head * pair), static_cast<cuuint64_t>(slot),
+                           static_cast<cuuint64_t>(page)};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(row), 1, DSA_SCALE_BLOCK, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DSA_OK : DSA_ECUDA;
 }
 
 Rows8Args rows8_args(const DsaKv8& kv, const DsaKv& sizes, const DsaAttn& at) {
@@ -207,6 +237,7 @@ Rows8Args rows8_args(const DsaKv8& kv, const DsaKv& sizes, const DsaAttn& at) {
   a.s_page = kv.s_page_stride;
   a.s_block = kv.s_block_stride;
   a.s_head = kv.s_head_stride;
+  a.bf16 = kv.dtype == DSA_BF16;
   return a;
 }
 
@@ -229,15 +260,16 @@ Cache8Args cache8_args(const DsaKv8& kv) {
 
 // launch(): the kernels with the finished arguments.
 template <typename F>
-int run_rows(RowsArgs& a, int64_t tokens, int64_t keys, int head_dim, int least, void* ws, size_t ws_bytes, F launch) {
-  RowsPlan need = rows_plan(tokens, keys, a.heads, a.hkv, head_dim, least, kRowsCtas);
-  if (need.ctas > INT_MAX) return DSA_EINVAL;
-  if (need.bytes > 0 && (ws == nullptr || !aligned16(ws))) return DSA_EINVAL;
-  if (ws_bytes < need.bytes) return DSA_ENOSPACE;
+int run_rows(RowsArgs& a, int64_t tokens, int64_t keys, int head_dim, Cache cache, size_t need, void* ws,
+             size_t ws_bytes, F launch) {
+  const RowsPlan most = rows_plan(tokens, keys, a.heads, a.hkv, head_dim, cache, a.joint, kMostSms);
+  if (most.ctas > INT_MAX || most.slices * a.hkv * most.passes > INT_MAX) return DSA_EINVAL;
+  if (need > 0 && (ws == nullptr || !aligned16(ws))) return DSA_EINVAL;
+  if (ws_bytes < need) return DSA_ENOSPACE;
   int sms;
   int st = device_sms(&sms);
   if (st != DSA_OK) return st;
-  const RowsPlan p = rows_plan(tokens, keys, a.heads, a.hkv, head_dim, least, 2 * sms < kRowsCtas ? 2 * sms : kRowsCtas);
+  const RowsPlan p = rows_plan(tokens, keys, a.heads, a.hkv, head_dim, cache, a.joint, sms);
   a.n_tokens = static_cast<int>(tokens);
   a.passes = p.passes;
   a.slices = static_cast<int>(p.slices);
@@ -248,7 +280,19 @@ int run_rows(RowsArgs& a, int64_t tokens, int64_t keys, int head_dim, int least,
     a.part_ml = reinterpret_cast<float2*>(base + p.off_ml);
     a.part_o = reinterpret_cast<float*>(base + p.off_o);
   }
-  return from_cuda(launch());
+  return launch();
+}
+
+// Scratch of a call over a cache in 16 bits, and in 8: the latter whatever the cache's
+// strides, which decide how many heads a CTA takes.
+size_t rows_bytes(int64_t tokens, int64_t keys, int heads, int hkv, int head_dim) {
+  return rows_plan(tokens, keys, heads, hkv, head_dim, kIn16, 1, kMostSms).bytes;
+}
+size_t rows8_bytes(int64_t tokens, int64_t keys, int heads, int hkv, int head_dim) {
+  const size_t one = rows_plan(tokens, keys, heads, hkv, head_dim, kIn8, 1, kMostSms).bytes;
+  if (head_dim == 128 || hkv % 2 != 0) return one;
+  const size_t two = rows_plan(tokens, keys, heads, hkv, head_dim, kIn8, 2, kMostSms).bytes;
+  return one > two ? one : two;
 }
 
 // What a batch's decode tokens read.
@@ -424,9 +468,8 @@ int dsa_kv_write(const void* k, int64_t k_row_stride, int64_t k_head_stride, con
 size_t dsa_attn_decode_workspace_size(const DsaBatch* batch, int32_t num_heads, int32_t num_kv_heads,
                                       int32_t head_dim) {
   if (check_step(batch, true) != DSA_OK || !heads_ok(num_heads, num_kv_heads, head_dim)) return 0;
-  return rows_plan(batch->num_decode_tokens, batch->num_reqs > 0 ? max_keys(batch) : 0, num_heads, num_kv_heads,
-                   head_dim, kLeast16, kRowsCtas)
-      .bytes;
+  return rows_bytes(batch->num_decode_tokens, batch->num_reqs > 0 ? max_keys(batch) : 0, num_heads, num_kv_heads,
+                    head_dim);
 }
 
 int dsa_attn_decode(const DsaBatch* batch, const DsaKv* kv, const DsaAttn* attn, void* ws, size_t ws_bytes,
@@ -442,14 +485,15 @@ int dsa_attn_decode(const DsaBatch* batch, const DsaKv* kv, const DsaAttn* attn,
   if (batch->num_blocks != c.num_blocks || batch->num_decodes < 1) return DSA_EINVAL;
   RowsArgs a = rows_args(c, at);
   set_decode(a, batch, dev_err);
-  return run_rows(a, batch->num_decode_tokens, a.max_keys, c.head_dim, kLeast16, ws, ws_bytes,
-                  [&] { return launch_attn_rows(a, c.head_dim, c.dtype, false, stream); });
+  return run_rows(a, batch->num_decode_tokens, a.max_keys, c.head_dim, kIn16,
+                  rows_bytes(batch->num_decode_tokens, a.max_keys, a.heads, a.hkv, c.head_dim), ws, ws_bytes,
+                  [&] { return from_cuda(launch_attn_rows(a, c.head_dim, c.dtype, false, stream)); });
 }
 
 size_t dsa_attn_selected_workspace_size(int64_t n_tokens, int32_t topk, int32_t num_heads, int32_t num_kv_heads,
                                         int32_t head_dim) {
   if (n_tokens < 0 || n_tokens > INT_MAX || topk < 1 || !heads_ok(num_heads, num_kv_heads, head_dim)) return 0;
-  return rows_plan(n_tokens, topk, num_heads, num_kv_heads, head_dim, kLeast16, kRowsCtas).bytes;
+  return rows_bytes(n_tokens, topk, num_heads, num_kv_heads, head_dim);
 }
 
 int dsa_attn_selected(const DsaKv* kv, const DsaAttn* attn, const int32_t* physical, int64_t n_tokens, int32_t topk,
@@ -465,8 +509,8 @@ int dsa_attn_selected(const DsaKv* kv, const DsaAttn* attn, const int32_t* physi
   a.physical = physical;
   a.topk = topk;
   a.err = dev_err;
-  return run_rows(a, n_tokens, topk, c.head_dim, kLeast16, ws, ws_bytes,
-                  [&] { return launch_attn_rows(a, c.head_dim, c.dtype, true, stream); });
+  return run_rows(a, n_tokens, topk, c.head_dim, kIn16, rows_bytes(n_tokens, topk, a.heads, a.hkv, c.head_dim), ws,
+                  ws_bytes, [&] { return from_cuda(launch_attn_rows(a, c.head_dim, c.dtype, true, stream)); });
 }
 
 int dsa_attn_prompt(const DsaBatch* batch, const DsaKv* kv, const int32_t* kv_start, const DsaAttn* attn,
@@ -579,9 +623,8 @@ int dsa_kv_read8(const DsaBatch* batch, const DsaKv8* kv, const int32_t* kv_star
 size_t dsa_attn_decode8_workspace_size(const DsaBatch* batch, int32_t num_heads, int32_t num_kv_heads,
                                        int32_t head_dim) {
   if (check_step(batch, true) != DSA_OK || !heads_ok(num_heads, num_kv_heads, head_dim)) return 0;
-  return rows_plan(batch->num_decode_tokens, batch->num_reqs > 0 ? max_keys(batch) : 0, num_heads, num_kv_heads,
-                   head_dim, kLeast8, kRowsCtas)
-      .bytes;
+  return rows8_bytes(batch->num_decode_tokens, batch->num_reqs > 0 ? max_keys(batch) : 0, num_heads, num_kv_heads,
+                     head_dim);
 }
 
 int dsa_attn_decode8(const DsaBatch* batch, const DsaKv8* kv, const DsaAttn* attn, void* ws, size_t ws_bytes,
@@ -598,14 +641,24 @@ int dsa_attn_decode8(const DsaBatch* batch, const DsaKv8* kv, const DsaAttn* att
   if (batch->num_blocks != c.num_blocks || batch->num_decodes < 1) return DSA_EINVAL;
   Rows8Args a = rows8_args(c, sizes, at);
   set_decode(a, batch, dev_err);
-  return run_rows(a, batch->num_decode_tokens, a.max_keys, c.head_dim, kLeast8, ws, ws_bytes,
-                  [&] { return launch_attn_rows8(a, c.head_dim, c.dtype, false, stream); });
+  a.pairs = pairs_of_64(c);
+  a.joint = a.pairs ? 2 : 1;
+  return run_rows(a, batch->num_decode_tokens, a.max_keys, c.head_dim, kIn8,
+                  rows8_bytes(batch->num_decode_tokens, a.max_keys, a.heads, a.hkv, c.head_dim), ws, ws_bytes,
+                  [&] {
+                    CUtensorMap maps[2];
+                    int e = make_kv8_map(&maps[0], c, a.joint, c.k, c.k_page_stride, c.k_slot_stride, c.k_head_stride);
+                    if (e != DSA_OK) return e;
+                    e = make_kv8_map(&maps[1], c, a.joint, c.v, c.v_page_stride, c.v_slot_stride, c.v_head_stride);
+                    if (e != DSA_OK) return e;
+                    return from_cuda(launch_attn_rows8(a, c.head_dim, false, maps, stream));
+                  });
 }
 
 size_t dsa_attn_selected8_workspace_size(int64_t n_tokens, int32_t topk, int32_t num_heads, int32_t num_kv_heads,
                                          int32_t head_dim) {
   if (n_tokens < 0 || n_tokens > INT_MAX || topk < 1 || !heads_ok(num_heads, num_kv_heads, head_dim)) return 0;
-  return rows_plan(n_tokens, topk, num_heads, num_kv_heads, head_dim, kLeast8, kRowsCtas).bytes;
+  return rows8_bytes(n_tokens, topk, num_heads, num_kv_heads, head_dim);
 }
 
 int dsa_attn_selected8(const DsaKv8* kv, const DsaAttn* attn, const int32_t* physical, int64_t n_tokens, int32_t topk,
@@ -622,8 +675,13 @@ int dsa_attn_selected8(const DsaKv8* kv, const DsaAttn* attn, const int32_t* phy
   a.physical = physical;
   a.topk = topk;
   a.err = dev_err;
-  return run_rows(a, n_tokens, topk, c.head_dim, kLeast8, ws, ws_bytes,
-                  [&] { return launch_attn_rows8(a, c.head_dim, c.dtype, true, stream); });
+  a.pairs = pairs_of_64(c);
+  a.joint = a.pairs ? 2 : 1;
+  return run_rows(a, n_tokens, topk, c.head_dim, kIn8, rows8_bytes(n_tokens, topk, a.heads, a.hkv, c.head_dim), ws,
+                  ws_bytes, [&] {
+                    const CUtensorMap maps[2] = {};
+                    return from_cuda(launch_attn_rows8(a, c.head_dim, true, maps, stream));
+                  });
 }
 
 size_t dsa_pages_workspace_size(int64_t num_blocks, int32_t n) {

@@ -503,7 +503,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
 constexpr int kJoinWarps = 8;
 
 template <int D, typename T, int WAYS>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ RowsArgs a, int krows) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ RowsArgs a, int krows,
+                                                                    bool early) {
   constexpr int V = D / 32;
   constexpr int kRowsCta = kJoinWarps / WAYS;
   __shared__ float so[WAYS > 1 ? kJoinWarps : 1][D];
@@ -513,9 +514,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = blockIdx.y * kRowsCta + warp / WAYS, head0 = pass * krows;
   const bool in = head0 + r < a.group && r < krows;
-  pdl_launch_dependents();
+  if (early) pdl_launch_dependents();
   pdl_wait();
-  const int2 d = a.desc[blockIdx.x];
+  // the main kernel's CTA of slice c with this head
+  auto cta = [&](int64_t c) { return (c * (a.hkv / a.joint) + h / a.joint) * a.passes + pass; };
+  const int2 d = a.desc[cta(part)];
   if (d.x < 0) return;
   float M = -INFINITY, L = 0.0f, o[V];
 #pragma unroll
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
   if (in) {
 #pragma unroll 4
     for (int c = part + warp % WAYS; c <= d.y; c += WAYS) {
-      const int64_t slot = 2 * ((static_cast<int64_t>(c) * a.hkv + h) * a.passes + pass) + (c == part ? 1 : 0);
+      const int64_t slot = (2 * cta(c) + (c == part ? 1 : 0)) * a.joint + h % a.joint;
       const float2 v = a.part_ml[slot * krows + r];
       const float* p = a.part_o + (slot * krows + r) * D + lane * V;
       float w[V];
@@ -569,13 +572,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
     a.lse[static_cast<int64_t>(d.x) * a.heads + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// krows: rows of the workspace per main CTA.
+// krows: rows of the workspace per main CTA and KV head; early: the next kernel's CTAs may begin.
 template <int D, typename T>
-cudaError_t join(const RowsArgs& a, int grid, int krows, cudaStream_t stream) {
+cudaError_t join(const RowsArgs& a, int krows, bool early, cudaStream_t stream) {
+  const int grid = a.slices * a.hkv * a.passes;
   const int rows = a.group < krows ? a.group : krows;
   if (a.slices > 4 * static_cast<int64_t>(a.n_tokens))
-    return launch_pdl(attn_join_kernel<D, T, 8>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, stream, a, krows);
-  return launch_pdl(attn_join_kernel<D, T, 1>, dim3(grid, (rows + 7) / 8), dim3(32 * kJoinWarps), 0, stream, a, krows);
+    return launch_pdl(attn_join_kernel<D, T, 8>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, stream, a, krows,
+                      early);
+  return launch_pdl(attn_join_kernel<D, T, 1>, dim3(grid, (rows + 7) / 8), dim3(32 * kJoinWarps), 0, stream, a, krows,
+                      early);
 }
 
 template <int D, typename T, int MT, bool SEL>
@@ -586,7 +592,7 @@ cudaError_t launch(const RowsArgs& a, int grid, cudaStream_t stream) {
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(fn), C::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
   if ((e = launch_pdl(fn, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, a)) != cudaSuccess || !a.split) return e;
-  return join<D, T>(a, grid, C::kRows, stream);
+  return join<D, T>(a, C::kRows, true, stream);
 }
 
 template <int D, typename T>
@@ -607,11 +613,11 @@ cudaError_t launch_attn_rows(const RowsArgs& a, int head_dim, int dtype, bool se
                          : launch_dt<64, __half>(a, grid, selected, stream);
 }
 
-cudaError_t launch_attn_join(const RowsArgs& a, int head_dim, int dtype, int grid, int krows, cudaStream_t stream) {
+cudaError_t launch_attn_join(const RowsArgs& a, int head_dim, int dtype, int krows, bool early, cudaStream_t stream) {
   if (dtype == DSA_BF16)
-    return head_dim == 128 ? join<128, __nv_bfloat16>(a, grid, krows, stream)
-                           : join<64, __nv_bfloat16>(a, grid, krows, stream);
-  return head_dim == 128 ? join<128, __half>(a, grid, krows, stream) : join<64, __half>(a, grid, krows, stream);
+    return head_dim == 128 ? join<128, __nv_bfloat16>(a, krows, early, stream)
+                           : join<64, __nv_bfloat16>(a, krows, early, stream);
+  return head_dim == 128 ? join<128, __half>(a, krows, early, stream) : join<64, __half>(a, krows, early, stream);
 }
 
 }  // namespace dsa

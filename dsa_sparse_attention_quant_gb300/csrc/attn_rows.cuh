@@ -141,14 +141,14 @@ struct Slice {
 // Split mode: slice `part` of the flat tile list, many tokens counted in rounds of
 // kPer a thread: their metadata's latency is what a round takes (4096 requests of
 // 300 keys, 32/8 heads of 128: 801 us with rounds of one a thread and a second
-// pass over all of them, so 780). All threads call; rounds[kRounds] is scratch.
+// pass over all of them, so 780). All THREADS threads call; rounds[kRounds] is scratch.
 constexpr int kPer = 4, kRounds = 1024;
-template <bool SEL>
+template <bool SEL, int THREADS = kThreads>
 __device__ void find_slice(const RowsArgs& a, int part, bool flag, Slice* s, int* scan, int* rounds) {
   const int T = a.n_tokens, tid = threadIdx.x;
   int tot, n[kPer], req[kPer], tiles[kPer], first = 0;  // of this thread's tokens of the last counted round
   int64_t total = 0;
-  const int per = T <= kThreads ? 1 : kPer;
+  const int per = T <= THREADS ? 1 : kPer;
   auto count = [&](int c0, bool f) {
     int sum = 0;
 #pragma unroll
@@ -163,7 +163,7 @@ __device__ void find_slice(const RowsArgs& a, int part, bool flag, Slice* s, int
     }
     first = block_scan_incl(sum, scan, &tot) - sum;
   };
-  constexpr int R = kThreads * kPer;
+  constexpr int R = THREADS * kPer;
   if (SEL) {
     total = static_cast<int64_t>(T) * tiles_of(a.topk);
   } else {

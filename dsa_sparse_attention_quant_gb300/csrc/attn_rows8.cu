@@ -42,26 +42,49 @@ constexpr int kScaleBlock = DSA_SCALE_BLOCK;
 static_assert(kWarpKeys == kScaleBlock, "a warp's keys of a tile share their scales");
 constexpr float kLeastScale = 0x1p-64f, kMostScale = 0x1p126f;
 
-template <int D, int NT>
+// How codes come into shared memory: TMA boxes of a page's 16 slots, asked for by the
+// loader; or 16 bytes a lane from the selected slots, asked for by the warps that use them
+// (64 tokens of 2048 slots: TMA gathers of four slots' rows 90 us, bulk copies of four
+// heads a slot 93, single rows 184).
+enum Load : int { kPages, kSlots };
+
+constexpr int kThreads8 = kThreads + 32;  // the consumers, and the loader
+
+// A row in shared memory is HP heads of a slot, 128 bytes: one head of 128, or two of 64
+// that lie side by side in the cache (64 bytes, where they do not). A tile is four blocks
+// of 16 rows, a warp's each.
+template <int D, int HP, int NT, int LOAD>
 struct Rows8Cfg {
-  static constexpr int kRows = 8 * NT;                  // query heads of a pass
-  static constexpr int kStageBytes = 2 * kWarpKeys * D;  // a warp's K codes, then its V codes
-  static constexpr int kStages = (D == 128 ? 5 : 10) - (NT == 4 ? (D == 128 ? 1 : 2) : 0);
-  static constexpr int kORow = D + 4;  // floats between rows of obuf: lanes of a store on 32 banks
-  static constexpr int kOffMeta = kWarps * kStages * kStageBytes;
-  static constexpr int kOffScale = kOffMeta + kWarps * kStages * 16;             // float2 [kWarps][kStages][16]
-  static constexpr int kOffMl = kOffScale + kWarps * kStages * kWarpKeys * 8;    // float2 [kWarps][kRows]
-  static constexpr int kOffO = kOffMl + kWarps * kRows * 8;                      // float [2][kRows][kORow]
-  static constexpr int kOffScan = kOffO + 2 * kRows * kORow * 4;                 // the slice, scan scratch
-  static constexpr int kSmemBytes = kOffScan + 48 * 4;
-  static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+  static constexpr int kRows = 8 * NT;                         // query heads of a KV head in a pass
+  static constexpr int kRowBytes = HP * D;
+  static constexpr int kCtas = NT * kRowBytes <= 128 ? 3 : 2;  // per SM: what registers allow
+  static constexpr int kStageBytes = 2 * kTile * kRowBytes;    // a tile's K codes, then its V codes
+  // D = 128: 8 requests of 128K keys, 64/8 heads: 321 us, with four stages 349
+  static constexpr int kStages = LOAD == kSlots ? (kRowBytes == 64 ? 5 : kCtas == 3 ? 3 : 4)
+                                                : (kRowBytes == 128 ? 1 : 2) * (kCtas == 3 ? 3 : NT == 4 ? 5 : 6);
+  // what a tile's consumers have to know besides, made by the loader: as far ahead as
+  // the codes are, or with slots further, since their addresses come this way
+  static constexpr int kInfos = LOAD == kSlots ? 8 : kStages;
+  static constexpr int kScales = kTile * HP;
+  static constexpr int kOffMeta = kStages * kStageBytes;                  // int4 [kInfos]
+  static constexpr int kOffBar = kOffMeta + kInfos * 16;                  // full, empty [kInfos]
+  static constexpr int kOffScale = kOffBar + kInfos * 16;                 // float2 [kInfos][kScales]
+  static constexpr int kOffAt = kOffScale + kInfos * kScales * 8;         // slots: longlong2 [kInfos][kTile]
+  static constexpr int kOffMl = kOffAt + (LOAD == kSlots ? kInfos * kTile * 16 : 0);  // float2 [kWarps][HP][kRows]
+  static constexpr int kOffQ = kOffMl + kWarps * HP * kRows * 8;          // NT = 4: q's fragments
+  static constexpr int kOffScan = kOffQ + (NT == 4 ? HP * kRows * D * 2 : 0);  // the slice, scan scratch, abort flag
+  static constexpr int kSmemBytes = kOffScan + 49 * 4;
+  static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
+  static_assert(kWarps * HP * 8 * D * 4 == kStageBytes, "O of four warps' eight heads fits a stage");
   static_assert(kOffMeta >= 4096, "find_slice's rounds lie in the ring");
+  static_assert(kInfos > kStages || LOAD == kPages, "the loader runs ahead");
 };
 
-// Where 16-byte chunk c of row r lies in a row of D codes: eight rows' chunks c on all banks.
-template <int D>
+// Where 16-byte chunk c of row r lies in a row of BYTES: eight rows' chunks c on all
+// banks; what the 128- and 64-byte swizzles of TMA copies give.
+template <int BYTES>
 __device__ __forceinline__ int swz(int r, int c) {
-  return (D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4;
+  return (BYTES == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4;
 }
 
 // Two E4M3 codes as fp16, exact.
@@ -81,19 +104,32 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-// 8 bytes global -> shared, zeros when `in` is false.
-__device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(in ? 8 : 0) : "memory");
+// 8 bytes global -> shared.
+__device__ __forceinline__ void cp8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// A row of q as the MMA's B fragments: q4 of four columns each, in fp16. Returns what
-// the scores have to be multiplied by. All lanes of a row (4) call.
-template <int KS>
-__device__ __forceinline__ float q_fragments(uint2 (&q4)[KS], __half) {
-  return 1.0f;
+// This thread's cp.async copies so far, as an arrival at the barrier when they have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// The consumer warps' barrier.
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
+// A bf16 row of q as fp16: q4 of four columns each. Returns what the scores have to be
+// multiplied by. All lanes of a row (4) call.
 template <int KS>
-__device__ __forceinline__ float q_fragments(uint2 (&q4)[KS], __nv_bfloat16) {
+__device__ __forceinline__ float to_half(uint2 (&q4)[KS]) {
   uint32_t most = 0;  // of the magnitudes' bits: NaN above infinity above the rest
 #pragma unroll
   for (int k = 0; k < KS; ++k) {
@@ -116,434 +152,614 @@ __device__ __forceinline__ float q_fragments(uint2 (&q4)[KS], __nv_bfloat16) {
   return __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
 }
 
-template <int D, typename T, int NT, bool SEL>
-__global__ void __launch_bounds__(kThreads, 2) attn_rows8_kernel(const __grid_constant__ Rows8Args a) {
-  using C = Rows8Cfg<D, NT>;
+// The dense tiles of a slice, 32 at a time: tile i of the slice belongs to the token
+// whose tiles end behind it. Tokens are looked at 32 at a time too, so that a slice of
+// many short ones reads their metadata once per 32.
+struct Tile8 {
+  int t, kt, n;  // token, tile of the token, keys of the token
+  int32_t page;
+};
+struct TileWindow {
+  int t0, n, req, begin, end;  // the first token; of token t0 + lane: keys, request, its tiles within the slice
+
+  // from token t on, whose first tile would be tile `at` of the slice
+  __device__ __forceinline__ void open(const RowsArgs& a, int t, int at) {
+    const int lane = threadIdx.x & 31;
+    t0 = t;
+    n = req = 0;
+    int tiles = 0;
+    if (t + lane < a.n_tokens) {
+      n = token_keys(a, t + lane, &req, false);
+      tiles = tiles_of(n);
+    }
+    end = tiles;
+#pragma unroll
+    for (int i = 1; i < 32; i *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, end, i);
+      if (lane >= i) end += v;
+    }
+    end += at;
+    begin = end - tiles;
+  }
+  // lane i: tile `first` + i of the slice's `total`
+  __device__ __forceinline__ Tile8 batch(const RowsArgs& a, int first, int total) {
+    const int i = first + (threadIdx.x & 31);
+    Tile8 d{0, 0, 0, -1};
+    int of = 0;
+    bool found = i >= total;
+    while (true) {
+      const int all = __shfl_sync(0xffffffffu, end, 31);
+      int k = 0;  // the tokens that end before tile i
+#pragma unroll
+      for (int step = 16; step > 0; step /= 2)
+        if (__shfl_sync(0xffffffffu, end, k + step - 1) <= i) k += step;
+      const int b = __shfl_sync(0xffffffffu, begin, k), r = __shfl_sync(0xffffffffu, req, k);
+      const int keys = __shfl_sync(0xffffffffu, n, k);
+      if (!found && i < all) {
+        found = true;
+        d.t = t0 + k;
+        d.kt = i - b;
+        d.n = keys;
+        of = r;
+      }
+      if (__all_sync(0xffffffffu, found) || t0 + 32 >= a.n_tokens) break;
+      open(a, t0 + 32, all);
+    }
+    if (i < total && d.n > 0) d.page = a.block_table[static_cast<int64_t>(of) * a.bt_stride + d.kt];
+    return d;
+  }
+};
+
+template <int D, int HP, int NT, int LOAD>
+__global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
+    attn_rows8_kernel(const __grid_constant__ Rows8Args a, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv) {
+  using C = Rows8Cfg<D, HP, NT, LOAD>;
   using E = Elem<__half>;
-  constexpr int S = C::kStages;
-  constexpr int CH = D / 16;    // 16-byte chunks per row of codes
-  constexpr int KS = D / 16;    // MMA k steps of q.k
-  constexpr int RPI = 32 / CH;  // rows one cp.async instruction of a warp covers
+  constexpr bool SEL = LOAD == kSlots;
+  constexpr int S = C::kStages, I = C::kInfos, RB = C::kRowBytes;
+  constexpr int CH = D / 16;  // 16-byte chunks of a head's codes: MMA k steps of q.k
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, c = lane & 3;
-  const uint32_t ring_u = smem_u32(smem + warp * S * C::kStageBytes);
-  int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta) + warp * S;
-  float2* scales = reinterpret_cast<float2*>(smem + C::kOffScale) + warp * S * kWarpKeys;
-  float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
-  float* obuf = reinterpret_cast<float*>(smem + C::kOffO);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* empty = full + I;
+  int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta);
+  float2* scales = reinterpret_cast<float2*>(smem + C::kOffScale);
   Slice* slice = reinterpret_cast<Slice*>(smem + C::kOffScan);
+  int* abort_flag = reinterpret_cast<int*>(smem + C::kOffScan) + 48;
 
   const int col = blockIdx.x / a.passes, pass = blockIdx.x - col * a.passes;
-  const int part = col / a.hkv, h = col - part * a.hkv;  // slice (split) or token, KV head
-  const int head0 = pass * C::kRows;                     // first query head of the group in this pass
-  const int rows = min(C::kRows, a.group - head0);       // its query heads
+  // slice (split) or token, and the first of its KV heads
+  const int part = col / (a.hkv / HP), h0 = (col - part * (a.hkv / HP)) * HP;
 
-  // Launched while the stream's previous kernel drains: nothing is read before
-  // it has ended. The join's CTAs in turn may take the places of CTAs that have
-  // ended, and wait there.
+  if (threadIdx.x < I) {
+    mbar_init(&full[threadIdx.x], 33);  // lane 0 with the copies' bytes, and every lane's scales
+    mbar_init(&empty[threadIdx.x], kWarps);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) *abort_flag = 0;
+  // Launched while the stream's previous kernel drains: nothing is read before it has ended.
   pdl_wait();
-  if (a.split) pdl_launch_dependents();
   // ---- this CTA's slice
-  Cursor cur;
-  cur.fresh = true;
   if (a.split) {
-    find_slice<SEL>(a, part, blockIdx.x == 0, slice, reinterpret_cast<int*>(slice + 1), reinterpret_cast<int*>(smem));
-    cur.left = slice->left;
-    if (cur.left == 0) {  // fewer tiles than slices
+    find_slice<SEL, kThreads8>(a, part, blockIdx.x == 0, slice, reinterpret_cast<int*>(slice + 1),
+                               reinterpret_cast<int*>(smem));
+    if (slice->left == 0) {  // fewer tiles than slices
       if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int2(-1, 0);
       return;
     }
-    cur.t = slice->t;
-    cur.kt = slice->kt;
-    cur.n = slice->n;
-    cur.req = slice->req;
-    cur.tiles = tiles_of(cur.n);
-  } else {
-    cur.t = part;
-    cur.kt = 0;
-    if (SEL) {
-      cur.n = a.topk;
-      cur.req = 0;
-    } else {
-      cur.n = token_keys(a, cur.t, &cur.req, threadIdx.x == 0 && h == 0 && pass == 0);
-    }
-    cur.tiles = tiles_of(cur.n);
-    cur.left = cur.tiles;
+    fence_proxy_async();  // its scratch lies where copies will
+  } else if (threadIdx.x == 0) {
+    int req = 0;
+    slice->t = part;
+    slice->kt = 0;
+    slice->n = SEL ? a.topk : token_keys(a, part, &req, h0 == 0 && pass == 0);
+    slice->req = req;
+    slice->left = tiles_of(slice->n);
   }
-  int desc_token = -1, desc_last = 0;  // the slice ends inside a token that it began: which, and its last slice
+  __syncthreads();
+  const int total = slice->left;
 
-  // ---- the loader: one tile of this warp's 16 keys and their scales into a stage
-  const uint8_t* kbase = static_cast<const uint8_t*>(a.k);
-  const uint8_t* vbase = static_cast<const uint8_t*>(a.v);
-  int32_t nid = -1;  // dense: the next tile's page; selected: this lane's slot of the next tile (lane & 15)
-  auto fetch_id = [&]() {
-    nid = -1;
-    if (cur.left <= 0) return;
+  if (warp == kWarps) {
+    // ---- the loader: a tile's codes and scales into a stage, stage after stage. What it
+    // has to know first comes in whole batches, so that no tile waits for it by itself:
+    // dense: lane i has tile i of 32: its token, tile of the token, keys and page;
+    // selected: the slots of the next kAhead tiles, lane i's i and i + 32
+    TileWindow win;
+    Tile8 mine;
+    constexpr int kAhead = 3;
+    int32_t ids[kAhead][2];
+    const int each = SEL ? tiles_of(a.topk) : 0;  // a token's tiles
+    int t = slice->t, kt = slice->kt, ft = t, fkt = kt;  // selected: the tile at hand, the next to be fetched
+    auto fetch = [&](int32_t (&id)[2], bool in) {
+      id[0] = id[1] = -1;
+      const int j = fkt * kTile + lane;
+      const int32_t* p = a.physical + static_cast<int64_t>(ft) * a.topk + j;
+      if (in && j < a.topk) id[0] = p[0];
+      if (in && j + 32 < a.topk) id[1] = p[32];
+      if (++fkt == each) {
+        fkt = 0;
+        ++ft;
+      }
+    };
     if (SEL) {
-      const int j = cur.kt * kTile + warp * kWarpKeys + (lane & 15);
-      if (j < a.topk) nid = a.physical[static_cast<int64_t>(cur.t) * a.topk + j];
-    } else if (cur.n > 0) {
-      nid = a.block_table[static_cast<int64_t>(cur.req) * a.bt_stride + cur.kt];
-    }
-  };
-  auto issue = [&](int stage) {
-    if (cur.left > 0) {
-      const uint32_t kdst = ring_u + stage * C::kStageBytes;
-      const uint32_t vdst = kdst + kWarpKeys * D;
-      const uint32_t sdst = smem_u32(scales + stage * kWarpKeys);
-      const int ch = lane % CH, r0 = lane / CH;
-      uint32_t mask = 0;
-      if (SEL) {
-        const bool in = nid >= 0 && static_cast<int64_t>(nid) < a.num_slots;
-        if (nid < -1 || (nid >= 0 && !in)) flag_error(a.err, DSA_DEVERR_ID_RANGE);
-        mask = __ballot_sync(0xffffffffu, in) & 0xffffu;
-        // lanes 0-15 hold the K rows' offsets, lanes 16-31 the V rows'
-        const bool isv = lane >= 16;
-        const int64_t page = in ? nid / kBlock : 0, slot = in ? nid % kBlock : 0;
-        const int64_t off = isv ? page * a.v_page + slot * a.v_slot + h * a.v_head
-                                : page * a.k_page + slot * a.k_slot + h * a.k_head;
-        if (mask != 0) {
-          if (!isv) cp8(sdst + lane * 8, a.scale + page * a.s_page + slot / kScaleBlock * a.s_block + h * a.s_head, in);
 #pragma unroll
-          for (int i = 0; i < kWarpKeys / RPI; ++i) {
-            const int r = i * RPI + r0;
-            const int64_t ko = __shfl_sync(0xffffffffu, off, r);
-            const int64_t vo = __shfl_sync(0xffffffffu, off, r + 16);
-            const bool ok = (mask >> r) & 1;
-            const uint32_t d = r * D + swz<D>(r, ch);
-            cp16(kdst + d, kbase + ko + ch * 16, ok);
-            cp16(vdst + d, vbase + vo + ch * 16, ok);
+      for (int i = 0; i < kAhead; ++i) fetch(ids[i], i < total);
+    }
+    const int t1 = t, kt1 = kt, n1st = slice->n, left1st = tiles_of(slice->n) - kt;  // the first token: its keys, its tiles here
+    int32_t page1st = -1;
+    if (!SEL && lane < left1st && n1st > 0)
+      page1st = a.block_table[static_cast<int64_t>(slice->req) * a.bt_stride + kt + lane];
+    bool fresh = true, opened = false;
+    int stage = 0, phase = 1;  // of the I
+#pragma unroll 1
+    for (int it = 0; it < total; ++it) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase, abort_flag, a.err))) break;
+      const uint32_t sdst = smem_u32(scales + stage * C::kScales);
+      int n = a.topk, tiles = each;
+      int32_t page = -1;
+      if (!SEL) {
+        if (it % 32 == 0) {
+          if (it == 0 && (left1st >= 32 || left1st >= total)) {
+            mine = Tile8{t1, kt1 + lane, n1st, page1st};
+          } else {
+            if (!opened) win.open(a, t1, -kt1);
+            opened = true;
+            mine = win.batch(a, it, total);
           }
         }
+        t = __shfl_sync(0xffffffffu, mine.t, it % 32);
+        kt = __shfl_sync(0xffffffffu, mine.kt, it % 32);
+        n = __shfl_sync(0xffffffffu, mine.n, it % 32);
+        page = __shfl_sync(0xffffffffu, mine.page, it % 32);
+        tiles = tiles_of(n);
+      }
+      const bool ends = kt == tiles - 1, last = ends || it == total - 1;
+      const int flags = (fresh ? kFirst : 0) | (last ? kLast : 0) | (kt == 0 ? kStartsItem : 0) | (ends ? kEndsItem : 0);
+      const int more = (tiles - 1 - kt) << 4;
+      if (SEL) {
+        const int32_t n0 = ids[0][0], n1 = ids[0][1];
+        const bool in0 = n0 >= 0 && static_cast<int64_t>(n0) < a.num_slots;
+        const bool in1 = n1 >= 0 && static_cast<int64_t>(n1) < a.num_slots;
+        if ((n0 != -1 && !in0) || (n1 != -1 && !in1)) flag_error(a.err, DSA_DEVERR_ID_RANGE);
+        const uint32_t lo = __ballot_sync(0xffffffffu, in0), hi = __ballot_sync(0xffffffffu, in1);
+        longlong2* at = reinterpret_cast<longlong2*>(smem + C::kOffAt) + stage * kTile;  // K's and V's rows
+        const uint32_t id0 = in0 ? n0 : 0, id1 = in1 ? n1 : 0;
+        const uint32_t p0 = id0 / kBlock, s0 = id0 % kBlock, p1 = id1 / kBlock, s1 = id1 % kBlock;
+        at[lane] = make_longlong2(p0 * a.k_page + s0 * a.k_slot, p0 * a.v_page + s0 * a.v_slot);
+        at[lane + 32] = make_longlong2(p1 * a.k_page + s1 * a.k_slot, p1 * a.v_page + s1 * a.v_slot);
+        // scales [block][head of the row][key of the block]
+        const float* sp = a.scale + h0 * a.s_head;
+        const float* sc0 = sp + p0 * a.s_page + s0 / kScaleBlock * a.s_block;
+        const float* sc1 = sp + p1 * a.s_page + s1 / kScaleBlock * a.s_block;
+        const uint32_t d0 = sdst + (lane / kScaleBlock * HP * kScaleBlock + lane % kScaleBlock) * 8;
+#pragma unroll
+        for (int z = 0; z < HP; ++z) {
+          if (in0) cp8(d0 + z * kScaleBlock * 8, sc0 + z * a.s_head);
+          if (in1) cp8(d0 + (2 * HP + z) * kScaleBlock * 8, sc1 + z * a.s_head);
+        }
+        __syncwarp();  // the rows' places are written
+        if (lane == 0) {
+          meta[stage] = make_int4(lo, hi, t, more | flags);
+          mbar_arrive(&full[stage]);
+        }
       } else {
-        const int j0 = cur.kt * kTile + warp * kWarpKeys;
-        int have = min(kWarpKeys, cur.n - j0);
-        if (cur.n > 0 && (nid < 0 || static_cast<int64_t>(nid) >= a.num_blocks)) {
+        int have = max(0, min(kTile, n - kt * kTile));
+        if (have > 0 && (page < 0 || static_cast<int64_t>(page) >= a.num_blocks)) {
           if (lane == 0) flag_error(a.err, DSA_DEVERR_BLOCK_RANGE);
           have = 0;
         }
-        if (have > 0) {
-          mask = (1u << have) - 1u;
-          if (lane == 0) cp8(sdst, a.scale + nid * a.s_page + warp * a.s_block + h * a.s_head, true);
-          const uint8_t* kp = kbase + nid * a.k_page + static_cast<int64_t>(warp * kWarpKeys + r0) * a.k_slot +
-                              h * a.k_head + ch * 16;
-          const uint8_t* vp = vbase + nid * a.v_page + static_cast<int64_t>(warp * kWarpKeys + r0) * a.v_slot +
-                              h * a.v_head + ch * 16;
+        const int blocks = (have + kScaleBlock - 1) / kScaleBlock;
+        if (lane == 0) {
+          const uint32_t lo = have >= 32 ? 0xffffffffu : (1u << have) - 1u;
+          const uint32_t hi = have >= 64 ? 0xffffffffu : have > 32 ? (1u << (have - 32)) - 1u : 0u;
+          meta[stage] = make_int4(lo, hi, t, more | flags);
+          mbar_arrive_expect_tx(&full[stage], blocks * 2 * kScaleBlock * RB);
+        }
+        __syncwarp();
+        uint8_t* kdst = smem + stage * C::kStageBytes;
+        uint8_t* vdst = kdst + kTile * RB;
+        // lanes 0-3 a block of K each, 4-7 of V; lanes 0-4HP a block's and head's scales
+        const int b = lane & 3;
+        if (lane < 8 && b < blocks)
+          tma_load_4d((lane < 4 ? kdst : vdst) + b * kScaleBlock * RB, lane < 4 ? &mk : &mv, &full[stage], 0, h0 / HP,
+                      b * kScaleBlock, page);
+        if (lane < 4 * HP && b < blocks)
+          cp8(sdst + (b * HP + lane / 4) * kScaleBlock * 8,
+              a.scale + page * a.s_page + b * a.s_block + (h0 + lane / 4) * a.s_head);
+      }
+      cp_arrive(&full[stage]);
+      fresh = last;
+      if (SEL) {
 #pragma unroll
-          for (int i = 0; i < kWarpKeys / RPI; ++i) {
-            const int r = i * RPI + r0;
-            const bool ok = r < have;
-            const uint32_t d = r * D + swz<D>(r, ch);
-            cp16(kdst + d, ok ? kp + i * RPI * a.k_slot : kbase, ok);
-            cp16(vdst + d, ok ? vp + i * RPI * a.v_slot : vbase, ok);
-          }
+        for (int i = 0; i + 1 < kAhead; ++i) {
+          ids[i][0] = ids[i + 1][0];
+          ids[i][1] = ids[i + 1][1];
+        }
+        fetch(ids[kAhead - 1], it + kAhead < total);
+        if (++kt == each) {
+          kt = 0;
+          ++t;
         }
       }
-      const bool ends = cur.kt == cur.tiles - 1, last = ends || cur.left == 1;
-      if (lane == 0) {
-        const int flags = (cur.fresh ? kFirst : 0) | (last ? kLast : 0) | (cur.kt == 0 ? kStartsItem : 0) |
-                          (ends ? kEndsItem : 0);
-        meta[stage] = make_int4(static_cast<int>(mask) | (flags << 16), cur.t, cur.tiles - 1 - cur.kt, 0);
+      if (++stage == I) {
+        stage = 0;
+        phase ^= 1;
       }
-      // advance
-      cur.fresh = last;
-      --cur.left;
-      if (!ends) {
-        ++cur.kt;
-      } else {
-        cur.kt = 0;
-        ++cur.t;
-        if (cur.left > 0) enter_token<SEL>(a, cur);
+    }
+    cp_wait<0>();
+    return;
+  }
+
+  // ---- the consumers: a warp has a block of 16 keys and HP heads; lane (g, c) of it keys
+  // g, g + 8, query heads 2c, 2c + 1 of each eight, and columns 16y + 2g, 16y + 2g + 1 of O
+  const int g = lane >> 2, c = lane & 3;
+  const int head0 = pass * C::kRows;                // first query head of the group in this pass
+  const int rows = min(C::kRows, a.group - head0);  // its query heads
+  float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+  uint2* qs = reinterpret_cast<uint2*>(smem + C::kOffQ);
+  int desc_token = -1, desc_last = 0;  // the slice ends inside a token that it began: which, and its last slice
+  float o[HP][NT][CH][4];
+  float m[HP][NT][2], l[HP][NT][2], rf[HP][NT][2];
+  uint2 qf[HP][NT == 4 ? 1 : NT][CH];
+  bool starts = true;
+  const float NEG = -INFINITY;
+  // where ldmatrix's rows lie in a stage; chunk k of them is at the address with k << 4 flipped
+  const int krow = warp * kWarpKeys + (lane & 7) + ((lane >> 4) << 3);
+  const uint32_t kaddr = smem_u32(smem) + krow * RB + swz<RB>(krow, (lane >> 3) & 1);
+  const int vrow = warp * kWarpKeys + (lane & 7) + (((lane >> 3) & 1) << 3);
+  const uint32_t vaddr = smem_u32(smem) + (kTile + vrow) * RB + swz<RB>(vrow, lane >> 4);
+  // slots: the copies of this warp's rows of a tile, whose places the loader has left
+  constexpr int RC = RB / 16, RPI = 32 / RC;  // 16-byte pieces of a row, rows that a copy of the warp covers
+  const int ch = lane % RC, r0 = lane / RC;
+  const uint8_t* kb = static_cast<const uint8_t*>(a.k) + h0 * a.k_head + ch * 16;
+  const uint8_t* vb = static_cast<const uint8_t*>(a.v) + h0 * a.v_head + ch * 16;
+  int info = 0, into = 0, next = 0, nphase = 0;  // of the tile at hand; of the next to be copied: stage, info
+  auto issue = [&](bool in) {
+    if (in) {
+      mbar_wait(&full[next], nphase, abort_flag, a.err);
+      __syncwarp();
+      const int4 mt = meta[next];
+      const uint32_t mask = (static_cast<uint32_t>(warp < 2 ? mt.x : mt.y) >> (16 * (warp & 1))) & 0xffffu;
+      const longlong2* at = reinterpret_cast<const longlong2*>(smem + C::kOffAt) + next * kTile + warp * kWarpKeys;
+      const uint32_t dst = smem_u32(smem) + into * C::kStageBytes + warp * kWarpKeys * RB;
+#pragma unroll
+      for (int i = 0; i < kWarpKeys / RPI; ++i) {
+        const int r = i * RPI + r0;
+        if ((mask >> r) & 1) {
+          const longlong2 o = at[r];
+          const uint32_t d = dst + r * RB + swz<RB>(r, ch);
+          cp16(d, kb + o.x, true);
+          cp16(d + kTile * RB, vb + o.y, true);
+        }
       }
-      fetch_id();
+      if (++into == S) into = 0;
+      if (++next == I) {
+        next = 0;
+        nphase ^= 1;
+      }
     }
     cp_commit();
   };
-
-  const int total = cur.left;
-  fetch_id();
+  if (SEL) {
 #pragma unroll 1
-  for (int s = 0; s < S - 1; ++s) issue(s);
-
-  // ---- the consumer: lane (g, c) has keys g, g + 8 of a tile, query heads 2c, 2c + 1
-  // of each eight, and columns 16y + 2g, 16y + 2g + 1 of O
-  float o[NT][CH][4];
-  float m[NT][2], l[NT][2], rf[NT][2];
-  uint2 qf[NT][KS];
-  bool starts = true;
-  const float NEG = -INFINITY;
-  int stage = 0, into = S - 1;
+    for (int i = 0; i < S - 1; ++i) issue(i < total);
+  }
+  int stage = 0, phase = 0;
 #pragma unroll 1
   for (int it = 0; it < total; ++it) {
-    cp_wait<S - 2>();
-    __syncwarp();
-    const int4 mt = meta[stage];
-    const uint32_t mask = static_cast<uint32_t>(mt.x) & 0xffffu;
-    const int flags = mt.x >> 16;
-    issue(into);  // the stage consumed in the previous step
-    if (++into == S) into = 0;
+    if (SEL) {
+      cp_wait<S - 2>();
+      __syncwarp();
+      issue(it + S - 1 < total);  // into the stage consumed in the previous step
+    } else {
+      mbar_wait(&full[info], phase, abort_flag, a.err);  // in vain: flagged, and the rest is unspecified
+      __syncwarp();
+    }
+    const int4 mt = meta[info];
+    const uint32_t mask = (static_cast<uint32_t>(warp < 2 ? mt.x : mt.y) >> (16 * (warp & 1))) & 0xffffu;
+    const int flags = mt.w & 15;
 
     if (flags & kFirst) {
       starts = flags & kStartsItem;
-      const T* q = static_cast<const T*>(a.q) + mt.y * a.q_row + static_cast<int64_t>(h * a.group + head0) * a.q_head;
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        m[x][0] = m[x][1] = NEG;
-        l[x][0] = l[x][1] = 0.0f;
+      for (int z = 0; z < HP; ++z) {
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + mt.z * a.q_row +
+                            (static_cast<int64_t>(h0 + z) * a.group + head0) * a.q_head;
 #pragma unroll
-        for (int y = 0; y < CH; ++y) o[x][y][0] = o[x][y][1] = o[x][y][2] = o[x][y][3] = 0.0f;
-        const bool in = x * 8 + g < rows;
-        const T* qp = q + (in ? x * 8 + g : 0) * a.q_head + c * 4;
+        for (int x = 0; x < NT; ++x) {
+          m[z][x][0] = m[z][x][1] = NEG;
+          l[z][x][0] = l[z][x][1] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-          qf[x][k] = in ? *reinterpret_cast<const uint2*>(qp + k * 16) : make_uint2(0, 0);
-        const float f = q_fragments<KS>(qf[x], T()) * a.scale_log2;  // of row x * 8 + g
-        rf[x][0] = __shfl_sync(0xffffffffu, f, 8 * c);
-        rf[x][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+          for (int y = 0; y < CH; ++y) o[z][x][y][0] = o[z][x][y][1] = o[z][x][y][2] = o[z][x][y][3] = 0.0f;
+          uint2 q4[CH];
+          const bool in = x * 8 + g < rows;
+          const uint16_t* qp = q + (in ? x * 8 + g : 0) * a.q_head + c * 4;
+#pragma unroll
+          for (int k = 0; k < CH; ++k) q4[k] = in ? *reinterpret_cast<const uint2*>(qp + k * 16) : make_uint2(0, 0);
+          const float f = (a.bf16 ? to_half<CH>(q4) : 1.0f) * a.scale_log2;  // of row x * 8 + g
+          rf[z][x][0] = __shfl_sync(0xffffffffu, f, 8 * c);
+          rf[z][x][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+          if constexpr (NT == 4) {  // in shared memory, each warp's eight heads for all
+            if (x == warp) {
+#pragma unroll
+              for (int k = 0; k < CH; ++k) qs[((z * NT + x) * CH + k) * 32 + lane] = q4[k];
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < CH; ++k) qf[z][x][k] = q4[k];
+          }
+        }
       }
+      if (NT == 4) consumers_sync();
     }
 
     if (mask != 0) {
-      const uint32_t ks = ring_u + stage * C::kStageBytes, vs = ks + kWarpKeys * D;
+      if (mask != 0xffffu) {
+        // an absent key's V may be anything, NaN among it, and 0 * NaN is NaN
+        const int r = lane & 15;
+        if (!((mask >> r) & 1)) {
+          uint4* row = reinterpret_cast<uint4*>(smem + stage * C::kStageBytes + (kTile + warp * kWarpKeys + r) * RB +
+                                                (lane >> 4) * (RB / 2));
+#pragma unroll
+          for (int i = 0; i < RB / 32; ++i) row[i] = make_uint4(0, 0, 0, 0);
+        }
+        if (!SEL) fence_proxy_async();  // before the copies that follow into this stage
+        __syncwarp();
+      }
       // S^T = K q^T
-      float s[NT][4];
+      float s[HP][NT][4];
 #pragma unroll
-      for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
+      for (int z = 0; z < HP; ++z)
+#pragma unroll
+        for (int x = 0; x < NT; ++x) s[z][x][0] = s[z][x][1] = s[z][x][2] = s[z][x][3] = 0.0f;
       {
-        const int row = (lane & 7) + ((lane >> 4) << 3), cb = (lane >> 3) & 1;
-        const uint32_t base = ks + row * D;
+        const uint32_t base = kaddr + stage * C::kStageBytes;
 #pragma unroll
-        for (int k = 0; k < KS; k += 2) {
-          uint32_t b[4];  // keys 0-7 chunks k, k + 1; keys 8-15 chunks k, k + 1
-          ldsm4(b, base + swz<D>(row, k + cb));
+        for (int j = 0; j < HP * CH; j += 2) {
+          const int z = j / CH, k = j % CH;
+          uint32_t b[4];  // keys 0-7 chunks j, j + 1; keys 8-15 chunks j, j + 1
+          ldsm4(b, base ^ (j << 4));
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const uint32_t f[4] = {half2_of(b[u]), half2_of(b[2 + u]), half2_of_high(b[u]), half2_of_high(b[2 + u])};
 #pragma unroll
-            for (int x = 0; x < NT; ++x) E::mma(s[x], f, qf[x][k + u].x, qf[x][k + u].y);
+            for (int x = 0; x < NT; ++x) {
+              if constexpr (NT == 4) {
+                const uint2 q2 = qs[((z * NT + x) * CH + k + u) * 32 + lane];
+                E::mma(s[z][x], f, q2.x, q2.y);
+              } else {
+                E::mma(s[z][x], f, qf[z][x][k + u].x, qf[z][x][k + u].y);
+              }
+            }
           }
         }
       }
-      // scores in powers of two with V's scale in them; absent keys out
-      const float2* sc = scales + stage * kWarpKeys;
-      const float2 s0 = sc[SEL ? g : 0], s1 = SEL ? sc[g + 8] : s0;
-      const float v0 = fminf(fmaxf(s0.y, kLeastScale), kMostScale), v1 = fminf(fmaxf(s1.y, kLeastScale), kMostScale);
-      const float lv0 = __log2f(v0), lv1 = __log2f(v1);
-      const float iv0 = __frcp_rn(v0), iv1 = __frcp_rn(v1);
+      uint32_t p[HP][NT][2];
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        s[x][0] = fmaf(s[x][0], rf[x][0] * s0.x, lv0);
-        s[x][1] = fmaf(s[x][1], rf[x][1] * s0.x, lv0);
-        s[x][2] = fmaf(s[x][2], rf[x][0] * s1.x, lv1);
-        s[x][3] = fmaf(s[x][3], rf[x][1] * s1.x, lv1);
-      }
-      if (mask != 0xffffu) {
-        const bool in0 = (mask >> g) & 1, in1 = (mask >> (g + 8)) & 1;
+      for (int z = 0; z < HP; ++z) {
+        // scores in powers of two with V's scale in them; absent keys out
+        const float2* sc = scales + info * C::kScales + (warp * HP + z) * kScaleBlock + (SEL ? g : 0);
+        const float2 s0 = sc[0], s1 = SEL ? sc[8] : s0;
+        const float v0 = fminf(fmaxf(s0.y, kLeastScale), kMostScale), v1 = fminf(fmaxf(s1.y, kLeastScale), kMostScale);
+        const float lv0 = lg2(v0), lv1 = lg2(v1);
+        const float iv0 = rcp(v0), iv1 = rcp(v1);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-          if (!in0) s[x][0] = s[x][1] = NEG;
-          if (!in1) s[x][2] = s[x][3] = NEG;
-        }
-      }
-      uint32_t p[NT][2];
-#pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        float t0 = fmaxf(s[x][0], s[x][2]), t1 = fmaxf(s[x][1], s[x][3]);
-        const bool move = t0 > m[x][0] + (E::kHead + kSlack) || t1 > m[x][1] + (E::kHead + kSlack);
-        if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-          for (int i = 4; i < 32; i *= 2) {
-            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, i));
-            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, i));
+          float(&w)[4] = s[z][x];
+          w[0] = fmaf(w[0], rf[z][x][0] * s0.x, lv0);
+          w[1] = fmaf(w[1], rf[z][x][1] * s0.x, lv0);
+          w[2] = fmaf(w[2], rf[z][x][0] * s1.x, lv1);
+          w[3] = fmaf(w[3], rf[z][x][1] * s1.x, lv1);
+          if (mask != 0xffffu) {
+            if (!((mask >> g) & 1)) w[0] = w[1] = NEG;
+            if (!((mask >> (g + 8)) & 1)) w[2] = w[3] = NEG;
           }
-          const float n0 = fmaxf(m[x][0], t0 - E::kHead), n1 = fmaxf(m[x][1], t1 - E::kHead);
-          const float f0 = m[x][0] == NEG ? 0.0f : ex2(m[x][0] - n0), f1 = m[x][1] == NEG ? 0.0f : ex2(m[x][1] - n1);
-          m[x][0] = n0;
-          m[x][1] = n1;
-          l[x][0] *= f0;
-          l[x][1] *= f1;
+          float t0 = fmaxf(w[0], w[2]), t1 = fmaxf(w[1], w[3]);
+          float(&mm)[2] = m[z][x];
+          const bool move = t0 > mm[0] + (E::kHead + kSlack) || t1 > mm[1] + (E::kHead + kSlack);
+          if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int y = 0; y < CH; ++y) {
-            o[x][y][0] *= f0;
-            o[x][y][1] *= f1;
-            o[x][y][2] *= f0;
-            o[x][y][3] *= f1;
+            for (int i = 4; i < 32; i *= 2) {
+              t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, i));
+              t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, i));
+            }
+            const float n0 = fmaxf(mm[0], t0 - E::kHead), n1 = fmaxf(mm[1], t1 - E::kHead);
+            const float f0 = mm[0] == NEG ? 0.0f : ex2(mm[0] - n0), f1 = mm[1] == NEG ? 0.0f : ex2(mm[1] - n1);
+            mm[0] = n0;
+            mm[1] = n1;
+            l[z][x][0] *= f0;
+            l[z][x][1] *= f1;
+#pragma unroll
+            for (int y = 0; y < CH; ++y) {
+              o[z][x][y][0] *= f0;
+              o[z][x][y][1] *= f1;
+              o[z][x][y][2] *= f0;
+              o[z][x][y][3] *= f1;
+            }
           }
+          const float m0 = mm[0] == NEG ? 0.0f : mm[0], m1 = mm[1] == NEG ? 0.0f : mm[1];
+          const float e0 = ex2(w[0] - m0), e1 = ex2(w[1] - m1), e2 = ex2(w[2] - m0), e3 = ex2(w[3] - m1);
+          // the sums are taken before the weights are rounded for the MMA: the
+          // rounding errors (half a step each, unbiased) enter the numerator only
+          l[z][x][0] = fmaf(e0, iv0, fmaf(e2, iv1, l[z][x][0]));
+          l[z][x][1] = fmaf(e1, iv0, fmaf(e3, iv1, l[z][x][1]));
+          p[z][x][0] = transpose8(E::pack(e0, e1));
+          p[z][x][1] = transpose8(E::pack(e2, e3));
         }
-        const float m0 = m[x][0] == NEG ? 0.0f : m[x][0], m1 = m[x][1] == NEG ? 0.0f : m[x][1];
-        const float e0 = ex2(s[x][0] - m0), e1 = ex2(s[x][1] - m1), e2 = ex2(s[x][2] - m0), e3 = ex2(s[x][3] - m1);
-        // the sums are taken before the weights are rounded for the MMA: the
-        // rounding errors (half a step each, unbiased) enter the numerator only
-        l[x][0] = fmaf(e0, iv0, fmaf(e2, iv1, l[x][0]));
-        l[x][1] = fmaf(e1, iv0, fmaf(e3, iv1, l[x][1]));
-        p[x][0] = transpose8(E::pack(e0, e1));
-        p[x][1] = transpose8(E::pack(e2, e3));
       }
       // O^T += V^T P^T
       {
-        const int row = (lane & 7) + (((lane >> 3) & 1) << 3), cb = lane >> 4;
-        const uint32_t base = vs + row * D;
+        const uint32_t base = vaddr + stage * C::kStageBytes;
 #pragma unroll
-        for (int y = 0; y < CH; y += 2) {
-          uint32_t b[4];  // chunk y: keys 0-7, 8-15; chunk y + 1: keys 0-7, 8-15
-          ldsm4_t(b, base + swz<D>(row, y + cb));
+        for (int j = 0; j < HP * CH; j += 2) {
+          const int z = j / CH, y = j % CH;
+          uint32_t b[4];  // chunk j: keys 0-7, 8-15; chunk j + 1: keys 0-7, 8-15
+          ldsm4_t(b, base ^ (j << 4));
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             // codes (key 2c: even, odd column; key 2c + 1: even, odd) -> a column's two keys
             const uint32_t w0 = __byte_perm(b[2 * u], 0, 0x3120), w1 = __byte_perm(b[2 * u + 1], 0, 0x3120);
             const uint32_t f[4] = {half2_of(w0), half2_of_high(w0), half2_of(w1), half2_of_high(w1)};
 #pragma unroll
-            for (int x = 0; x < NT; ++x) E::mma(o[x][y + u], f, p[x][0], p[x][1]);
+            for (int x = 0; x < NT; ++x) E::mma(o[z][x][y + u], f, p[z][x][0], p[z][x][1]);
           }
         }
       }
     }
-    if (++stage == S) stage = 0;
 
     if (flags & kLast) {
-      // ---- the four warps' partial results into one
+      // ---- the partial results of the warps that share a head into one: each leaves its
+      // O, eight query heads at a time, in the stage that has just been read; then 16
+      // threads a row add them
+      const bool whole = starts && (flags & kEndsItem);
+      const int r8 = threadIdx.x / 16;                                  // row of the eight
+      constexpr int W = D / 16;                                         // columns of a thread
+      const int at = r8 * D + ((threadIdx.x % 16 * W) ^ (r8 / 2 * 8));  // where they lie in eight rows of O
+      float* os = reinterpret_cast<float*>(smem + stage * C::kStageBytes);
 #pragma unroll
-      for (int x = 0; x < NT; ++x)
+      for (int x = 0; x < NT; ++x) {
+        consumers_sync();  // all have read the stage, or the rows before
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float t = l[x][e];
+        for (int z = 0; z < HP; ++z) {
+          if (x == 0) {
 #pragma unroll
-          for (int i = 4; i < 32; i *= 2) t += __shfl_xor_sync(0xffffffffu, t, i);
-          l[x][e] = t;
-        }
-      __syncthreads();  // the previous item's buffers are read
-      if (g == 0) {
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) ml[warp * C::kRows + x * 8 + 2 * c + e] = make_float2(m[x][e], l[x][e]);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float M = NEG, L = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * C::kRows + x * 8 + 2 * c + e].x);
-          const float Ms = M == NEG ? 0.0f : M;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 v = ml[w * C::kRows + x * 8 + 2 * c + e];
-            L += v.y * ex2(v.x - Ms);
-          }
-          const float f = ex2(m[x][e] - Ms);
-#pragma unroll
-          for (int y = 0; y < CH; ++y) {
-            o[x][y][e] *= f;
-            o[x][y][2 + e] *= f;
-          }
-          m[x][e] = M;
-          l[x][e] = L;
-        }
-      // O of warps 2, 3 into 0, 1, then of 1 into 0
-#pragma unroll
-      for (int step = 2; step >= 1; step >>= 1) {
-        if (warp >= step && warp < 2 * step) {
-#pragma unroll
-          for (int x = 0; x < NT; ++x)
-#pragma unroll
-            for (int y = 0; y < CH; ++y)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<float2*>(obuf + ((warp - step) * C::kRows + x * 8 + 2 * c + e) * C::kORow + y * 16 +
-                                           2 * g) = make_float2(o[x][y][e], o[x][y][2 + e]);
-        }
-        __syncthreads();
-        if (warp < step) {
-#pragma unroll
-          for (int x = 0; x < NT; ++x)
-#pragma unroll
-            for (int y = 0; y < CH; ++y)
+            for (int x2 = 0; x2 < NT; ++x2)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float2 v = *reinterpret_cast<const float2*>(
-                    obuf + (warp * C::kRows + x * 8 + 2 * c + e) * C::kORow + y * 16 + 2 * g);
-                o[x][y][e] += v.x;
-                o[x][y][2 + e] += v.y;
+                float t = l[z][x2][e];
+#pragma unroll
+                for (int i = 4; i < 32; i *= 2) t += __shfl_xor_sync(0xffffffffu, t, i);
+                if (g == 0) ml[(warp * HP + z) * C::kRows + x2 * 8 + 2 * c + e] = make_float2(m[z][x2][e], t);
               }
+          }
+          float* mine = os + (warp * HP + z) * 8 * D;
+#pragma unroll
+          for (int y = 0; y < CH; ++y)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)  // columns moved by eights: four rows' stores on 32 banks
+              *reinterpret_cast<float2*>(mine + (2 * c + e) * D + ((y * 16 + 2 * g) ^ (c * 8))) =
+                  make_float2(o[z][x][y][e], o[z][x][y][2 + e]);
         }
-        if (step == 2) __syncthreads();
-      }
-      const bool whole = starts && (flags & kEndsItem);
-      if (warp == 0) {
-        // slot 2c: a part that continues an earlier CTA's item; 2c + 1: the beginning of one
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0);
+        consumers_sync();
+        const int r = x * 8 + r8;
+        if (r < rows) {
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
+          for (int z = 0; z < HP; ++z) {
+            float M = NEG, L = 0.0f, sum[W];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = x * 8 + 2 * c + e;
-            if (r >= rows) continue;
-            const float L = l[x][e], M = m[x][e];
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[(w * HP + z) * C::kRows + r].x);
+            const float Ms = M == NEG ? 0.0f : M;
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum[i] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              const float2 v = ml[(w * HP + z) * C::kRows + r];
+              const float f = ex2(v.x - Ms);
+              const float* p = os + (w * HP + z) * 8 * D + at;
+              L = fmaf(v.y, f, L);
+#pragma unroll
+              for (int i = 0; i < W; i += 4) {
+                const float4 u = *reinterpret_cast<const float4*>(p + i);
+                sum[i] = fmaf(u.x, f, sum[i]);
+                sum[i + 1] = fmaf(u.y, f, sum[i + 1]);
+                sum[i + 2] = fmaf(u.z, f, sum[i + 2]);
+                sum[i + 3] = fmaf(u.w, f, sum[i + 3]);
+              }
+            }
+            const int c0 = threadIdx.x % 16 * W;
             if (whole) {
-              const int64_t head = static_cast<int64_t>(h) * a.group + head0 + r;
-              T* out = static_cast<T*>(a.out) + mt.y * a.out_row + head * a.out_head;
+              const int64_t head = static_cast<int64_t>(h0 + z) * a.group + head0 + r;
+              uint16_t* out = static_cast<uint16_t*>(a.out) + mt.z * a.out_row + head * a.out_head + c0;
               // L = 0: no key, or only scores of -infinity (O is then 0, or NaN by 0 times
               // a V that is NaN); no score but NaN leaves M alone and L NaN
               const float inv = 1.0f / L;
+              uint32_t w[W / 2];
 #pragma unroll
-              for (int y = 0; y < CH; ++y)
-                *reinterpret_cast<uint32_t*>(out + y * 16 + 2 * g) =
-                    L == 0.0f ? 0u : Elem<T>::pack(o[x][y][e] * inv, o[x][y][2 + e] * inv);
-              if (a.lse != nullptr && g == 0)
-                a.lse[static_cast<int64_t>(mt.y) * a.heads + head] =
+              for (int i = 0; i < W; i += 2)
+                w[i / 2] = L == 0.0f ? 0u
+                           : a.bf16  ? Elem<__nv_bfloat16>::pack(sum[i] * inv, sum[i + 1] * inv)
+                                     : E::pack(sum[i] * inv, sum[i + 1] * inv);
+              if constexpr (W == 8)
+                *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+              else
+                *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+              if (a.lse != nullptr && c0 == 0)
+                a.lse[static_cast<int64_t>(mt.z) * a.heads + head] =
                     L == 0.0f ? NEG : (M + log2f(L)) * 0.6931471805599453f;
             } else {
-              float* po = a.part_o + (slot * C::kRows + r) * D;
+              // slot 2c: a part that continues an earlier CTA's item; 2c + 1: the beginning of one
+              const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0)) * HP + z;
+              float* po = a.part_o + (slot * C::kRows + r) * D + c0;
 #pragma unroll
-              for (int y = 0; y < CH; ++y)
-                *reinterpret_cast<float2*>(po + y * 16 + 2 * g) = make_float2(o[x][y][e], o[x][y][2 + e]);
-              if (g == 0) a.part_ml[slot * C::kRows + r] = make_float2(M, L);
+              for (int i = 0; i < W; i += 4)
+                *reinterpret_cast<float4*>(po + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
+              if (c0 == 0) a.part_ml[slot * C::kRows + r] = make_float2(M, L);
             }
           }
+        }
       }
-      if (!whole && starts) {  // it began here and goes on: mt.z tiles after this one, in the next slices
-        desc_token = mt.y;
-        const int64_t end = slice->end + mt.z;
+      if (SEL)
+        consumers_sync();  // all have read it, before the copies that follow into this stage
+      else
+        fence_proxy_async();
+      if (!whole && starts) {  // it began here and goes on: so many tiles after this one, in the next slices
+        desc_token = mt.z;
+        const int64_t end = slice->end + (mt.w >> 4);
         desc_last = static_cast<int>((end * slice->in_use + slice->all - 1) / slice->all) - 1;
       }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[info]);
+    if (++stage == S) stage = 0;
+    if (++info == I) {
+      info = 0;
+      phase ^= 1;
+    }
   }
-  cp_wait<0>();
+  if (SEL) cp_wait<0>();
+  if (*static_cast<volatile int*>(abort_flag)) {
+    // a wait gave up: copies in flight land in this CTA's memory, so they get their time again
+    const unsigned long long t0 = global_ns();
+    for (int s = 0; s < I && s < total; ++s)
+      while (!mbar_try_wait(smem_u32(&full[s]), ((total - 1 - s) / I) & 1) && global_ns() - t0 < kWaitLimitNs) {
+      }
+  }
   if (a.split && threadIdx.x == 0) a.desc[blockIdx.x] = make_int2(desc_token, desc_last);
 }
 
-template <int D, typename T, int NT, bool SEL>
-cudaError_t launch(const Rows8Args& a, int grid, int dtype, cudaStream_t stream) {
+template <int D, int HP, int NT, int LOAD>
+cudaError_t launch(const Rows8Args& a, int grid, const CUtensorMap* maps, cudaStream_t stream) {
   static uint64_t done = 0;
-  using C = Rows8Cfg<D, NT>;
-  auto* fn = attn_rows8_kernel<D, T, NT, SEL>;
+  using C = Rows8Cfg<D, HP, NT, LOAD>;
+  auto* fn = attn_rows8_kernel<D, HP, NT, LOAD>;
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(fn), C::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(fn, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, a)) != cudaSuccess || !a.split) return e;
-  return launch_attn_join(a, D, dtype, grid, C::kRows, stream);
+  e = launch_pdl(fn, dim3(grid), dim3(kThreads8), C::kSmemBytes, stream, a, maps[0], maps[1]);
+  if (e != cudaSuccess || !a.split) return e;
+  // the next kernel is not let in while the join runs: its CTAs would take places
+  // where one of this kernel's three would have to go (8 x 128K keys: 321 us, so 315)
+  return launch_attn_join(a, D, a.bf16 ? DSA_BF16 : DSA_FP16, C::kRows, false, stream);
 }
 
-template <int D, typename T>
-cudaError_t launch_dt(const Rows8Args& a, int grid, int dtype, bool sel, cudaStream_t stream) {
-  if (a.group <= 8)
-    return sel ? launch<D, T, 1, true>(a, grid, dtype, stream) : launch<D, T, 1, false>(a, grid, dtype, stream);
-  if (a.group <= 16)
-    return sel ? launch<D, T, 2, true>(a, grid, dtype, stream) : launch<D, T, 2, false>(a, grid, dtype, stream);
-  return sel ? launch<D, T, 4, true>(a, grid, dtype, stream) : launch<D, T, 4, false>(a, grid, dtype, stream);
+template <int D, int HP, int LOAD>
+cudaError_t launch_rows(const Rows8Args& a, int grid, const CUtensorMap* maps, cudaStream_t stream) {
+  if (a.group <= 8) return launch<D, HP, 1, LOAD>(a, grid, maps, stream);
+  if (a.group <= 16) return launch<D, HP, 2, LOAD>(a, grid, maps, stream);
+  return launch<D, HP, 4, LOAD>(a, grid, maps, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_rows8(const Rows8Args& a, int head_dim, int dtype, bool selected, cudaStream_t stream) {
-  const int grid = a.slices * a.hkv * a.passes;
-  if (dtype == DSA_BF16)
-    return head_dim == 128 ? launch_dt<128, __nv_bfloat16>(a, grid, dtype, selected, stream)
-                           : launch_dt<64, __nv_bfloat16>(a, grid, dtype, selected, stream);
-  return head_dim == 128 ? launch_dt<128, __half>(a, grid, dtype, selected, stream)
-                         : launch_dt<64, __half>(a, grid, dtype, selected, stream);
+cudaError_t launch_attn_rows8(const Rows8Args& a, int head_dim, bool selected, const CUtensorMap* maps,
+                              cudaStream_t stream) {
+  const int grid = a.slices * (a.hkv / a.joint) * a.passes;
+  if (!selected) {
+    if (head_dim == 128) return launch_rows<128, 1, kPages>(a, grid, maps, stream);
+    return a.pairs ? launch_rows<64, 2, kPages>(a, grid, maps, stream) : launch_rows<64, 1, kPages>(a, grid, maps, stream);
+  }
+  if (head_dim == 128) return launch_rows<128, 1, kSlots>(a, grid, maps, stream);
+  return a.pairs ? launch_rows<64, 2, kSlots>(a, grid, maps, stream) : launch_rows<64, 1, kSlots>(a, grid, maps, stream);
 }
 
 }  // namespace dsa

@@ -86,7 +86,7 @@ def check_lists(q, k, v, sc, lists, out, lse, dtype, scale, only=None):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("hq,hkv", [(2, 2), (16, 2), (7, 1), (32, 2), (20, 1), (40, 1)])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (16, 2), (7, 1), (32, 2), (20, 1), (40, 1), (6, 3), (40, 2)])
 def test_decode_lengths_and_groups(dtype, d, hq, hkv):
     s = Step8(hq + d, [1, 0, 15, 16, 17, 64, 65, 300], [1] * 8, hq, hkv, d, dtype)
     err = i32([0])
@@ -110,17 +110,18 @@ def test_decode_split_over_the_length(dtype, d, hq, hkv):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
-@pytest.mark.parametrize("layout", ["heads", "joined"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("layout", ["heads", "joined", "loose"])
 @pytest.mark.parametrize("keys", [[300, 64, 129], [3000, 64, 129]])
-def test_decode_cache_layouts_and_strided_rows(layout, keys):
-    s = Step8(3, keys, [1, 1, 1], 8, 2, 128, torch.bfloat16, layout)
+def test_decode_cache_layouts_and_strided_rows(layout, keys, d):
+    s = Step8(3, keys, [1, 1, 1], 8, 2, d, torch.bfloat16, layout)
     wide = torch.zeros((3, 9, 200), dtype=torch.bfloat16, device=DEV)   # q and out as views of wider tensors
-    q = wide[:, 1:, 8:136]
+    q = wide[:, 1:, 8:8 + d]
     q.copy_(s.q)
     obuf = torch.full((3, 8, 160), 5.0, dtype=torch.bfloat16, device=DEV)
-    out, lse = dsa.attn_decode8(s.batch, q, s.k, s.v, s.sc, out=obuf[:, :, 16:144])
+    out, lse = dsa.attn_decode8(s.batch, q, s.k, s.v, s.sc, out=obuf[:, :, 16:16 + d])
     s.check(out, lse)
-    assert bool((obuf[:, :, :16] == 5).all()) and bool((obuf[:, :, 144:] == 5).all())
+    assert bool((obuf[:, :, :16] == 5).all()) and bool((obuf[:, :, 16 + d:] == 5).all())
 
 
 def test_decode_several_tokens_per_request_and_padding():
@@ -295,7 +296,7 @@ def check_selected(q, k, v, sc, phys, out, lse, dtype):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("tokens,topk,hq,hkv", [(3, 1, 4, 2), (2, 37, 8, 8), (5, 512, 24, 2), (3, 1030, 33, 1),
-                                                (70, 600, 6, 2)])
+                                                (70, 600, 6, 2), (9, 300, 16, 16), (2, 2048, 40, 8)])
 def test_selected_shapes(dtype, d, tokens, topk, hq, hkv):
     q, k, v, sc, phys = selected_case(tokens + topk, tokens, topk, hq, hkv, d, dtype)
     phys[1] = -1                       # a token with nothing selected
@@ -307,9 +308,11 @@ def test_selected_shapes(dtype, d, tokens, topk, hq, hkv):
     assert int(err.item()) == 0
 
 
-@pytest.mark.parametrize("layout", ["heads", "joined"])
-def test_selected_layouts_and_bad_slots(layout):
-    q, k, v, sc, phys = selected_case(5, 4, 900, 8, 4, 128, torch.bfloat16, layout=layout)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(8, 4), (36, 4), (80, 4), (6, 6)])
+@pytest.mark.parametrize("layout", ["pages", "heads", "joined", "loose"])
+def test_selected_layouts_and_bad_slots(layout, hq, hkv, d):
+    q, k, v, sc, phys = selected_case(5, 4, 900, hq, hkv, d, torch.bfloat16, layout=layout)
     bad = phys.clone()
     bad[2, 10], bad[2, 11], bad[3, 899] = 40 * 64, -2, 2 ** 31 - 1
     err = i32([0])

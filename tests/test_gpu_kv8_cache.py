@@ -27,6 +27,10 @@ def cache8(gen, blocks, hkv, d, layout="pages", filled=True):
         both = torch.zeros((blocks, 2, 64, hkv, d + 16), dtype=torch.uint8, device=DEV).view(F8)
         k, v = both[:, 0, :, :, 16:], both[:, 1, :, :, :d]
         sc = torch.zeros((blocks, 5, hkv + 1, 4), device=DEV)[:, :4, :hkv, :2]
+    elif layout == "loose":     # pages that are no whole number of slots apart
+        k, v = (torch.zeros((blocks, 64 * hkv * d + 48), dtype=torch.uint8, device=DEV).view(F8)[:, 16:16 + 64 * hkv * d]
+                .unflatten(1, (64, hkv, d)) for _ in range(2))
+        sc = torch.zeros((blocks, 4, hkv, 2), device=DEV)
     else:
         k, v, sc = dsa.new_kv_cache8(blocks, hkv, d)
     if filled:
