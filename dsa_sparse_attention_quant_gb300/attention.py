@@ -19,6 +19,7 @@ from .binding import DsaAttnC, DsaCacheDescC, DsaError, DsaKv8C, DsaKvC, DsaPage
 BLOCK_SIZE = 64
 SCALE_BLOCK = 16  # slots of a page that share a scale in an 8-bit cache
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_F8 = torch.float8_e4m3fn
 # torch.cuda.current_device() without its check that CUDA is up: asked only once a CUDA tensor is at hand
 _device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
@@ -40,7 +41,7 @@ def new_kv_cache8(num_blocks: int, num_kv_heads: int, head_dim: int, device=None
         raise DsaError("an 8-bit KV cache has rows of 64 or 128, at least one page and one head")
     dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
     n, heads = int(num_blocks), int(num_kv_heads)
-    codes = [torch.zeros((n, BLOCK_SIZE, heads, int(head_dim)), dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+    codes = [torch.zeros((n, BLOCK_SIZE, heads, int(head_dim)), dtype=torch.uint8, device=dev).view(_F8)
              for _ in range(2)]
     return (*codes, torch.zeros((n, BLOCK_SIZE // SCALE_BLOCK, heads, 2), dtype=torch.float32, device=dev))
 
@@ -107,28 +108,65 @@ def _kv(k, v, packed=False):
 
 
 def _kv8(k, v, scale, rows, what):
-    """(C description, heads, head_dim, dtype) of an 8-bit cache's codes
+    """(C description, device, heads, head_dim, dtype) of an 8-bit cache's codes
     [num_blocks, 64, heads, head_dim] and scales [num_blocks, 4, heads, 2], for
-    rows (``what``) in 16 bits; any strides with a contiguous last axis."""
-    _here(k, "k_cache", torch.float8_e4m3fn)
-    shape, dev = k.shape, k.get_device()
-    if not isinstance(v, torch.Tensor) or v.get_device() != dev or v.dtype is not k.dtype or v.shape != shape:
-        _here(v, "v_cache", torch.float8_e4m3fn)
+    rows (``what``) in 16 bits; any strides with a contiguous last axis. All that a
+    good call has to pass is asked for once; what is wrong is looked for after that."""
+    try:
+        dev, shape, dtype = k.get_device(), k.shape, rows.dtype
+        n, slots, heads, d = shape
+        code = _DTYPES.get(dtype)
+        ks, vs, ss = k.stride(), v.stride(), scale.stride()
+        good = (k.dtype is _F8 and v.dtype is _F8 and scale.dtype is torch.float32 and v.shape == shape
+                and slots == BLOCK_SIZE and scale.shape == (n, BLOCK_SIZE // SCALE_BLOCK, heads, 2) and code is not None
+                and ks[3] == vs[3] == ss[3] == 1 and dev >= 0
+                and v.get_device() == scale.get_device() == rows.get_device() == dev == _device())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _not_kv8(k, v, scale, rows, what)
+    return (_KV8.pack(k.data_ptr(), v.data_ptr(), scale.data_ptr(), code, heads, d, n, ks[0], ks[1], ks[2], vs[0], vs[1],
+                      vs[2], ss[0], ss[1], ss[2]), dev, heads, d, dtype)
+
+
+def _not_kv8(k, v, scale, rows, what):
+    _here(k, "k_cache", _F8)
+    _here(v, "v_cache", _F8)
+    if v.shape != k.shape:
         raise DsaError("k_cache and v_cache must have one shape")
-    if len(shape) != 4 or shape[1] != BLOCK_SIZE:
+    if k.dim() != 4 or k.shape[1] != BLOCK_SIZE:
         raise DsaError("k_cache and v_cache must be [num_blocks, 64, heads, head_dim]")
-    n, _, heads, d = shape
-    if _here(scale, "kv_scale", torch.float32).shape != (n, BLOCK_SIZE // SCALE_BLOCK, heads, 2):
+    if _here(scale, "kv_scale", torch.float32).shape != (k.shape[0], BLOCK_SIZE // SCALE_BLOCK, k.shape[2], 2):
         raise DsaError("kv_scale must be [num_blocks, 4, heads, 2]")
-    ks, vs, ss = k.stride(), v.stride(), scale.stride()
-    if ks[3] != 1 or vs[3] != 1 or ss[3] != 1:
-        raise DsaError("k_cache, v_cache and kv_scale must have a contiguous last axis")
-    dtype = _here(rows, what).dtype
-    code = _DTYPES.get(dtype)
-    if code is None:
-        raise DsaError(f"{what} must be bf16 or fp16, got {dtype}")
-    return (_KV8.pack(k.data_ptr(), v.data_ptr(), scale.data_ptr(), code, heads, d, n, *ks[:3], *vs[:3], *ss[:3]), heads,
-            d, dtype)
+    if _here(rows, what).dtype not in _DTYPES:
+        raise DsaError(f"{what} must be bf16 or fp16, got {rows.dtype}")
+    raise DsaError("k_cache, v_cache and kv_scale must have a contiguous last axis")
+
+
+def _rows8(t, what, want, dtype, dev):
+    """(address, row stride, head stride) of rows [n, heads, head_dim] in 16 bits."""
+    s = t.stride() if isinstance(t, torch.Tensor) and t.shape == want else None
+    if s is None or t.dtype is not dtype or t.get_device() != dev or s[2] != 1:
+        if _here(t, what, dtype).shape != want:
+            raise DsaError(f"{what} must be {list(want)}")
+        raise DsaError(f"{what} must have a contiguous last axis")
+    return t.data_ptr(), s[0], s[1]
+
+
+def _attn8(q, out, lse, kv_heads, d, dtype, dev, scale, rows, every, stream):
+    """_attn() for a q whose device and type _kv8() has seen."""
+    shape = q.shape
+    if len(shape) == 3 and shape[2] == d and shape[0] >= rows and kv_heads > 0 and shape[1] > 0 \
+            and shape[1] % kv_heads == 0 and isinstance(out, torch.Tensor) and out.shape == shape \
+            and out.dtype is dtype and out.get_device() == dev and isinstance(lse, torch.Tensor) \
+            and lse.shape == shape[:2] and lse.dtype is torch.float32 and lse.get_device() == dev \
+            and lse.is_contiguous():
+        qs, os = q.stride(), out.stride()
+        if qs[2] == 1 and os[2] == 1:
+            heads = shape[1]
+            return (_ATTN.pack(q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1], lse.data_ptr(), heads, scale),
+                    out, lse, heads)
+    return _attn(q, out, lse, kv_heads, d, dtype, scale, rows, every, stream)   # makes what is missing, or refuses
 
 
 def _made(stream, shape, dtype, device, rest):
@@ -286,19 +324,16 @@ def kv_write8(k, v, slot_mapping, k_cache, v_cache, kv_scale, ws=None, dev_err=N
     8-bit cache (``new_kv_cache8``) at their slots (int64, -1 = padding). A block's
     scale is made anew when its first slot is written and may rise after that, which
     rounds the rows that are there to the raised one."""
-    kv, heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, k, "k rows")
+    kv, dev, heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, k, "k rows")
     n = _dense(slot_mapping, "slot_mapping", torch.int64).numel()
     want = (n, heads, d)
-    for t, what in ((k, "k rows"), (v, "v rows")):
-        if _here(t, what, dtype).shape != want:
-            raise DsaError(f"{what} must be [{n}, {heads}, {d}]")
-        if t.stride(2) != 1:
-            raise DsaError(f"{what} must have a contiguous last axis")
+    kp, kr, kh = _rows8(k, "k rows", want, dtype, dev)
+    vp, vr, vh = _rows8(v, "v rows", want, dtype, dev)
     if n == 0:
         return
     ws = _scratch(ws, lambda: kv_write8_workspace_size(n, k_cache.shape[0]), k.device, stream)
-    st = load().dsa_kv_write8(k.data_ptr(), *k.stride()[:2], v.data_ptr(), *v.stride()[:2], n, slot_mapping.data_ptr(),
-                              kv, ws.data_ptr(), ws.numel(), _err(dev_err), _on(stream))
+    st = load().dsa_kv_write8(kp, kr, kh, vp, vr, vh, n, slot_mapping.data_ptr(), kv, ws.data_ptr(), ws.numel(),
+                              _err(dev_err), _on(stream))
     _check(st, "dsa_kv_write8")
 
 
@@ -308,15 +343,16 @@ def kv_read8(batch, k_cache, v_cache, kv_scale, kv_start, k, v, past: bool = Fal
     heads, head_dim] (bf16 or fp16), as ``attn_prompt`` takes packed keys; with
     ``past`` without the request's own query tokens. Other rows stay as they were.
     Returns (k, v)."""
-    kv, heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, k, "k rows")
-    rows, rheads, rd, _ = _kv(k, v, packed=True)
-    if (rheads, rd) != (heads, d):
-        raise DsaError(f"k and v rows must be [rows, {heads}, {d}]")
+    kv, dev, heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, k, "k rows")
+    n = k.shape[0] if k.dim() else 0
+    kp, kr, kh = _rows8(k, "k rows", (n, heads, d), dtype, dev)
+    vp, vr, vh = _rows8(v, "v rows", (n, heads, d), dtype, dev)
     _here(batch.seq_lens, "the batch")
     if _dense(kv_start, "kv_start", torch.int32).numel() < batch.num_reqs:
         raise DsaError("kv_start needs an entry per request")
-    if k.shape[0] == 0:
+    if n == 0:
         return k, v
+    rows = _KV.pack(kp, vp, _DTYPES[dtype], heads, d, n, d, kr, kh, d, vr, vh)
     st = load().dsa_kv_read8(ctypes.byref(batch.c), kv, kv_start.data_ptr(), rows, 1 if past else 0, _err(dev_err),
                              _on(stream))
     _check(st, "dsa_kv_read8")
@@ -331,10 +367,10 @@ def attn_decode8_workspace_size(batch, num_heads: int, num_kv_heads: int, head_d
 def attn_decode8(batch, q, k_cache, v_cache, kv_scale, scale: float = 0.0, out=None, lse=None, ws=None, dev_err=None,
                  stream=None):
     """``attn_decode`` over an 8-bit cache (``new_kv_cache8``); q is bf16 or fp16."""
-    kv, kv_heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, q, "q")
+    kv, dev, kv_heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, q, "q")
     _here(batch.seq_lens, "the batch")
     n = batch.num_decode_tokens
-    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, dtype, scale, n, n == q.shape[0], stream)
+    at, out, lse, heads = _attn8(q, out, lse, kv_heads, d, dtype, dev, scale, n, n == q.shape[0], stream)
     ws = _scratch(ws, lambda: attn_decode8_workspace_size(batch, heads, kv_heads, d), q.device, stream)
     st = load().dsa_attn_decode8(ctypes.byref(batch.c), kv, at, ws.data_ptr(), ws.numel(), _err(dev_err), _on(stream))
     _check(st, "dsa_attn_decode8")
@@ -349,12 +385,12 @@ def attn_selected8_workspace_size(n_tokens: int, topk: int, num_heads: int, num_
 def attn_selected8(q, k_cache, v_cache, kv_scale, physical, scale: float = 0.0, out=None, lse=None, ws=None,
                    dev_err=None, stream=None):
     """``attn_selected`` over an 8-bit cache (``new_kv_cache8``); q is bf16 or fp16."""
-    kv, kv_heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, q, "q")
+    kv, dev, kv_heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, q, "q")
     shape = _dense(physical, "physical", torch.int32).shape
     if len(shape) != 2 or shape[1] < 1:
         raise DsaError("physical must be [tokens, topk]")
     n, topk = shape
-    at, out, lse, heads = _attn(q, out, lse, kv_heads, d, dtype, scale, n, True, stream)
+    at, out, lse, heads = _attn8(q, out, lse, kv_heads, d, dtype, dev, scale, n, True, stream)
     if q.shape[0] != n:
         raise DsaError(f"q has {q.shape[0]} rows, physical {n}")
     ws = _scratch(ws, lambda: attn_selected8_workspace_size(n, topk, heads, kv_heads, d), q.device, stream)

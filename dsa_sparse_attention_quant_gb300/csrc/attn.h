@@ -80,8 +80,8 @@ struct Write8Args {
   int32_t* token_of;  // [slots]: the last token with that slot, or anything; nullptr: few tokens
   int32_t* err;
 };
-constexpr int kWrite8Few = 512;  // up to this many tokens: one launch, without token_of
-cudaError_t launch_kv_write8(const Write8Args& a, int head_dim, int dtype, cudaStream_t stream);
+constexpr int kWrite8Few = 1024;  // up to this many tokens: one launch, without token_of
+cudaError_t launch_kv_write8(const Write8Args& a, int head_dim, int dtype, int num_sms, cudaStream_t stream);
 
 struct Read8Args {
   Cache8Args c;

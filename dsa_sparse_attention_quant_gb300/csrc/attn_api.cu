@@ -594,7 +594,7 @@ int dsa_kv_write8(const void* k, int64_t k_row_stride, int64_t k_head_stride, co
   const Write8Args a{cache8_args(c), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                      k_row_stride, k_head_stride, v_row_stride, v_head_stride,
                      n_tokens, slot_mapping, need > 0 ? static_cast<int32_t*>(ws) : nullptr, dev_err};
-  return from_cuda(launch_kv_write8(a, c.head_dim, c.dtype, stream));
+  return from_cuda(launch_kv_write8(a, c.head_dim, c.dtype, sms, stream));
 }
 
 int dsa_kv_read8(const DsaBatch* batch, const DsaKv8* kv, const int32_t* kv_start, const DsaKv* rows, int32_t past,

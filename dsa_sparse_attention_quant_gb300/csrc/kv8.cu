@@ -60,6 +60,15 @@ __device__ __forceinline__ void values(uint32_t codes, float2* lo, float2* hi) {
   *lo = __half22float2(*reinterpret_cast<const __half2*>(&a));
   *hi = __half22float2(*reinterpret_cast<const __half2*>(&b));
 }
+// Eight codes' values in the type.
+template <typename T>
+__device__ __forceinline__ uint4 row_of(uint2 codes, float s, T type) {
+  float2 f[4];
+  values(codes.x, &f[0], &f[1]);
+  values(codes.y, &f[2], &f[3]);
+  return make_uint4(narrow(f[0].x * s, f[0].y * s, type), narrow(f[1].x * s, f[1].y * s, type),
+                    narrow(f[2].x * s, f[2].y * s, type), narrow(f[3].x * s, f[3].y * s, type));
+}
 __device__ __forceinline__ uint32_t rescaled(uint32_t codes, float f) {
   float2 lo, hi;
   values(codes, &lo, &hi);
@@ -68,7 +77,7 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t codes, float f) {
 
 // ---------------------------------------------------------------------- write
 // Who writes a block: the call's tokens of a block are found by its slots, whatever
-// their places in the list. With few tokens a warp looks the list through; with many
+// their places in the list. With few tokens each CTA looks the list through; with many
 // a first kernel leaves each slot's last token in token_of, which needs no clearing:
 // an entry counts only if it names a token whose slot this is. Either way the token
 // at the block's lowest written slot takes the whole block.
@@ -168,72 +177,101 @@ __device__ __forceinline__ void write_block(const Write8Args& a, int64_t block, 
   if (lane == 0) *scale = s;
 }
 
-// A CTA takes PER tokens of the list: a warp each finds its token's block, then all
-// warps share the blocks' heads.
-template <int D, typename T, int PER>
-__global__ void __launch_bounds__(kThreads) write8_kernel(const __grid_constant__ Write8Args a) {
-  __shared__ int32_t src[PER][kScaleBlock];
-  __shared__ int64_t block[PER];
-  __shared__ int lead[PER];
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t slots = a.c.num_blocks * kBlock;
-  for (int i = warp; i < PER; i += kWarps) {
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * PER + i;
-    const int64_t slot = t < a.n_tokens ? a.slot_mapping[t] : -1;
-    const bool ok = slot >= 0 && slot < slots;
-    if (slot != -1 && !ok && lane == 0) flag_error(a.err, DSA_DEVERR_SLOT_RANGE);
-    const int64_t b = slot / kScaleBlock;
-    int32_t mine = -1;  // lane r < 16: the token of the block's slot r
-    if (ok) {
-      if (a.token_of != nullptr) {
-        if (lane < kScaleBlock) {
-          const int32_t v = a.token_of[b * kScaleBlock + lane];
-          if (v >= 0 && v < a.n_tokens && a.slot_mapping[v] == b * kScaleBlock + lane) mine = v;
-        }
-      } else {
-        if (lane < kScaleBlock) src[i][lane] = -1;
-        __syncwarp();
-        for (int j = lane; j < a.n_tokens; j += 32) {
-          const int64_t other = a.slot_mapping[j];
-          if (other >= 0 && other / kScaleBlock == b) atomicMax(&src[i][other % kScaleBlock], j);
-        }
-        __syncwarp();
-        if (lane < kScaleBlock) mine = src[i][lane];
-      }
-    }
-    const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0);
-    const int32_t first = there ? __shfl_sync(0xffffffffu, mine, __ffs(there) - 1) : -1;
-    if (lane < kScaleBlock) src[i][lane] = mine;
-    if (lane == 0) {
-      block[i] = b;
-      lead[i] = ok && first == t;
-    }
-  }
-  __syncthreads();
-  const int each = 2 * a.c.hkv;
-  int at = warp;  // this warp's unit, counted over the blocks taken here
+// The blocks of a CTA's tokens: src[i][r] = the token of slot r of block[i], or -1;
+// list[0, n) = those that are taken here.
+template <int PER>
+struct Blocks {
+  int32_t src[PER][kScaleBlock];
+  int64_t block[PER];
+  int list[PER], n;
+  bool lead[PER];
+};
+
+// All warps share the blocks' heads, those of the grid's other CTAs with these tokens too.
+template <int D, typename T, bool SHARED, int PER>
+__device__ __forceinline__ void write_blocks(const Write8Args& a, const Blocks<PER>& s) {
+  const int each = 2 * a.c.hkv, units = s.n * each;
 #pragma unroll 1
-  for (int i = 0; i < PER; ++i) {
-    if (!lead[i]) continue;
-    for (; at < each; at += kWarps) write_block<D, T>(a, block[i], src[i], at >> 1, at & 1);
-    at -= each;
+  for (int u = (SHARED ? blockIdx.y * kWarps : 0) + (threadIdx.x >> 5); u < units;
+       u += SHARED ? gridDim.y * kWarps : kWarps) {
+    const int i = PER == 1 ? 0 : s.list[u / each], hv = PER == 1 ? u : u % each;
+    write_block<D, T>(a, s.block[i], s.src[i], hv >> 1, hv & 1);
   }
 }
 
+// Few tokens: a CTA each, whose threads look the list through.
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) write8_few_kernel(const __grid_constant__ Write8Args a) {
+  __shared__ Blocks<1> s;
+  pdl_wait();
+  const int64_t slot = a.slot_mapping[blockIdx.x], slots = a.c.num_blocks * kBlock, b = slot / kScaleBlock;
+  if (slot < 0 || slot >= slots) {
+    if (slot != -1 && threadIdx.x == 0) flag_error(a.err, DSA_DEVERR_SLOT_RANGE);
+    return;
+  }
+  if (threadIdx.x < kScaleBlock) s.src[0][threadIdx.x] = -1;
+  if (threadIdx.x == 0) {
+    s.block[0] = b;
+    s.n = 1;
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < a.n_tokens; j += kThreads) {
+    const int64_t other = a.slot_mapping[j];
+    if (other >= 0 && other / kScaleBlock == b) atomicMax(&s.src[0][other % kScaleBlock], j);
+  }
+  __syncthreads();
+  int first = 0;
+  while (s.src[0][first] < 0) ++first;  // this token's slot is there
+  if (s.src[0][first] != static_cast<int32_t>(blockIdx.x)) return;
+  write_blocks<D, T, false>(a, s);
+}
+
+// Many: a CTA per 16 tokens of the list, 16 threads a token, a thread a slot of its block.
+constexpr int kPer = kThreads / kScaleBlock;
+template <int D, typename T, bool SHARED>
+__global__ void __launch_bounds__(kThreads, 4) write8_many_kernel(const __grid_constant__ Write8Args a) {
+  __shared__ Blocks<kPer> s;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, i = threadIdx.x / kScaleBlock, r = threadIdx.x % kScaleBlock;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kPer + i, slots = a.c.num_blocks * kBlock;
+  const int64_t slot = t < a.n_tokens ? a.slot_mapping[t] : -1, first = slot / kScaleBlock * kScaleBlock;
+  const bool ok = slot >= 0 && slot < slots;
+  if (slot != -1 && !ok && r == 0 && blockIdx.y == 0) flag_error(a.err, DSA_DEVERR_SLOT_RANGE);
+  int32_t mine = -1;
+  if (ok) {
+    const int32_t v = a.token_of[first + r];
+    if (v >= 0 && v < a.n_tokens && a.slot_mapping[v] == first + r) mine = v;
+  }
+  const uint32_t there = (__ballot_sync(0xffffffffu, mine >= 0) >> (lane & 16)) & 0xffffu;
+  const int32_t lowest = __shfl_sync(0xffffffffu, mine, (lane & 16) + (there ? __ffs(there) - 1 : 0));
+  s.src[i][r] = mine;
+  if (r == 0) {
+    s.block[i] = slot / kScaleBlock;
+    s.lead[i] = there && lowest == t;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {  // in order, alike in the CTAs that share them
+    const bool lead = lane < kPer && s.lead[lane];
+    const uint32_t m = __ballot_sync(0xffffffffu, lead);
+    if (lead) s.list[__popc(m & ((1u << lane) - 1u))] = lane;
+    if (lane == 0) s.n = __popc(m);
+  }
+  __syncthreads();
+  write_blocks<D, T, SHARED>(a, s);
+}
+
 // ----------------------------------------------------------------------- read
-// A warp per (block of a request, head, K or V), in order; lengths are counted in
+// A warp per (block of a request, head), K and V, in order; lengths are counted in
 // rounds of kThreads requests.
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__ Read8Args a) {
-  constexpr int CH = D / 8;             // 8-byte chunks of a row of codes: 16 bytes of a row read
+  constexpr int CH = D / 8;  // 8-byte chunks of a row of codes: 16 bytes of a row read
   constexpr int RPI = 32 / CH;
   constexpr int N = kScaleBlock / RPI;
   __shared__ int scan[33];
   __shared__ int ends[kThreads], keys[kThreads];
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ch = lane % CH, r0 = lane / CH;
-  const int each = 2 * a.c.hkv;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
   int64_t at = static_cast<int64_t>(blockIdx.x) * kWarps + warp;  // this warp's unit, from the round's first one
   for (int q0 = 0; q0 < a.num_reqs; q0 += kThreads) {
@@ -256,10 +294,10 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__
     ends[tid] = incl;
     keys[tid] = n;
     __syncthreads();
-    const int64_t units = static_cast<int64_t>(tot) * each;
+    const int64_t units = static_cast<int64_t>(tot) * a.c.hkv;
     int i = 0;
     for (; at < units; at += warps) {
-      const int b = static_cast<int>(at / each), hv = static_cast<int>(at - static_cast<int64_t>(b) * each);
+      const int b = static_cast<int>(at / a.c.hkv), h = static_cast<int>(at - static_cast<int64_t>(b) * a.c.hkv);
       while (ends[i] <= b) ++i;
       const int first = (b - (i > 0 ? ends[i - 1] : 0)) * kScaleBlock, have = min(kScaleBlock, keys[i] - first);
       const int64_t page = a.block_table[static_cast<int64_t>(q0 + i) * a.bt_stride + first / kBlock];
@@ -267,27 +305,26 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__
         if (lane == 0) flag_error(a.err, DSA_DEVERR_BLOCK_RANGE);
         continue;
       }
-      const int h = hv >> 1, part = first % kBlock / kScaleBlock;
-      const bool isv = hv & 1;
-      const int64_t slot = isv ? a.c.v_slot : a.c.k_slot, row = isv ? a.v_row : a.k_row;
-      const uint8_t* codes = (isv ? a.c.v + page * a.c.v_page + h * a.c.v_head : a.c.k + page * a.c.k_page + h * a.c.k_head) +
-                             (part * kScaleBlock + r0) * slot + ch * 8;
-      uint16_t* out = (isv ? a.v + h * a.v_rhead : a.k + h * a.k_rhead) +
-                      (static_cast<int64_t>(a.kv_start[q0 + i]) + first + r0) * row + ch * 8;
-      uint2 x[N];
+      const int part = first % kBlock / kScaleBlock;
+      const uint8_t* kp = a.c.k + page * a.c.k_page + h * a.c.k_head + (part * kScaleBlock + r0) * a.c.k_slot + ch * 8;
+      const uint8_t* vp = a.c.v + page * a.c.v_page + h * a.c.v_head + (part * kScaleBlock + r0) * a.c.v_slot + ch * 8;
+      uint2 x[N], y[N];
 #pragma unroll
-      for (int u = 0; u < N; ++u)
-        if (u * RPI + r0 < have) x[u] = *reinterpret_cast<const uint2*>(codes + u * RPI * slot);
-      const float s = a.c.scale[page * a.c.s_page + part * a.c.s_block + h * a.c.s_head + (isv ? 1 : 0)];
+      for (int u = 0; u < N; ++u) {
+        if (u * RPI + r0 < have) {
+          x[u] = *reinterpret_cast<const uint2*>(kp + u * RPI * a.c.k_slot);
+          y[u] = *reinterpret_cast<const uint2*>(vp + u * RPI * a.c.v_slot);
+        }
+      }
+      const float2 s = *reinterpret_cast<const float2*>(a.c.scale + page * a.c.s_page + part * a.c.s_block + h * a.c.s_head);
+      const int64_t row = static_cast<int64_t>(a.kv_start[q0 + i]) + first + r0;
+      uint16_t* ko = a.k + h * a.k_rhead + row * a.k_row + ch * 8;
+      uint16_t* vo = a.v + h * a.v_rhead + row * a.v_row + ch * 8;
 #pragma unroll
       for (int u = 0; u < N; ++u) {
         if (u * RPI + r0 >= have) continue;
-        float2 f[4];
-        values(x[u].x, &f[0], &f[1]);
-        values(x[u].y, &f[2], &f[3]);
-        *reinterpret_cast<uint4*>(out + u * RPI * row) =
-            make_uint4(narrow(f[0].x * s, f[0].y * s, T()), narrow(f[1].x * s, f[1].y * s, T()),
-                       narrow(f[2].x * s, f[2].y * s, T()), narrow(f[3].x * s, f[3].y * s, T()));
+        *reinterpret_cast<uint4*>(ko + u * RPI * a.k_row) = row_of(x[u], s.x, T());
+        *reinterpret_cast<uint4*>(vo + u * RPI * a.v_row) = row_of(y[u], s.y, T());
       }
     }
     at -= units;
@@ -296,30 +333,35 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__
 }
 
 template <int D, typename T>
-cudaError_t write8(const Write8Args& a, cudaStream_t stream) {
+cudaError_t write8(const Write8Args& a, int num_sms, cudaStream_t stream) {
   if (a.token_of == nullptr)
-    return launch_pdl(write8_kernel<D, T, 1>, dim3(static_cast<unsigned>(a.n_tokens)), dim3(kThreads), 0, stream, a);
+    return launch_pdl(write8_few_kernel<D, T>, dim3(static_cast<unsigned>(a.n_tokens)), dim3(kThreads), 0, stream, a);
   cudaError_t e = launch_pdl(write8_claim_kernel, dim3(static_cast<unsigned>((a.n_tokens + kThreads - 1) / kThreads)),
                              dim3(kThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
-  constexpr int PER = 16;
-  return launch_pdl(write8_kernel<D, T, PER>, dim3(static_cast<unsigned>((a.n_tokens + PER - 1) / PER)),
-                    dim3(kThreads), 0, stream, a);
+  // tokens may lie in one block or each in its own: few CTAs' blocks are shared by more
+  const int64_t chunks = (a.n_tokens + kPer - 1) / kPer, want = static_cast<int64_t>(num_sms) * 8 / chunks;
+  const int64_t most = (static_cast<int64_t>(kPer) * 2 * a.c.hkv + kWarps - 1) / kWarps;
+  const int64_t across = want < 1 ? 1 : want < most ? want : most;
+  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(across)), block(kThreads);
+  // (the shared form's loop takes 40.5 us, so 35.3, for the 30572 rows)
+  return across > 1 ? launch_pdl(write8_many_kernel<D, T, true>, grid, block, 0, stream, a)
+                    : launch_pdl(write8_many_kernel<D, T, false>, grid, block, 0, stream, a);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_write8(const Write8Args& a, int head_dim, int dtype, cudaStream_t stream) {
+cudaError_t launch_kv_write8(const Write8Args& a, int head_dim, int dtype, int num_sms, cudaStream_t stream) {
   if (dtype == DSA_BF16)
-    return head_dim == 128 ? write8<128, __nv_bfloat16>(a, stream) : write8<64, __nv_bfloat16>(a, stream);
-  return head_dim == 128 ? write8<128, __half>(a, stream) : write8<64, __half>(a, stream);
+    return head_dim == 128 ? write8<128, __nv_bfloat16>(a, num_sms, stream) : write8<64, __nv_bfloat16>(a, num_sms, stream);
+  return head_dim == 128 ? write8<128, __half>(a, num_sms, stream) : write8<64, __half>(a, num_sms, stream);
 }
 
 cudaError_t launch_kv_read8(const Read8Args& a, int head_dim, int dtype, int num_sms, cudaStream_t stream) {
   // at most so many blocks are read, whatever the lengths
   const int64_t blocks = static_cast<int64_t>(a.num_reqs) * ((a.max_keys + kScaleBlock - 1) / kScaleBlock);
-  int64_t grid = (blocks * 2 * a.c.hkv + kWarps - 1) / kWarps;
-  const int64_t cap = static_cast<int64_t>(num_sms) * 8;
+  int64_t grid = (blocks * a.c.hkv + kWarps - 1) / kWarps;
+  const int64_t cap = static_cast<int64_t>(num_sms) * 16;
   if (grid > cap) grid = cap;
   if (grid < 1) grid = 1;
   const dim3 g(static_cast<unsigned>(grid)), b(kThreads);

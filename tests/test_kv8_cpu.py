@@ -156,13 +156,16 @@ def test_nothing_is_read_as_read_only(name):
         assert word not in text, word
 
 
+KERNELS = {"attn_rows8_kernel", "write8_claim_kernel", "write8_few_kernel", "write8_many_kernel", "read8_kernel"}
+
+
 def test_kernels_wait_whatever_they_have_to_do():
     # at the kernel's outermost level, before any return
     seen = set()
     for name, body in bodies():
-        if name not in ("attn_rows8_kernel", "write8_claim_kernel", "write8_kernel", "read8_kernel"):
+        if name not in KERNELS:
             continue
         seen.add(name)
         head = body[:body.index("pdl_wait();")]
         assert head.count("{") == head.count("}") and "return" not in head, name
-    assert len(seen) == 4
+    assert seen == KERNELS
