@@ -14,6 +14,7 @@ import struct
 
 import torch
 
+from . import binding
 from .binding import DsaAttnC, DsaCacheDescC, DsaError, DsaKv8C, DsaKvC, DsaPagesC, _check, load
 
 BLOCK_SIZE = 64
@@ -151,6 +152,14 @@ def _rows8(t, what, want, dtype, dev):
             raise DsaError(f"{what} must be {list(want)}")
         raise DsaError(f"{what} must have a contiguous last axis")
     return t.data_ptr(), s[0], s[1]
+
+
+def _list8(t, what, dtype, dev):
+    """Elements of a contiguous tensor on the call's device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _dense(t, what, dtype)
+        raise DsaError(f"{what} must be on cuda:{dev}")
+    return t.numel()
 
 
 def _attn8(q, out, lse, kv_heads, d, dtype, dev, scale, rows, every, stream):
@@ -325,16 +334,19 @@ def kv_write8(k, v, slot_mapping, k_cache, v_cache, kv_scale, ws=None, dev_err=N
     scale is made anew when its first slot is written and may rise after that, which
     rounds the rows that are there to the raised one."""
     kv, dev, heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, k, "k rows")
-    n = _dense(slot_mapping, "slot_mapping", torch.int64).numel()
+    n = _list8(slot_mapping, "slot_mapping", torch.int64, dev)
     want = (n, heads, d)
     kp, kr, kh = _rows8(k, "k rows", want, dtype, dev)
     vp, vr, vh = _rows8(v, "v rows", want, dtype, dev)
     if n == 0:
         return
-    ws = _scratch(ws, lambda: kv_write8_workspace_size(n, k_cache.shape[0]), k.device, stream)
-    st = load().dsa_kv_write8(kp, kr, kh, vp, vr, vh, n, slot_mapping.data_ptr(), kv, ws.data_ptr(), ws.numel(),
-                              _err(dev_err), _on(stream))
-    _check(st, "dsa_kv_write8")
+    if ws is None:
+        ws = _scratch(None, lambda: kv_write8_workspace_size(n, k_cache.shape[0]), k.device, stream)
+    room = _list8(ws, "ws", torch.uint8, dev)
+    st = (binding._lib or load()).dsa_kv_write8(kp, kr, kh, vp, vr, vh, n, slot_mapping.data_ptr(), kv, ws.data_ptr(),
+                                                room, None if dev_err is None else _err(dev_err), _on(stream))
+    if st:
+        _check(st, "dsa_kv_write8")
 
 
 def kv_read8(batch, k_cache, v_cache, kv_scale, kv_start, k, v, past: bool = False, dev_err=None, stream=None):
@@ -347,15 +359,17 @@ def kv_read8(batch, k_cache, v_cache, kv_scale, kv_start, k, v, past: bool = Fal
     n = k.shape[0] if k.dim() else 0
     kp, kr, kh = _rows8(k, "k rows", (n, heads, d), dtype, dev)
     vp, vr, vh = _rows8(v, "v rows", (n, heads, d), dtype, dev)
-    _here(batch.seq_lens, "the batch")
-    if _dense(kv_start, "kv_start", torch.int32).numel() < batch.num_reqs:
+    if batch.seq_lens.get_device() != dev:
+        _here(batch.seq_lens, "the batch")
+    if _list8(kv_start, "kv_start", torch.int32, dev) < batch.num_reqs:
         raise DsaError("kv_start needs an entry per request")
     if n == 0:
         return k, v
     rows = _KV.pack(kp, vp, _DTYPES[dtype], heads, d, n, d, kr, kh, d, vr, vh)
-    st = load().dsa_kv_read8(ctypes.byref(batch.c), kv, kv_start.data_ptr(), rows, 1 if past else 0, _err(dev_err),
-                             _on(stream))
-    _check(st, "dsa_kv_read8")
+    st = (binding._lib or load()).dsa_kv_read8(ctypes.byref(batch.c), kv, kv_start.data_ptr(), rows, 1 if past else 0,
+                                               None if dev_err is None else _err(dev_err), _on(stream))
+    if st:
+        _check(st, "dsa_kv_read8")
     return k, v
 
 
@@ -368,12 +382,17 @@ def attn_decode8(batch, q, k_cache, v_cache, kv_scale, scale: float = 0.0, out=N
                  stream=None):
     """``attn_decode`` over an 8-bit cache (``new_kv_cache8``); q is bf16 or fp16."""
     kv, dev, kv_heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, q, "q")
-    _here(batch.seq_lens, "the batch")
+    if batch.seq_lens.get_device() != dev:
+        _here(batch.seq_lens, "the batch")
     n = batch.num_decode_tokens
     at, out, lse, heads = _attn8(q, out, lse, kv_heads, d, dtype, dev, scale, n, n == q.shape[0], stream)
-    ws = _scratch(ws, lambda: attn_decode8_workspace_size(batch, heads, kv_heads, d), q.device, stream)
-    st = load().dsa_attn_decode8(ctypes.byref(batch.c), kv, at, ws.data_ptr(), ws.numel(), _err(dev_err), _on(stream))
-    _check(st, "dsa_attn_decode8")
+    if ws is None:
+        ws = _scratch(None, lambda: attn_decode8_workspace_size(batch, heads, kv_heads, d), q.device, stream)
+    room = _list8(ws, "ws", torch.uint8, dev)
+    st = (binding._lib or load()).dsa_attn_decode8(ctypes.byref(batch.c), kv, at, ws.data_ptr(), room,
+                                                   None if dev_err is None else _err(dev_err), _on(stream))
+    if st:
+        _check(st, "dsa_attn_decode8")
     return out, lse
 
 
@@ -386,17 +405,21 @@ def attn_selected8(q, k_cache, v_cache, kv_scale, physical, scale: float = 0.0, 
                    dev_err=None, stream=None):
     """``attn_selected`` over an 8-bit cache (``new_kv_cache8``); q is bf16 or fp16."""
     kv, dev, kv_heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, q, "q")
-    shape = _dense(physical, "physical", torch.int32).shape
+    _list8(physical, "physical", torch.int32, dev)
+    shape = physical.shape
     if len(shape) != 2 or shape[1] < 1:
         raise DsaError("physical must be [tokens, topk]")
     n, topk = shape
     at, out, lse, heads = _attn8(q, out, lse, kv_heads, d, dtype, dev, scale, n, True, stream)
     if q.shape[0] != n:
         raise DsaError(f"q has {q.shape[0]} rows, physical {n}")
-    ws = _scratch(ws, lambda: attn_selected8_workspace_size(n, topk, heads, kv_heads, d), q.device, stream)
-    st = load().dsa_attn_selected8(kv, at, physical.data_ptr(), n, topk, ws.data_ptr(), ws.numel(), _err(dev_err),
-                                   _on(stream))
-    _check(st, "dsa_attn_selected8")
+    if ws is None:
+        ws = _scratch(None, lambda: attn_selected8_workspace_size(n, topk, heads, kv_heads, d), q.device, stream)
+    room = _list8(ws, "ws", torch.uint8, dev)
+    st = (binding._lib or load()).dsa_attn_selected8(kv, at, physical.data_ptr(), n, topk, ws.data_ptr(), room,
+                                                     None if dev_err is None else _err(dev_err), _on(stream))
+    if st:
+        _check(st, "dsa_attn_selected8")
     return out, lse
 
 

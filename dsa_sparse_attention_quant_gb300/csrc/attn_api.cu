@@ -141,7 +141,7 @@ RowsPlan rows_plan(int64_t tokens, int64_t keys, int heads, int hkv, int head_di
   const int group = heads / hkv;
   // the kernels' tiles of query heads, and their CTAs per SM (RowsCfg, Rows8Cfg)
   p.rows = cache == kIn8 ? 8 : 16;
-  while (p.rows < 32 && p.rows < group) p.rows *= 2;
+  if (p.rows < group) p.rows *= 2;
   const int row = cache == kIn8 && joint > 1 ? 128 : head_dim;
   const int per_sm = cache == kIn8 && p.rows * row <= 8 * 128 ? 3 : 2;
   p.passes = (group + p.rows - 1) / p.rows;

@@ -26,7 +26,9 @@
 // their 16 rows and the query heads as their 8 columns (S^T = K q^T, O^T = V^T P^T):
 // G <= 8 query heads fill the tile that a 16-row tile of heads would half fill, and
 // K's and V's fragments, which have to be made from codes, are A operands that
-// several tiles of heads share. A lane's four codes of a K row are four columns
+// two tiles of heads share (G > 8). More than 16 query heads take a pass over the keys
+// per 16 of them: with tiles for 32 the registers do not suffice (8 requests of 32K
+// keys, 64/1 heads of 128: 61 us, so 74; 40/2 of 64: 52, so 98). A lane's four codes of a K row are four columns
 // d..d+3: two of them are taken as the MMA's k slots 2c, 2c+1 and two as 2c+8, 2c+9,
 // and q's columns are loaded in that order. V comes through the transposing ldmatrix
 // as pairs of codes (2d, 2d+1): even columns become the tile's rows 0-7, odd ones
@@ -61,7 +63,7 @@ struct Rows8Cfg {
   static constexpr int kStageBytes = 2 * kTile * kRowBytes;    // a tile's K codes, then its V codes
   // D = 128: 8 requests of 128K keys, 64/8 heads: 321 us, with four stages 349
   static constexpr int kStages = LOAD == kSlots ? (kRowBytes == 64 ? 5 : kCtas == 3 ? 3 : 4)
-                                                : (kRowBytes == 128 ? 1 : 2) * (kCtas == 3 ? 3 : NT == 4 ? 5 : 6);
+                                                : (kRowBytes == 128 ? 1 : 2) * (kCtas == 3 ? 3 : 6);
   // what a tile's consumers have to know besides, made by the loader: as far ahead as
   // the codes are, or with slots further, since their addresses come this way
   static constexpr int kInfos = LOAD == kSlots ? 8 : kStages;
@@ -71,8 +73,7 @@ struct Rows8Cfg {
   static constexpr int kOffScale = kOffBar + kInfos * 16;                 // float2 [kInfos][kScales]
   static constexpr int kOffAt = kOffScale + kInfos * kScales * 8;         // slots: longlong2 [kInfos][kTile]
   static constexpr int kOffMl = kOffAt + (LOAD == kSlots ? kInfos * kTile * 16 : 0);  // float2 [kWarps][HP][kRows]
-  static constexpr int kOffQ = kOffMl + kWarps * HP * kRows * 8;          // NT = 4: q's fragments
-  static constexpr int kOffScan = kOffQ + (NT == 4 ? HP * kRows * D * 2 : 0);  // the slice, scan scratch, abort flag
+  static constexpr int kOffScan = kOffMl + kWarps * HP * kRows * 8;       // the slice, scan scratch, abort flag
   static constexpr int kSmemBytes = kOffScan + 49 * 4;
   static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
   static_assert(kWarps * HP * 8 * D * 4 == kStageBytes, "O of four warps' eight heads fits a stage");
@@ -397,11 +398,10 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
   const int head0 = pass * C::kRows;                // first query head of the group in this pass
   const int rows = min(C::kRows, a.group - head0);  // its query heads
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
-  uint2* qs = reinterpret_cast<uint2*>(smem + C::kOffQ);
   int desc_token = -1, desc_last = 0;  // the slice ends inside a token that it began: which, and its last slice
   float o[HP][NT][CH][4];
-  float m[HP][NT][2], l[HP][NT][2], rf[HP][NT][2];
-  uint2 qf[HP][NT == 4 ? 1 : NT][CH];
+  float m[HP][NT][2], l[HP][NT][2], lr[HP][NT][2], rf[HP][NT][2];  // lr: fp16: the sum of the rounded weights
+  uint2 qf[HP][NT][CH];
   bool starts = true;
   const float NEG = -INFINITY;
   // where ldmatrix's rows lie in a stage; chunk k of them is at the address with k << 4 flipped
@@ -469,10 +469,10 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
           m[z][x][0] = m[z][x][1] = NEG;
-          l[z][x][0] = l[z][x][1] = 0.0f;
+          l[z][x][0] = l[z][x][1] = lr[z][x][0] = lr[z][x][1] = 0.0f;
 #pragma unroll
           for (int y = 0; y < CH; ++y) o[z][x][y][0] = o[z][x][y][1] = o[z][x][y][2] = o[z][x][y][3] = 0.0f;
-          uint2 q4[CH];
+          uint2(&q4)[CH] = qf[z][x];
           const bool in = x * 8 + g < rows;
           const uint16_t* qp = q + (in ? x * 8 + g : 0) * a.q_head + c * 4;
 #pragma unroll
@@ -480,18 +480,8 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
           const float f = (a.bf16 ? to_half<CH>(q4) : 1.0f) * a.scale_log2;  // of row x * 8 + g
           rf[z][x][0] = __shfl_sync(0xffffffffu, f, 8 * c);
           rf[z][x][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
-          if constexpr (NT == 4) {  // in shared memory, each warp's eight heads for all
-            if (x == warp) {
-#pragma unroll
-              for (int k = 0; k < CH; ++k) qs[((z * NT + x) * CH + k) * 32 + lane] = q4[k];
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < CH; ++k) qf[z][x][k] = q4[k];
-          }
         }
       }
-      if (NT == 4) consumers_sync();
     }
 
     if (mask != 0) {
@@ -524,14 +514,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
           for (int u = 0; u < 2; ++u) {
             const uint32_t f[4] = {half2_of(b[u]), half2_of(b[2 + u]), half2_of_high(b[u]), half2_of_high(b[2 + u])};
 #pragma unroll
-            for (int x = 0; x < NT; ++x) {
-              if constexpr (NT == 4) {
-                const uint2 q2 = qs[((z * NT + x) * CH + k + u) * 32 + lane];
-                E::mma(s[z][x], f, q2.x, q2.y);
-              } else {
-                E::mma(s[z][x], f, qf[z][x][k + u].x, qf[z][x][k + u].y);
-              }
-            }
+            for (int x = 0; x < NT; ++x) E::mma(s[z][x], f, qf[z][x][k + u].x, qf[z][x][k + u].y);
           }
         }
       }
@@ -570,6 +553,8 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
             mm[1] = n1;
             l[z][x][0] *= f0;
             l[z][x][1] *= f1;
+            lr[z][x][0] *= f0;
+            lr[z][x][1] *= f1;
 #pragma unroll
             for (int y = 0; y < CH; ++y) {
               o[z][x][y][0] *= f0;
@@ -580,12 +565,17 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
           }
           const float m0 = mm[0] == NEG ? 0.0f : mm[0], m1 = mm[1] == NEG ? 0.0f : mm[1];
           const float e0 = ex2(w[0] - m0), e1 = ex2(w[1] - m1), e2 = ex2(w[2] - m0), e3 = ex2(w[3] - m1);
-          // the sums are taken before the weights are rounded for the MMA: the
-          // rounding errors (half a step each, unbiased) enter the numerator only
           l[z][x][0] = fmaf(e0, iv0, fmaf(e2, iv1, l[z][x][0]));
           l[z][x][1] = fmaf(e1, iv0, fmaf(e3, iv1, l[z][x][1]));
-          p[z][x][0] = transpose8(E::pack(e0, e1));
-          p[z][x][1] = transpose8(E::pack(e2, e3));
+          const uint32_t p0 = E::pack(e0, e1), p1 = E::pack(e2, e3);
+          if (!a.bf16) {
+            const float2 r0 = __half22float2(*reinterpret_cast<const __half2*>(&p0));
+            const float2 r1 = __half22float2(*reinterpret_cast<const __half2*>(&p1));
+            lr[z][x][0] = fmaf(r0.x, iv0, fmaf(r1.x, iv1, lr[z][x][0]));
+            lr[z][x][1] = fmaf(r0.y, iv0, fmaf(r1.y, iv1, lr[z][x][1]));
+          }
+          p[z][x][0] = transpose8(p0);
+          p[z][x][1] = transpose8(p1);
         }
       }
       // O^T += V^T P^T
@@ -622,16 +612,20 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
         consumers_sync();  // all have read the stage, or the rows before
 #pragma unroll
         for (int z = 0; z < HP; ++z) {
-          if (x == 0) {
+          float even[2] = {1.0f, 1.0f};
 #pragma unroll
-            for (int x2 = 0; x2 < NT; ++x2)
+          for (int e = 0; e < 2; ++e) {
+            float sum = l[z][x][e], rounded = lr[z][x][e];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float t = l[z][x2][e];
-#pragma unroll
-                for (int i = 4; i < 32; i *= 2) t += __shfl_xor_sync(0xffffffffu, t, i);
-                if (g == 0) ml[(warp * HP + z) * C::kRows + x2 * 8 + 2 * c + e] = make_float2(m[z][x2][e], t);
-              }
+            for (int i = 4; i < 32; i *= 2) {
+              sum += __shfl_xor_sync(0xffffffffu, sum, i);
+              rounded += __shfl_xor_sync(0xffffffffu, rounded, i);
+            }
+            if (g == 0) ml[(warp * HP + z) * C::kRows + x * 8 + 2 * c + e] = make_float2(m[z][x][e], sum);
+            // fp16: O is divided by the sum of the weights that made it, so that a row with few
+            // keys has not their rounding and the result's (2 requests of 53 to 167 keys: 1.47 times
+            // the error of 32-bit arithmetic, so 1.1); not where weights below 2^-14 count
+            if (!a.bf16 && fabsf(rounded - sum) <= 0x1p-10f * sum && sum > 0.0f) even[e] = sum / rounded;
           }
           float* mine = os + (warp * HP + z) * 8 * D;
 #pragma unroll
@@ -639,7 +633,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
 #pragma unroll
             for (int e = 0; e < 2; ++e)  // columns moved by eights: four rows' stores on 32 banks
               *reinterpret_cast<float2*>(mine + (2 * c + e) * D + ((y * 16 + 2 * g) ^ (c * 8))) =
-                  make_float2(o[z][x][y][e], o[z][x][y][2 + e]);
+                  make_float2(o[z][x][y][e] * even[e], o[z][x][y][2 + e] * even[e]);
         }
         consumers_sync();
         const int r = x * 8 + r8;
@@ -744,9 +738,7 @@ cudaError_t launch(const Rows8Args& a, int grid, const CUtensorMap* maps, cudaSt
 
 template <int D, int HP, int LOAD>
 cudaError_t launch_rows(const Rows8Args& a, int grid, const CUtensorMap* maps, cudaStream_t stream) {
-  if (a.group <= 8) return launch<D, HP, 1, LOAD>(a, grid, maps, stream);
-  if (a.group <= 16) return launch<D, HP, 2, LOAD>(a, grid, maps, stream);
-  return launch<D, HP, 4, LOAD>(a, grid, maps, stream);
+  return a.group <= 8 ? launch<D, HP, 1, LOAD>(a, grid, maps, stream) : launch<D, HP, 2, LOAD>(a, grid, maps, stream);
 }
 
 }  // namespace
