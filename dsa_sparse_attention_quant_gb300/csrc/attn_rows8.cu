@@ -105,6 +105,17 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
+// A box of a 4-D tensor map into shared memory, completing on an mbarrier.
+__device__ __forceinline__ void tma_box_4d(void* dst, const void* tmap, uint64_t* bar, int32_t c0, int32_t c1,
+                                           int32_t c2, int32_t c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
+      "%6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+// This thread's plain accesses to shared memory before later TMA copies there.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // 8 bytes global -> shared.
 __device__ __forceinline__ void cp8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
       if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int2(-1, 0);
       return;
     }
-    fence_proxy_async();  // its scratch lies where copies will
+    fence_async();  // its scratch lies where copies will
   } else if (threadIdx.x == 0) {
     int req = 0;
     slice->t = part;
@@ -363,7 +374,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
         // lanes 0-3 a block of K each, 4-7 of V; lanes 0-4HP a block's and head's scales
         const int b = lane & 3;
         if (lane < 8 && b < blocks)
-          tma_load_4d((lane < 4 ? kdst : vdst) + b * kScaleBlock * RB, lane < 4 ? &mk : &mv, &full[stage], 0, h0 / HP,
+          tma_box_4d((lane < 4 ? kdst : vdst) + b * kScaleBlock * RB, lane < 4 ? &mk : &mv, &full[stage], 0, h0 / HP,
                       b * kScaleBlock, page);
         if (lane < 4 * HP && b < blocks)
           cp8(sdst + (b * HP + lane / 4) * kScaleBlock * 8,
@@ -494,7 +505,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
 #pragma unroll
           for (int i = 0; i < RB / 32; ++i) row[i] = make_uint4(0, 0, 0, 0);
         }
-        if (!SEL) fence_proxy_async();  // before the copies that follow into this stage
+        if (!SEL) fence_async();  // before the copies that follow into this stage
         __syncwarp();
       }
       // S^T = K q^T
@@ -696,7 +707,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
       if (SEL)
         consumers_sync();  // all have read it, before the copies that follow into this stage
       else
-        fence_proxy_async();
+        fence_async();
       if (!whole && starts) {  // it began here and goes on: so many tiles after this one, in the next slices
         desc_token = mt.z;
         const int64_t end = slice->end + (mt.w >> 4);
