@@ -131,7 +131,8 @@ __device__ __forceinline__ void write_block(const Write8Args& a, int64_t block, 
 #pragma unroll
     for (uint32_t w : {x[i].x, x[i].y, x[i].z, x[i].w}) most = __vmaxu2(most, w & 0x7FFF7FFFu);
   const uint32_t inf = inf_bits(T());
-  if ((most & 0xFFFFu) >= inf || (most >> 16) >= inf) {
+  const bool finite = !__any_sync(0xffffffffu, (most & 0xFFFFu) >= inf || (most >> 16) >= inf);
+  if (!finite) {
     most = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -160,18 +161,22 @@ __device__ __forceinline__ void write_block(const Write8Args& a, int64_t block, 
       *at = v;
     }
   }
+  uint8_t* at = codes + r0 * slot + ch * 8;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if (!in[i]) continue;
     float2 f[4] = {wide(x[i].x, T()), wide(x[i].y, T()), wide(x[i].z, T()), wide(x[i].w, T())};
+    if (!finite) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      // x - x: 0, or NaN for what is not finite, which has NaN as its code
-      f[k].x = fmaf(f[k].x, inv, f[k].x - f[k].x);
-      f[k].y = fmaf(f[k].y, inv, f[k].y - f[k].y);
+      for (int k = 0; k < 4; ++k) {
+        // x - x: 0, or NaN for what is not finite, which has NaN as its code
+        f[k].x += f[k].x - f[k].x;
+        f[k].y += f[k].y - f[k].y;
+      }
     }
-    *reinterpret_cast<uint2*>(codes + (i * RPI + r0) * slot + ch * 8) =
-        make_uint2(e4m3x4(f[0].x, f[0].y, f[1].x, f[1].y), e4m3x4(f[2].x, f[2].y, f[3].x, f[3].y));
+    *reinterpret_cast<uint2*>(at + i * RPI * slot) =
+        make_uint2(e4m3x4(f[0].x * inv, f[0].y * inv, f[1].x * inv, f[1].y * inv),
+                   e4m3x4(f[2].x * inv, f[2].y * inv, f[3].x * inv, f[3].y * inv));
   }
   __syncwarp();  // all have read the old scale
   if (lane == 0) *scale = s;
@@ -282,8 +287,9 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__
       if (start >= 0) {  // below 0: this request is not read
         const int sl = a.seq_lens[r];
         n = sl;
-        if (a.past) n -= a.qsl[r + 1] - a.qsl[r];
-        if (sl < 0 || n < 0 || n > a.max_keys || start + n > a.rows) {
+        const int ql = a.past ? a.qsl[r + 1] - a.qsl[r] : 0;
+        n -= ql;
+        if (sl < 0 || ql < 0 || n < 0 || n > a.max_keys || start + n > a.rows) {
           if (blockIdx.x == 0) flag_error(a.err, DSA_DEVERR_SEQ_RANGE);
           n = 0;
         }
