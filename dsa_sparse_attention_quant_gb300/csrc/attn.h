@@ -57,6 +57,7 @@ struct Rows8Args : RowsArgs {
   int64_t s_page, s_block, s_head;
   bool bf16;   // of q and out; else fp16
   bool pairs;  // heads of 64 side by side, an even number of them
+  int cluster;  // not split: CTAs that share a token's keys and join its rows among themselves
 };
 // maps: K and V as {row, rows of heads, 64 slots, pages}; not used for selected slots.
 cudaError_t launch_attn_rows8(const Rows8Args& a, int head_dim, bool selected, const CUtensorMap* maps,

@@ -111,6 +111,7 @@ struct RowsPlan {
   int64_t slices;    // split: slices of the tile list, else the tokens
   int64_t ctas;      // per slice, KV head and pass
   bool split;
+  int cluster;       // not split: CTAs that share a token (8 bits)
   size_t off_ml, off_o, bytes;
 };
 
@@ -130,6 +131,13 @@ constexpr int kDirectSms = 152;
 // (2 requests of 4096 keys, 40/1 heads: 14.3 us, with 1 tile 18.5; one of 768,
 // 32/8: 7.9, with 4 tiles 9.1).
 constexpr int kMinTiles = 2;
+// 8 bits: tokens of up to this many tiles are shared by clusters of up to 8 CTAs, two
+// tiles each at least, while all of them have places: a cluster joins its token's rows
+// through shared memory, without a second launch. 2 requests of 4096 keys, 40/8 heads of
+// 128: 11.5 us, cut into slices 14.3; 16 tokens of 1024 slots, 32/8: 15.8, 18.1; but one
+// request of 8192, 32/8: 15.9, 13.5; and with more than 8 query heads a KV head one
+// token of 2048 slots, 40/2: 12.6, 11.7.
+constexpr int kMostCluster = 8, kClusterTiles = 64;
 
 // One slice per CTA place: cut two or four times finer, so that CTAs that stream
 // slower take less, the partials and the CTAs' starts cost more than that gains
@@ -149,6 +157,15 @@ RowsPlan rows_plan(int64_t tokens, int64_t keys, int heads, int hkv, int head_di
   const int64_t tiles = keys > 0 ? (keys + kBlock - 1) / kBlock : 1;
   p.split = tiles > kDirectTiles || tokens * across > per_sm * kDirectSms;
   p.slices = tokens;
+  p.cluster = 1;
+  if (cache == kIn8 && p.rows == 8 && tiles <= kClusterTiles) {
+    while (p.cluster < kMostCluster && tiles >= 4 * p.cluster &&
+           2 * p.cluster * tokens * across <= per_sm * kDirectSms)
+      p.cluster *= 2;
+    // more than 8 tiles a CTA are cut into slices all the same
+    if (tiles > kDirectTiles * p.cluster) p.cluster = 1;
+    if (p.cluster > 1) p.split = false;
+  }
   if (p.split) {
     const int64_t most = (tokens * tiles + kMinTiles - 1) / kMinTiles;
     int64_t s = per_sm * (sms < kMostSms ? sms : kMostSms) / across;
@@ -204,7 +221,8 @@ bool pairs_of_64(const DsaKv8& kv) {
 
 // Codes of K or V as a 4-D tensor {row, rows of heads, slots, pages} with `pair` heads a
 // row: one box is 16 slots of a row.
-int make_kv8_map(CUtensorMap* m, const DsaKv8& kv, int pair, const void* base, int64_t page, int64_t slot, int64_t head) {
+int make_kv8_map(CUtensorMap* m, const DsaKv8& kv, int pair, const void* base, int64_t page, int64_t slot,
+                 int64_t head) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   int st = tensor_map_encoder(&enc);
   if (st != DSA_OK) return st;
@@ -260,7 +278,7 @@ Cache8Args cache8_args(const DsaKv8& kv) {
 
 // launch(): the kernels with the finished arguments.
 template <typename F>
-int run_rows(RowsArgs& a, int64_t tokens, int64_t keys, int head_dim, Cache cache, size_t need, void* ws,
+int run_rows(RowsArgs& a, int* cluster, int64_t tokens, int64_t keys, int head_dim, Cache cache, size_t need, void* ws,
              size_t ws_bytes, F launch) {
   const RowsPlan most = rows_plan(tokens, keys, a.heads, a.hkv, head_dim, cache, a.joint, kMostSms);
   if (most.ctas > INT_MAX || most.slices * a.hkv * most.passes > INT_MAX) return DSA_EINVAL;
@@ -274,6 +292,7 @@ int run_rows(RowsArgs& a, int64_t tokens, int64_t keys, int head_dim, Cache cach
   a.passes = p.passes;
   a.slices = static_cast<int>(p.slices);
   a.split = p.split;
+  if (cluster != nullptr) *cluster = p.cluster;
   if (p.split) {
     uint8_t* base = static_cast<uint8_t*>(ws);
     a.desc = reinterpret_cast<int2*>(base);
@@ -485,7 +504,7 @@ int dsa_attn_decode(const DsaBatch* batch, const DsaKv* kv, const DsaAttn* attn,
   if (batch->num_blocks != c.num_blocks || batch->num_decodes < 1) return DSA_EINVAL;
   RowsArgs a = rows_args(c, at);
   set_decode(a, batch, dev_err);
-  return run_rows(a, batch->num_decode_tokens, a.max_keys, c.head_dim, kIn16,
+  return run_rows(a, nullptr, batch->num_decode_tokens, a.max_keys, c.head_dim, kIn16,
                   rows_bytes(batch->num_decode_tokens, a.max_keys, a.heads, a.hkv, c.head_dim), ws, ws_bytes,
                   [&] { return from_cuda(launch_attn_rows(a, c.head_dim, c.dtype, false, stream)); });
 }
@@ -509,8 +528,9 @@ int dsa_attn_selected(const DsaKv* kv, const DsaAttn* attn, const int32_t* physi
   a.physical = physical;
   a.topk = topk;
   a.err = dev_err;
-  return run_rows(a, n_tokens, topk, c.head_dim, kIn16, rows_bytes(n_tokens, topk, a.heads, a.hkv, c.head_dim), ws,
-                  ws_bytes, [&] { return from_cuda(launch_attn_rows(a, c.head_dim, c.dtype, true, stream)); });
+  return run_rows(a, nullptr, n_tokens, topk, c.head_dim, kIn16,
+                  rows_bytes(n_tokens, topk, a.heads, a.hkv, c.head_dim), ws, ws_bytes,
+                  [&] { return from_cuda(launch_attn_rows(a, c.head_dim, c.dtype, true, stream)); });
 }
 
 int dsa_attn_prompt(const DsaBatch* batch, const DsaKv* kv, const int32_t* kv_start, const DsaAttn* attn,
@@ -643,7 +663,7 @@ int dsa_attn_decode8(const DsaBatch* batch, const DsaKv8* kv, const DsaAttn* att
   set_decode(a, batch, dev_err);
   a.pairs = pairs_of_64(c);
   a.joint = a.pairs ? 2 : 1;
-  return run_rows(a, batch->num_decode_tokens, a.max_keys, c.head_dim, kIn8,
+  return run_rows(a, &a.cluster, batch->num_decode_tokens, a.max_keys, c.head_dim, kIn8,
                   rows8_bytes(batch->num_decode_tokens, a.max_keys, a.heads, a.hkv, c.head_dim), ws, ws_bytes,
                   [&] {
                     CUtensorMap maps[2];
@@ -677,8 +697,8 @@ int dsa_attn_selected8(const DsaKv8* kv, const DsaAttn* attn, const int32_t* phy
   a.err = dev_err;
   a.pairs = pairs_of_64(c);
   a.joint = a.pairs ? 2 : 1;
-  return run_rows(a, n_tokens, topk, c.head_dim, kIn8, rows8_bytes(n_tokens, topk, a.heads, a.hkv, c.head_dim), ws,
-                  ws_bytes, [&] {
+  return run_rows(a, &a.cluster, n_tokens, topk, c.head_dim, kIn8,
+                  rows8_bytes(n_tokens, topk, a.heads, a.hkv, c.head_dim), ws, ws_bytes, [&] {
                     const CUtensorMap maps[2] = {};
                     return from_cuda(launch_attn_rows8(a, c.head_dim, true, maps, stream));
                   });

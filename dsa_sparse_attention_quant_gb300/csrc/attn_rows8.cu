@@ -50,6 +50,7 @@ constexpr float kLeastScale = 0x1p-64f, kMostScale = 0x1p126f;
 // heads a slot 93, single rows 184).
 enum Load : int { kPages, kSlots };
 
+constexpr int kMostCluster = 8;
 constexpr int kThreads8 = kThreads + 32;  // the consumers, and the loader
 
 // A row in shared memory is HP heads of a slot, 128 bytes: one head of 128, or two of 64
@@ -69,11 +70,12 @@ struct Rows8Cfg {
   static constexpr int kInfos = LOAD == kSlots ? 8 : kStages;
   static constexpr int kScales = kTile * HP;
   static constexpr int kOffMeta = kStages * kStageBytes;                  // int4 [kInfos]
-  static constexpr int kOffBar = kOffMeta + kInfos * 16;                  // full, empty [kInfos]
-  static constexpr int kOffScale = kOffBar + kInfos * 16;                 // float2 [kInfos][kScales]
+  static constexpr int kOffBar = kOffMeta + kInfos * 16;                 // full, empty, scaled [kInfos], meeting
+  static constexpr int kOffScale = kOffBar + kInfos * 32;                 // float2 [kInfos][kScales]
   static constexpr int kOffAt = kOffScale + kInfos * kScales * 8;         // slots: longlong2 [kInfos][kTile]
   static constexpr int kOffMl = kOffAt + (LOAD == kSlots ? kInfos * kTile * 16 : 0);  // float2 [kWarps][HP][kRows]
-  static constexpr int kOffScan = kOffMl + kWarps * HP * kRows * 8;       // the slice, scan scratch, abort flag
+  static constexpr int kOffParts = kOffMl + kWarps * HP * kRows * 8;      // cluster: float2 [HP][kRows]
+  static constexpr int kOffScan = kOffParts + HP * kRows * 8;             // the slice, scan scratch, abort flag
   static constexpr int kSmemBytes = kOffScan + 49 * 4;
   static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
   static_assert(kWarps * HP * 8 * D * 4 == kStageBytes, "O of four warps' eight heads fits a stage");
@@ -135,9 +137,6 @@ __device__ __forceinline__ float rcp(float x) {
 __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// The consumer warps' barrier.
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
-
 // A bf16 row of q as fp16: q4 of four columns each. Returns what the scores have to be
 // multiplied by. All lanes of a row (4) call.
 template <int KS>
@@ -162,6 +161,56 @@ __device__ __forceinline__ float to_half(uint2 (&q4)[KS]) {
     q4[k].y = Elem<__half>::pack(b.x * up, b.y * up);
   }
   return __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+}
+
+// W columns of a finished row, O = 2^M sum over L. L = 0: no key, or only scores of
+// -infinity (O is then 0, or NaN by 0 times a V that is NaN); no score but NaN leaves M
+// alone and L NaN.
+template <int W>
+__device__ __forceinline__ void store_row(const Rows8Args& a, int token, int64_t head, int c0, const float (&sum)[W],
+                                          float M, float L) {
+  uint16_t* out = static_cast<uint16_t*>(a.out) + token * a.out_row + head * a.out_head + c0;
+  const float inv = 1.0f / L;
+  uint32_t w[W / 2];
+#pragma unroll
+  for (int i = 0; i < W; i += 2)
+    w[i / 2] = L == 0.0f ? 0u
+               : a.bf16  ? Elem<__nv_bfloat16>::pack(sum[i] * inv, sum[i + 1] * inv)
+                         : Elem<__half>::pack(sum[i] * inv, sum[i + 1] * inv);
+  if constexpr (W == 8)
+    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+  else
+    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  if (a.lse != nullptr && c0 == 0)
+    a.lse[static_cast<int64_t>(token) * a.heads + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// All threads of the cluster's CTAs that have not ended; what they wrote before is seen.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// *p of the cluster's CTA `rank`: the same place in its shared memory.
+template <typename V>
+__device__ __forceinline__ V remote(const V* p, int rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  if constexpr (sizeof(V) == 16) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+  } else {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+  }
+}
+template <typename V>
+__device__ __forceinline__ V remote(const float* p, int rank) {
+  return remote<V>(reinterpret_cast<const V*>(p), rank);
 }
 
 // The dense tiles of a slice, 32 at a time: tile i of the slice belongs to the token
@@ -235,21 +284,31 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* empty = full + I;
+  uint64_t* scaled = SEL ? empty + I : full;  // slots: their places are used before their scales are there
+  uint64_t* meeting = empty + 2 * I;          // of the consumers
   int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta);
   float2* scales = reinterpret_cast<float2*>(smem + C::kOffScale);
   Slice* slice = reinterpret_cast<Slice*>(smem + C::kOffScan);
   int* abort_flag = reinterpret_cast<int*>(smem + C::kOffScan) + 48;
 
-  const int col = blockIdx.x / a.passes, pass = blockIdx.x - col * a.passes;
+  const int cluster = NT == 1 ? a.cluster : 1;
+  const int place = blockIdx.x / cluster, rank = blockIdx.x - place * cluster;  // a token's CTAs side by side
+  const int col = place / a.passes, pass = place - col * a.passes;
   // slice (split) or token, and the first of its KV heads
   const int part = col / (a.hkv / HP), h0 = (col - part * (a.hkv / HP)) * HP;
 
   if (threadIdx.x < I) {
-    mbar_init(&full[threadIdx.x], 33);  // lane 0 with the copies' bytes, and every lane's scales
+    // lane 0 with the copies' bytes or the slots' places, and every lane's scales
+    mbar_init(&full[threadIdx.x], SEL ? 1 : 33);
+    if (SEL) mbar_init(&scaled[threadIdx.x], 32);
     mbar_init(&empty[threadIdx.x], kWarps);
     fence_barrier_init();
   }
-  if (threadIdx.x == 0) *abort_flag = 0;
+  if (threadIdx.x == 0) {
+    mbar_init(meeting, kWarps);
+    fence_barrier_init();
+    *abort_flag = 0;
+  }
   // Launched while the stream's previous kernel drains: nothing is read before it has ended.
   pdl_wait();
   // ---- this CTA's slice
@@ -264,10 +323,11 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
   } else if (threadIdx.x == 0) {
     int req = 0;
     slice->t = part;
-    slice->kt = 0;
-    slice->n = SEL ? a.topk : token_keys(a, part, &req, h0 == 0 && pass == 0);
+    slice->n = SEL ? a.topk : token_keys(a, part, &req, h0 == 0 && pass == 0 && rank == 0);
     slice->req = req;
-    slice->left = tiles_of(slice->n);
+    const int tiles = tiles_of(slice->n);
+    slice->kt = tiles * rank / cluster;  // (a cluster's tokens are short)
+    slice->left = tiles * (rank + 1) / cluster - slice->kt;
   }
   __syncthreads();
   const int total = slice->left;
@@ -298,7 +358,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) fetch(ids[i], i < total);
     }
-    const int t1 = t, kt1 = kt, n1st = slice->n, left1st = tiles_of(slice->n) - kt;  // the first token: its keys, its tiles here
+    const int t1 = t, kt1 = kt, n1st = slice->n, left1st = tiles_of(n1st) - kt;  // the first token, its tiles here
     int32_t page1st = -1;
     if (!SEL && lane < left1st && n1st > 0)
       page1st = a.block_table[static_cast<int64_t>(slice->req) * a.bt_stride + kt + lane];
@@ -327,7 +387,8 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
         tiles = tiles_of(n);
       }
       const bool ends = kt == tiles - 1, last = ends || it == total - 1;
-      const int flags = (fresh ? kFirst : 0) | (last ? kLast : 0) | (kt == 0 ? kStartsItem : 0) | (ends ? kEndsItem : 0);
+      const int flags =
+          (fresh ? kFirst : 0) | (last ? kLast : 0) | (kt == 0 ? kStartsItem : 0) | (ends ? kEndsItem : 0);
       const int more = (tiles - 1 - kt) << 4;
       if (SEL) {
         const int32_t n0 = ids[0][0], n1 = ids[0][1];
@@ -340,6 +401,11 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
         const uint32_t p0 = id0 / kBlock, s0 = id0 % kBlock, p1 = id1 / kBlock, s1 = id1 % kBlock;
         at[lane] = make_longlong2(p0 * a.k_page + s0 * a.k_slot, p0 * a.v_page + s0 * a.v_slot);
         at[lane + 32] = make_longlong2(p1 * a.k_page + s1 * a.k_slot, p1 * a.v_page + s1 * a.v_slot);
+        __syncwarp();  // the rows' places are written
+        if (lane == 0) {
+          meta[stage] = make_int4(lo, hi, t, more | flags);
+          mbar_arrive(&full[stage]);
+        }
         // scales [block][head of the row][key of the block]
         const float* sp = a.scale + h0 * a.s_head;
         const float* sc0 = sp + p0 * a.s_page + s0 / kScaleBlock * a.s_block;
@@ -349,11 +415,6 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
         for (int z = 0; z < HP; ++z) {
           if (in0) cp8(d0 + z * kScaleBlock * 8, sc0 + z * a.s_head);
           if (in1) cp8(d0 + (2 * HP + z) * kScaleBlock * 8, sc1 + z * a.s_head);
-        }
-        __syncwarp();  // the rows' places are written
-        if (lane == 0) {
-          meta[stage] = make_int4(lo, hi, t, more | flags);
-          mbar_arrive(&full[stage]);
         }
       } else {
         int have = max(0, min(kTile, n - kt * kTile));
@@ -380,7 +441,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
           cp8(sdst + (b * HP + lane / 4) * kScaleBlock * 8,
               a.scale + page * a.s_page + b * a.s_block + (h0 + lane / 4) * a.s_head);
       }
-      cp_arrive(&full[stage]);
+      cp_arrive(&scaled[stage]);
       fresh = last;
       if (SEL) {
 #pragma unroll
@@ -409,6 +470,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
   const int head0 = pass * C::kRows;                // first query head of the group in this pass
   const int rows = min(C::kRows, a.group - head0);  // its query heads
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+  float2* parts_ml = reinterpret_cast<float2*>(smem + C::kOffParts);
   int desc_token = -1, desc_last = 0;  // the slice ends inside a token that it began: which, and its last slice
   float o[HP][NT][CH][4];
   float m[HP][NT][2], l[HP][NT][2], lr[HP][NT][2], rf[HP][NT][2];  // lr: fp16: the sum of the rounded weights
@@ -428,10 +490,10 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
   int info = 0, into = 0, next = 0, nphase = 0;  // of the tile at hand; of the next to be copied: stage, info
   auto issue = [&](bool in) {
     if (in) {
-      mbar_wait(&full[next], nphase, abort_flag, a.err);
-      __syncwarp();
+      const bool here = __all_sync(0xffffffffu, mbar_wait(&full[next], nphase, abort_flag, a.err));
       const int4 mt = meta[next];
-      const uint32_t mask = (static_cast<uint32_t>(warp < 2 ? mt.x : mt.y) >> (16 * (warp & 1))) & 0xffffu;
+      const uint32_t mask =
+          here ? (static_cast<uint32_t>(warp < 2 ? mt.x : mt.y) >> (16 * (warp & 1))) & 0xffffu : 0u;
       const longlong2* at = reinterpret_cast<const longlong2*>(smem + C::kOffAt) + next * kTile + warp * kWarpKeys;
       const uint32_t dst = smem_u32(smem) + into * C::kStageBytes + warp * kWarpKeys * RB;
 #pragma unroll
@@ -456,6 +518,15 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
 #pragma unroll 1
     for (int i = 0; i < S - 1; ++i) issue(i < total);
   }
+  // the consumers meet; a wait of theirs in vain is flagged, and all go on
+  int mphase = 0;
+  auto meet = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(meeting);
+    mbar_wait(meeting, mphase, abort_flag, a.err);
+    __syncwarp();
+    mphase ^= 1;
+  };
   int stage = 0, phase = 0;
 #pragma unroll 1
   for (int it = 0; it < total; ++it) {
@@ -463,11 +534,10 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
       cp_wait<S - 2>();
       __syncwarp();
       issue(it + S - 1 < total);  // into the stage consumed in the previous step
-    } else {
-      mbar_wait(&full[info], phase, abort_flag, a.err);  // in vain: flagged, and the rest is unspecified
-      __syncwarp();
     }
-    const int4 mt = meta[info];
+    // a wait in vain is flagged; the tile is left out and its rows are unspecified
+    const bool here = __all_sync(0xffffffffu, mbar_wait(&scaled[info], phase, abort_flag, a.err));
+    const int4 mt = here ? meta[info] : make_int4(0, 0, 0, 0);
     const uint32_t mask = (static_cast<uint32_t>(warp < 2 ? mt.x : mt.y) >> (16 * (warp & 1))) & 0xffffu;
     const int flags = mt.w & 15;
 
@@ -614,13 +684,14 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
       // O, eight query heads at a time, in the stage that has just been read; then 16
       // threads a row add them
       const bool whole = starts && (flags & kEndsItem);
+      float* parts = reinterpret_cast<float*>(smem + (stage + 1) % S * C::kStageBytes);
       const int r8 = threadIdx.x / 16;                                  // row of the eight
       constexpr int W = D / 16;                                         // columns of a thread
       const int at = r8 * D + ((threadIdx.x % 16 * W) ^ (r8 / 2 * 8));  // where they lie in eight rows of O
       float* os = reinterpret_cast<float*>(smem + stage * C::kStageBytes);
 #pragma unroll
       for (int x = 0; x < NT; ++x) {
-        consumers_sync();  // all have read the stage, or the rows before
+        meet();  // all have read the stage, or the rows before
 #pragma unroll
         for (int z = 0; z < HP; ++z) {
           float even[2] = {1.0f, 1.0f};
@@ -646,7 +717,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
               *reinterpret_cast<float2*>(mine + (2 * c + e) * D + ((y * 16 + 2 * g) ^ (c * 8))) =
                   make_float2(o[z][x][y][e] * even[e], o[z][x][y][2 + e] * even[e]);
         }
-        consumers_sync();
+        meet();
         const int r = x * 8 + r8;
         if (r < rows) {
 #pragma unroll
@@ -673,25 +744,15 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
               }
             }
             const int c0 = threadIdx.x % 16 * W;
-            if (whole) {
-              const int64_t head = static_cast<int64_t>(h0 + z) * a.group + head0 + r;
-              uint16_t* out = static_cast<uint16_t*>(a.out) + mt.z * a.out_row + head * a.out_head + c0;
-              // L = 0: no key, or only scores of -infinity (O is then 0, or NaN by 0 times
-              // a V that is NaN); no score but NaN leaves M alone and L NaN
-              const float inv = 1.0f / L;
-              uint32_t w[W / 2];
+            if (NT == 1 && cluster > 1) {
+              // for the cluster's CTAs to read: in the next stage, which no copy is left for
+              float* px = parts + (z * C::kRows + r) * D + c0;
 #pragma unroll
-              for (int i = 0; i < W; i += 2)
-                w[i / 2] = L == 0.0f ? 0u
-                           : a.bf16  ? Elem<__nv_bfloat16>::pack(sum[i] * inv, sum[i + 1] * inv)
-                                     : E::pack(sum[i] * inv, sum[i + 1] * inv);
-              if constexpr (W == 8)
-                *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-              else
-                *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-              if (a.lse != nullptr && c0 == 0)
-                a.lse[static_cast<int64_t>(mt.z) * a.heads + head] =
-                    L == 0.0f ? NEG : (M + log2f(L)) * 0.6931471805599453f;
+              for (int i = 0; i < W; i += 4)
+                *reinterpret_cast<float4*>(px + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
+              if (c0 == 0) parts_ml[z * C::kRows + r] = make_float2(M, L);
+            } else if (whole) {
+              store_row<W>(a, mt.z, static_cast<int64_t>(h0 + z) * a.group + head0 + r, c0, sum, M, L);
             } else {
               // slot 2c: a part that continues an earlier CTA's item; 2c + 1: the beginning of one
               const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0)) * HP + z;
@@ -705,10 +766,10 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
         }
       }
       if (SEL)
-        consumers_sync();  // all have read it, before the copies that follow into this stage
+        meet();  // all have read it, before the copies that follow into this stage
       else
         fence_async();
-      if (!whole && starts) {  // it began here and goes on: so many tiles after this one, in the next slices
+      if (a.split && !whole && starts) {  // it began here and goes on: so many tiles after this one, in the next slices
         desc_token = mt.z;
         const int64_t end = slice->end + (mt.w >> 4);
         desc_last = static_cast<int>((end * slice->in_use + slice->all - 1) / slice->all) - 1;
@@ -727,10 +788,58 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
     // a wait gave up: copies in flight land in this CTA's memory, so they get their time again
     const unsigned long long t0 = global_ns();
     for (int s = 0; s < I && s < total; ++s)
-      while (!mbar_try_wait(smem_u32(&full[s]), ((total - 1 - s) / I) & 1) && global_ns() - t0 < kWaitLimitNs) {
+      while (!mbar_try_wait(smem_u32(&scaled[s]), ((total - 1 - s) / I) & 1) && global_ns() - t0 < kWaitLimitNs) {
       }
   }
   if (a.split && threadIdx.x == 0) a.desc[blockIdx.x] = make_int2(desc_token, desc_last);
+  if (NT > 1 || cluster == 1) return;
+  // ---- a cluster's CTAs have a token's keys in turn: its rows are shared out, and each
+  // CTA adds its rows' parts out of the others' shared memory
+  if (total == 0 && threadIdx.x < HP * C::kRows) parts_ml[threadIdx.x] = make_float2(NEG, 0.0f);  // no keys, no part
+  cluster_sync();
+  constexpr int W = D / 16;
+  const int c0 = threadIdx.x % 16 * W, tiles = tiles_of(slice->n);
+  for (int i = (threadIdx.x / 16) * cluster + rank; i < HP * rows; i += kThreads / 16 * cluster) {
+    const int z = i / rows, row = z * C::kRows + i - z * rows;
+    float M = NEG, L = 0.0f, sum[W];
+    float2 v[kMostCluster];
+#pragma unroll
+    for (int k = 0; k < kMostCluster; ++k) {
+      v[k] = k < cluster ? remote<float2>(parts_ml + row, k) : make_float2(NEG, 0.0f);
+      M = fmaxf(M, v[k].x);
+    }
+    const float ref = M == NEG ? 0.0f : M;
+#pragma unroll
+    for (int j = 0; j < W; ++j) sum[j] = 0.0f;
+#pragma unroll
+    for (int k0 = 0; k0 < kMostCluster; k0 += 4) {
+      if (k0 >= cluster) break;
+      float4 u[4][W / 4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // the stage that a CTA's parts lie in is behind its last tile's
+        const int left = tiles * (k0 + k + 1) / cluster - tiles * (k0 + k) / cluster;
+        const float* px = reinterpret_cast<const float*>(smem + left % S * C::kStageBytes) + row * D + c0;
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j)
+          u[k][j] = k0 + k < cluster && left > 0 ? remote<float4>(px + 4 * j, k0 + k) : make_float4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float e = ex2(v[k0 + k].x - ref);
+        L = fmaf(v[k0 + k].y, e, L);
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j) {
+          sum[4 * j] = fmaf(u[k][j].x, e, sum[4 * j]);
+          sum[4 * j + 1] = fmaf(u[k][j].y, e, sum[4 * j + 1]);
+          sum[4 * j + 2] = fmaf(u[k][j].z, e, sum[4 * j + 2]);
+          sum[4 * j + 3] = fmaf(u[k][j].w, e, sum[4 * j + 3]);
+        }
+      }
+    }
+    store_row<W>(a, part, static_cast<int64_t>(h0 + z) * a.group + head0 + i - z * rows, c0, sum, M, L);
+  }
+  cluster_sync();  // all have read this CTA's
 }
 
 template <int D, int HP, int NT, int LOAD>
@@ -740,6 +849,22 @@ cudaError_t launch(const Rows8Args& a, int grid, const CUtensorMap* maps, cudaSt
   auto* fn = attn_rows8_kernel<D, HP, NT, LOAD>;
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(fn), C::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
+  if (a.cluster > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads8);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fn, a, maps[0], maps[1]);
+  }
   e = launch_pdl(fn, dim3(grid), dim3(kThreads8), C::kSmemBytes, stream, a, maps[0], maps[1]);
   if (e != cudaSuccess || !a.split) return e;
   // the next kernel is not let in while the join runs: its CTAs would take places
@@ -756,13 +881,15 @@ cudaError_t launch_rows(const Rows8Args& a, int grid, const CUtensorMap* maps, c
 
 cudaError_t launch_attn_rows8(const Rows8Args& a, int head_dim, bool selected, const CUtensorMap* maps,
                               cudaStream_t stream) {
-  const int grid = a.slices * (a.hkv / a.joint) * a.passes;
+  const int grid = a.slices * (a.hkv / a.joint) * a.passes * a.cluster;
   if (!selected) {
     if (head_dim == 128) return launch_rows<128, 1, kPages>(a, grid, maps, stream);
-    return a.pairs ? launch_rows<64, 2, kPages>(a, grid, maps, stream) : launch_rows<64, 1, kPages>(a, grid, maps, stream);
+    return a.pairs ? launch_rows<64, 2, kPages>(a, grid, maps, stream)
+                   : launch_rows<64, 1, kPages>(a, grid, maps, stream);
   }
   if (head_dim == 128) return launch_rows<128, 1, kSlots>(a, grid, maps, stream);
-  return a.pairs ? launch_rows<64, 2, kSlots>(a, grid, maps, stream) : launch_rows<64, 1, kSlots>(a, grid, maps, stream);
+  return a.pairs ? launch_rows<64, 2, kSlots>(a, grid, maps, stream)
+                 : launch_rows<64, 1, kSlots>(a, grid, maps, stream);
 }
 
 }  // namespace dsa

@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__
           y[u] = *reinterpret_cast<const uint2*>(vp + u * RPI * a.c.v_slot);
         }
       }
-      const float2 s = *reinterpret_cast<const float2*>(a.c.scale + page * a.c.s_page + part * a.c.s_block + h * a.c.s_head);
+      const float* sp = a.c.scale + page * a.c.s_page + part * a.c.s_block + h * a.c.s_head;
+      const float2 s = *reinterpret_cast<const float2*>(sp);
       const int64_t row = static_cast<int64_t>(a.kv_start[q0 + i]) + first + r0;
       uint16_t* ko = a.k + h * a.k_rhead + row * a.k_row + ch * 8;
       uint16_t* vo = a.v + h * a.v_rhead + row * a.v_row + ch * 8;
@@ -359,7 +360,8 @@ cudaError_t write8(const Write8Args& a, int num_sms, cudaStream_t stream) {
 
 cudaError_t launch_kv_write8(const Write8Args& a, int head_dim, int dtype, int num_sms, cudaStream_t stream) {
   if (dtype == DSA_BF16)
-    return head_dim == 128 ? write8<128, __nv_bfloat16>(a, num_sms, stream) : write8<64, __nv_bfloat16>(a, num_sms, stream);
+    return head_dim == 128 ? write8<128, __nv_bfloat16>(a, num_sms, stream)
+                           : write8<64, __nv_bfloat16>(a, num_sms, stream);
   return head_dim == 128 ? write8<128, __half>(a, num_sms, stream) : write8<64, __half>(a, num_sms, stream);
 }
 

@@ -544,9 +544,9 @@ DSA_API int dsa_kv_write8(const void *k, int64_t k_row_stride, int64_t k_head_st
  * batch->num_blocks must equal kv->num_blocks; keys that a block-table row and
  * max_seq_len allow are at most 2^27 - 64; query_start_loc may be NULL without
  * past, req_id_per_token is not used.
- * Flags: DSA_DEVERR_SEQ_RANGE (seq_len negative, below q_len with past, or
- * beyond the block-table row, max_seq_len or the packed rows: the request is not
- * read), DSA_DEVERR_BLOCK_RANGE (the block's rows are left as they were). */
+ * Flags: DSA_DEVERR_SEQ_RANGE (seq_len negative, with past q_len negative or above
+ * it, or keys beyond the block-table row, max_seq_len or the packed rows: the
+ * request is not read), DSA_DEVERR_BLOCK_RANGE (the block's rows are left as they were). */
 DSA_API int dsa_kv_read8(const DsaBatch *batch, const DsaKv8 *kv, const int32_t *kv_start, const DsaKv *rows,
                  int32_t past, int32_t *dev_err, dsa_stream_t stream);
 

@@ -97,7 +97,7 @@ def test_decode_lengths_and_groups(dtype, d, hq, hkv):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("hq,hkv", [(4, 4), (24, 2), (24, 1)])
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (24, 2), (24, 1), (16, 2), (9, 3)])
 def test_decode_split_over_the_length(dtype, d, hq, hkv):
     s = Step8(7 * hq + d, [5000, 1, 0, 777, 64, 2049], [1] * 6, hq, hkv, d, dtype)
     err = i32([0])
@@ -112,7 +112,7 @@ def test_decode_split_over_the_length(dtype, d, hq, hkv):
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("layout", ["heads", "joined", "loose"])
-@pytest.mark.parametrize("keys", [[300, 64, 129], [3000, 64, 129]])
+@pytest.mark.parametrize("keys", [[300, 64, 129], [3000, 64, 129], [6000, 64, 129]])
 def test_decode_cache_layouts_and_strided_rows(layout, keys, d):
     s = Step8(3, keys, [1, 1, 1], 8, 2, d, torch.bfloat16, layout)
     wide = torch.zeros((3, 9, 200), dtype=torch.bfloat16, device=DEV)   # q and out as views of wider tensors
@@ -122,6 +122,20 @@ def test_decode_cache_layouts_and_strided_rows(layout, keys, d):
     out, lse = dsa.attn_decode8(s.batch, q, s.k, s.v, s.sc, out=obuf[:, :, 16:16 + d])
     s.check(out, lse)
     assert bool((obuf[:, :, :16] == 5).all()) and bool((obuf[:, :, 16 + d:] == 5).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 1), (12, 1), (40, 2), (9, 3)])
+@pytest.mark.parametrize("keys", [[257], [1000, 70, 0], [4096], [520, 1, 3000, 64, 2]])
+def test_decode_tokens_that_clusters_share(dtype, d, hq, hkv, keys):
+    s = Step8(hq + d + len(keys), keys, [1] * len(keys), hq, hkv, d, dtype)
+    err = i32([0])
+    out, lse = s.run(dev_err=err)
+    s.check(out, lse)
+    assert int(err.item()) == 0
+    out2, lse2 = s.run()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
 def test_decode_several_tokens_per_request_and_padding():
@@ -174,7 +188,8 @@ def test_decode_sizes_of_q(dtype, factor):
 
 def test_decode_bf16_rows_far_from_fp16():
     for e in (-120, -60, 60, 100):
-        s = Step8(15, [300], [1], 4, 2, 64, torch.bfloat16, scales=(-max(-60, min(60, e)) - 8, -max(-60, min(60, e)) - 3))
+        up = max(-60, min(60, e))
+        s = Step8(15, [300], [1], 4, 2, 64, torch.bfloat16, scales=(-up - 8, -up - 3))
         s.q = s.q * 2.0 ** e
         s.q[0, 1, 5] = 0.0
         s.q[0, 2] = 0.0
@@ -183,7 +198,7 @@ def test_decode_bf16_rows_far_from_fp16():
 
 
 @pytest.mark.parametrize("spread", [(-8, -3), (-40, 20), (-64, -30), (30, 100)])
-@pytest.mark.parametrize("keys", [200, 3000])
+@pytest.mark.parametrize("keys", [200, 3000, 6000])
 def test_decode_values_of_uneven_scales(spread, keys):
     # V's scales far apart: the largest weight times scale leads, the sum does not
     s = Step8(20, [keys], [1], 8, 2, 64, torch.bfloat16)
@@ -222,7 +237,7 @@ def test_decode_zeroed_cache():
     assert bool((out == 0).all()) and bool(((lse - math.log(150)).abs() < 1e-5).all())
 
 
-@pytest.mark.parametrize("keys", [300, 3000])
+@pytest.mark.parametrize("keys", [300, 3000, 5000])
 def test_visible_nan_stays_in_its_rows(keys):
     s = Step8(16, [keys, 300], [1, 1], 4, 2, 64, torch.bfloat16)
     at = torch.tensor(s.slots(0, keys), dtype=torch.int32, device=DEV)
@@ -342,14 +357,39 @@ def test_rows_beyond_32_bit_offsets():
     q = torch.randn((1, 16, d), generator=g, device=DEV).to(torch.bfloat16)
     batch = dsa.Batch(i32([0, 1]), i32([64]), i32([[blocks - 1]]), i32([0]), 1, blocks)
     last = (k[blocks - 1:], v[blocks - 1:], sc[blocks - 1:])
-    for out, lse in (dsa.attn_selected8(q, k, v, sc, slots.to(torch.int32)[None]), dsa.attn_decode8(batch, q, k, v, sc)):
+    phys = slots.to(torch.int32)[None]
+    for out, lse in (dsa.attn_selected8(q, k, v, sc, phys), dsa.attn_decode8(batch, q, k, v, sc)):
         check_lists(q, *last, [torch.arange(64, device=DEV)], out, lse, torch.bfloat16, d ** -0.5)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hkv", [1, 2])
+def test_cache_of_one_page(d, hkv):
+    # the page's stride is nothing's, the only head's neither
+    g = torch.Generator(device=DEV).manual_seed(31)
+    codes_of = codes(g, 64, hkv, d)
+    k, v = (torch.as_strided(codes_of, (1, 64, hkv, d), (1, hkv * d, 3 if hkv == 1 else d, 1)) for _ in range(2))
+    sc = torch.full((1, 4, hkv, 2), 2.0 ** -7, device=DEV)
+    q = torch.randn((1, 4 * hkv, d), generator=g, device=DEV).to(torch.bfloat16)
+    batch = dsa.Batch(i32([0, 1]), i32([50]), i32([[0]]), i32([0]), 1, 1)
+    phys = torch.arange(50, dtype=torch.int32, device=DEV)[None]
+    for out, lse in (dsa.attn_selected8(q, k, v, sc, phys), dsa.attn_decode8(batch, q, k, v, sc)):
+        check_lists(q, k, v, sc, [torch.arange(50, device=DEV)], out, lse, torch.bfloat16, d ** -0.5)
+    rows = [torch.randn((20, hkv, d), generator=g, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    k, v = (torch.as_strided(torch.zeros((64, hkv, d), dtype=torch.uint8, device=DEV).view(F8), (1, 64, hkv, d),
+                             (1, hkv * d, 3 if hkv == 1 else d, 1)) for _ in range(2))
+    k2, v2, sc2 = dsa.new_kv_cache8(1, hkv, d)
+    dsa.kv_write8(*rows, torch.arange(30, 50, device=DEV), k, v, sc)
+    sc2.fill_(2.0 ** -7)
+    dsa.kv_write8(*rows, torch.arange(30, 50, device=DEV), k2, v2, sc2)
+    assert torch.equal(k.view(torch.uint8), k2.view(torch.uint8)) and torch.equal(sc, sc2)
 
 
 # ----------------------------------------------------------- streams and graphs
 
-def test_streams_and_captured_graphs():
-    s = Step8(30, [3000, 500, 77], [1] * 3, 16, 2, 128, torch.bfloat16)
+@pytest.mark.parametrize("keys", [3000, 7000])
+def test_streams_and_captured_graphs(keys):
+    s = Step8(30, [keys, 500, 77], [1] * 3, 16, 2, 128, torch.bfloat16)
     phys = torch.full((3, 900), -1, dtype=torch.int32, device=DEV)
     for r, n in enumerate([900, 500, 77]):
         phys[r, :n] = torch.tensor(s.slots(r, n), dtype=torch.int32, device=DEV)

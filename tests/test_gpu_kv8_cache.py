@@ -21,7 +21,8 @@ def cache8(gen, blocks, hkv, d, layout="pages", filled=True):
     """An 8-bit cache in one of several memory layouts, its codes and scales random
     (what slots may hold that were written before), or as it is made."""
     if layout == "heads":       # [blocks, heads, 64, d], scales [blocks, heads, 4, 2]
-        k, v = (torch.zeros((blocks, hkv, 64, d), dtype=torch.uint8, device=DEV).view(F8).transpose(1, 2) for _ in range(2))
+        k, v = (torch.zeros((blocks, hkv, 64, d), dtype=torch.uint8, device=DEV).view(F8).transpose(1, 2)
+                for _ in range(2))
         sc = torch.zeros((blocks, hkv, 4, 2), device=DEV).transpose(1, 2)
     elif layout == "joined":    # K and V in one allocation with room between the rows, scales in wider rows
         both = torch.zeros((blocks, 2, 64, hkv, d + 16), dtype=torch.uint8, device=DEV).view(F8)
@@ -82,7 +83,7 @@ def test_write_lists_of_slots(dtype, d, hkv, layout):
     err = i32([0])
     for slots in ([5],                                         # joins a block
                   [16],                                        # opens one
-                  list(range(60, 70)) + [-1] + list(range(30, 36)) + [70, 71, -1],   # over a page's end, a block in two runs
+                  list(range(60, 70)) + [-1] + list(range(30, 36)) + [70, 71, -1],  # a page's end, a block twice
                   [383, 0, 382, 15, 7]):                       # in no order
         m.write(*rows(g, len(slots), hkv, d, dtype), slots, dev_err=err)
         m.check()
@@ -126,8 +127,8 @@ def test_write_token_by_token():
 
 def test_write_scales_at_their_borders():
     # 448 * 2^e and its neighbours; zeros; the type's least and largest values
-    vals = [448.0, 450.0, 446.0, 1.75, 1.7578125, 1.7421875, 0.0, -0.0, 2.0 ** -70, 2.0 ** -133, 3.38953139e38, -3.38953139e38,
-            2.0 ** -55.2, 7.0 * 2 ** -60]
+    vals = [448.0, 450.0, 446.0, 1.75, 1.7578125, 1.7421875, 0.0, -0.0, 2.0 ** -70, 2.0 ** -133, 3.38953139e38,
+            -3.38953139e38, 2.0 ** -55.2, 7.0 * 2 ** -60]
     g = torch.Generator(device=DEV).manual_seed(4)
     m = Mirror(*cache8(g, len(vals), 1, 64))
     k = torch.zeros((len(vals), 1, 64), dtype=torch.bfloat16, device=DEV)
@@ -247,7 +248,7 @@ def test_read_bad_metadata_is_flagged():
     bt = i32([[0, 1], [2, 3], [4, 99], [6, 7], [5, 5]])
 
     def read(lens, qlens, starts, past=False):
-        qsl = [0]
+        qsl = [3]
         for n in qlens:
             qsl.append(qsl[-1] + n)
         batch = dsa.Batch(i32(qsl), i32(lens), bt, i32([]), 0, 8, max_seq_len=128)
@@ -261,9 +262,13 @@ def test_read_bad_metadata_is_flagged():
     assert err == 2 | 16
     assert torch.equal(ko[:64], val[0].to(torch.bfloat16)) and torch.equal(ko[64:100], val[1, :36].to(torch.bfloat16))
     assert bool((ko[100:230] == 9).all())                       # longer than the row: not read
-    assert torch.equal(ko[230:294], val[4].to(torch.bfloat16)) and bool((ko[294:] == 9).all())   # page 99; beyond the rows
+    # page 99; beyond the rows
+    assert torch.equal(ko[230:294], val[4].to(torch.bfloat16)) and bool((ko[294:] == 9).all())
     ko, vo, err = read([10, 10, 0, 0, 0], [11, 10, 0, 0, 0], [0, 20, 50, 60, 2 ** 31 - 1], past=True)
     assert err == 16 and bool((ko == 9).all())                  # shorter than the query; nothing but the query
+    ko, vo, err = read([10, 20, 0, 0, 0], [-2, 4, 0, 0, 0], [0, 100, 0, 0, 0], past=True)
+    assert err == 16 and bool((ko[:100] == 9).all()) and bool((ko[116:] == 9).all())
+    assert torch.equal(ko[100:116], val[2, :16].to(torch.bfloat16))
 
 
 def test_read_and_write_beyond_32_bit_offsets():

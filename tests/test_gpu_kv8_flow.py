@@ -136,7 +136,8 @@ class Loop8:
                 k, v, sv = self.stored(layer, r)
                 assert k.shape[0] == lens[i]
                 for e in range(HQ):
-                    ref = kv8_ref.attend(q[layer][i, e], k[:, e // 4], v[:, e // 4], sv[:, e // 4], D ** -0.5, torch.bfloat16)
+                    h = e // 4
+                    ref = kv8_ref.attend(q[layer][i, e], k[:, h], v[:, h], sv[:, h], D ** -0.5, torch.bfloat16)
                     for out, lse in (got[layer], dense):
                         check(out[i, e], lse[i, e], ref, f"layer {layer} row {r} head {e}")
         assert dsa.check_device_error(self.err) == 0

@@ -96,12 +96,21 @@ def test_read_refused():
 
 def test_scratch_checked_and_sized():
     lib = binding.load()
-    need = lib.dsa_attn_decode8_workspace_size(ctypes.byref(batch()), 8, 2, 128)
-    assert need > 0 and decode(size=need - 1) == ENOSPACE
-    assert decode(ws=None) == EINVAL and decode(ws=4104) == EINVAL
-    need = lib.dsa_attn_selected8_workspace_size(4, 700, 8, 2, 128)
-    assert need > 0 and selected(size=need - 1) == ENOSPACE
+    b = batch(max_seq_len=50000, bt_stride=800)
+    need = lib.dsa_attn_decode8_workspace_size(ctypes.byref(b), 8, 2, 128)
+    assert need > 0 and decode(b=b, size=need - 1) == ENOSPACE
+    assert decode(b=b, ws=None) == EINVAL and decode(b=b, ws=4104) == EINVAL
+    need = lib.dsa_attn_selected8_workspace_size(4, 20000, 8, 2, 128)
+    assert need > 0 and selected(topk=20000, size=need - 1) == ENOSPACE
+    # short rows are not cut, or among CTAs that join them without scratch
     assert lib.dsa_attn_selected8_workspace_size(4, 64, 8, 2, 128) == 0
+    assert lib.dsa_attn_selected8_workspace_size(4, 700, 8, 2, 128) == 0
+    # what suffices for more tokens or longer rows suffices for fewer and shorter ones
+    for hq, hkv in ((8, 8), (8, 1), (32, 8), (40, 2)):
+        size = [[lib.dsa_attn_selected8_workspace_size(n, 64 * t, hq, hkv, 128) for t in (1, 3, 8, 9, 16, 33, 64, 65, 300)]
+                for n in (1, 2, 5, 9, 20, 60, 150, 500, 4000)]
+        assert all(a <= b for row in size for a, b in zip(row, row[1:]))
+        assert all(a <= b for col in zip(*size) for a, b in zip(col, col[1:]))
     for bad in ((4, 700, 7, 2, 128), (4, 700, 8, 2, 100), (-1, 700, 8, 2, 128), (4, 0, 8, 2, 128), (4, 700, 8, 0, 128)):
         assert lib.dsa_attn_selected8_workspace_size(*bad) == 0
     assert lib.dsa_attn_decode8_workspace_size(ctypes.byref(batch(num_reqs=-1)), 8, 2, 128) == 0
