@@ -20,20 +20,38 @@
 // where the largest is 2^6 at least).
 //
 // What bounds it: one read of the codes, 2*D bytes a (key, KV head), and 0.5 of
-// scales for 4*G*D operations.
+// scales for 4*G*D operations: HBM, in the large calls. 64/8 heads of 128: 8 requests of 128K
+// keys 318 us (6.7 TB/s), 32 of 4K to 8K 72 us (5.6: 4 us until all CTAs stream,
+// 4 between their ends, 3 of the join); 64 tokens of 2048 selected slots 70 us (3.9 TB/s:
+// rows of 128 bytes in no order; 57 us with each token's slots in order); 24 requests of up to
+// 8K, 16/16 heads of 64, 28 us. One request of 300 keys takes 9 to 10 us, the host's time for
+// the call. More than 16 query heads a KV head: the making of fragments and the MMAs (8
+// requests of 32K keys, 64/1 heads of 128: 61 to 67 us, the keys alone 10).
 //
-// Mapping: slices, warps and rings as in attn_rows.cu. The MMAs take the keys as
-// their 16 rows and the query heads as their 8 columns (S^T = K q^T, O^T = V^T P^T):
-// G <= 8 query heads fill the tile that a 16-row tile of heads would half fill, and
-// K's and V's fragments, which have to be made from codes, are A operands that
-// two tiles of heads share (G > 8). More than 16 query heads take a pass over the keys
-// per 16 of them: with tiles for 32 the registers do not suffice (8 requests of 32K
-// keys, 64/1 heads of 128: 61 us, so 74; 40/2 of 64: 52, so 98). A lane's four codes of a K row are four columns
-// d..d+3: two of them are taken as the MMA's k slots 2c, 2c+1 and two as 2c+8, 2c+9,
-// and q's columns are loaded in that order. V comes through the transposing ldmatrix
-// as pairs of codes (2d, 2d+1): even columns become the tile's rows 0-7, odd ones
-// rows 8-15, so that no byte moves between lanes. P^T is S^T's fragment transposed
-// (movmatrix).
+// Fragments: the MMAs take the keys as their 16 rows and the query heads as their 8
+// columns (S^T = K q^T, O^T = V^T P^T): G <= 8 query heads fill the tile that a 16-row
+// tile of heads would half fill, and K's and V's fragments, which have to be made from
+// codes, are A operands that two tiles of heads share (G > 8). More than 16 query heads
+// take a pass over the keys per 16 of them: with tiles for 32 the registers do not suffice
+// (8 requests of 32K keys, 64/1 heads of 128: 61 us, so 74; 40/2 of 64: 52, so 98). A
+// lane's four codes of a K row are four columns d..d+3: two of them are taken as the MMA's
+// k slots 2c, 2c+1 and two as 2c+8, 2c+9, and q's columns are loaded in that order. V
+// comes through the transposing ldmatrix as pairs of codes (2d, 2d+1): even columns become
+// the tile's rows 0-7, odd ones rows 8-15, so that no byte moves between lanes. P^T is
+// S^T's fragment transposed (movmatrix).
+//
+// Mapping: the (token, 64-key tile) list is cut into slices, and parts are joined, as in
+// attn_rows.cu. A CTA has four consumer warps, which own 16 keys of a tile each (a scale
+// block), and a loader warp, which finds tokens, pages and slots ahead, 32 tiles at a time,
+// and fills the stages with TMA boxes of 16 slots; so the consumers' registers hold only
+// what the products need, and three CTAs sit on an SM, or two where G > 8 (each warp with
+// copies of its own, two CTAs: 8 requests of 128K keys 361 us, 32 of 4K to 8K 84).
+// Selected slots' rows the consumers fetch themselves (Load, below), from addresses that
+// the loader has made. Heads of 64 are taken two at a time where they lie side by side, so
+// that a row in shared memory is 128 bytes (the ragged requests: 39 us, so 27).
+//
+// Short tokens (rows_plan) are shared by the CTAs of a cluster, which join a token's rows
+// out of each other's shared memory: one launch and no scratch.
 #include "attn_rows.cuh"
 
 namespace dsa {

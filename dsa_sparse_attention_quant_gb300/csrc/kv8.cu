@@ -13,7 +13,11 @@
 // depends on the call's rows and the block alone, not on the order of the list or of
 // the threads.
 //
-// What bounds both: HBM, 4*D bytes of rows and 2*D of codes a (token, head).
+// What bounds both: HBM, 4*D bytes of rows and 2*D of codes a (token, head). 8 heads of
+// 128: 30572 rows of 8 requests written in 35 us (5.4 TB/s; the claims are a launch of
+// their own), 113K rows of 8 requests of up to 16K read back in 109 us (6.5 TB/s, two
+// thirds of it writes). 64 rows written, or 301 read back, take 8 to 9 us, the host's
+// time for the call.
 #include "attn.h"
 #include "common.cuh"
 
@@ -346,7 +350,8 @@ cudaError_t write8(const Write8Args& a, int num_sms, cudaStream_t stream) {
   cudaError_t e = launch_pdl(write8_claim_kernel, dim3(static_cast<unsigned>((a.n_tokens + kThreads - 1) / kThreads)),
                              dim3(kThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
-  // tokens may lie in one block or each in its own: few CTAs' blocks are shared by more
+  // tokens may lie in one block or each in its own: few CTAs' blocks are shared by more, up to
+  // 8 CTAs an SM (1500 rows of 1500 sequences 14.9 us; up to 2 17.5, up to 32 16.8)
   const int64_t chunks = (a.n_tokens + kPer - 1) / kPer, want = static_cast<int64_t>(num_sms) * 8 / chunks;
   const int64_t most = (static_cast<int64_t>(kPer) * 2 * a.c.hkv + kWarps - 1) / kWarps;
   const int64_t across = want < 1 ? 1 : want < most ? want : most;
@@ -369,7 +374,9 @@ cudaError_t launch_kv_read8(const Read8Args& a, int head_dim, int dtype, int num
   // at most so many blocks are read, whatever the lengths
   const int64_t blocks = static_cast<int64_t>(a.num_reqs) * ((a.max_keys + kScaleBlock - 1) / kScaleBlock);
   int64_t grid = (blocks * a.c.hkv + kWarps - 1) / kWarps;
-  const int64_t cap = static_cast<int64_t>(num_sms) * 16;
+  // so many CTAs an SM that those at the end are short (113K rows, 8 heads of 128: 107.3 us;
+  // with 16 109.0, with 8 110.9)
+  const int64_t cap = static_cast<int64_t>(num_sms) * 32;
   if (grid > cap) grid = cap;
   if (grid < 1) grid = 1;
   const dim3 g(static_cast<unsigned>(grid)), b(kThreads);
