@@ -150,8 +150,7 @@ RowsPlan rows_plan(int64_t tokens, int64_t keys, int heads, int hkv, int head_di
   // the kernels' tiles of query heads, and their CTAs per SM (RowsCfg, Rows8Cfg)
   p.rows = cache == kIn8 ? 8 : 16;
   if (p.rows < group) p.rows *= 2;
-  const int row = cache == kIn8 && joint > 1 ? 128 : head_dim;
-  const int per_sm = cache == kIn8 && p.rows * row <= 8 * 128 ? 3 : 2;
+  const int per_sm = cache == kIn8 && (p.rows == 8 || joint == 1) ? 3 : 2;
   p.passes = (group + p.rows - 1) / p.rows;
   const int64_t across = static_cast<int64_t>(hkv / joint) * p.passes;  // CTAs a slice
   const int64_t tiles = keys > 0 ? (keys + kBlock - 1) / kBlock : 1;

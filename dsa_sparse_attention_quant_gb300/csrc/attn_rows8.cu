@@ -23,10 +23,10 @@
 // scales for 4*G*D operations: HBM, in the large calls. 64/8 heads of 128: 8 requests of 128K
 // keys 318 us (6.7 TB/s), 32 of 4K to 8K 72 us (5.6: 4 us until all CTAs stream,
 // 4 between their ends, 3 of the join); 64 tokens of 2048 selected slots 70 us (3.9 TB/s:
-// rows of 128 bytes in no order; 57 us with each token's slots in order); 24 requests of up to
-// 8K, 16/16 heads of 64, 28 us. One request of 300 keys takes 9 to 10 us, the host's time for
+// rows of 128 bytes in no order; 57 us with each token's slots in order); 24 requests of 1
+// to 4001, 16/16 heads of 64, 28 us. One request of 300 keys takes 9 to 10 us, the host's time for
 // the call. More than 16 query heads a KV head: the making of fragments and the MMAs (8
-// requests of 32K keys, 64/1 heads of 128: 61 to 67 us, the keys alone 10).
+// requests of 32K keys, 64/1 heads of 128: 61 us, the keys alone 10).
 //
 // Fragments: the MMAs take the keys as their 16 rows and the query heads as their 8
 // columns (S^T = K q^T, O^T = V^T P^T): G <= 8 query heads fill the tile that a 16-row
@@ -44,8 +44,8 @@
 // attn_rows.cu. A CTA has four consumer warps, which own 16 keys of a tile each (a scale
 // block), and a loader warp, which finds tokens, pages and slots ahead, 32 tiles at a time,
 // and fills the stages with TMA boxes of 16 slots; so the consumers' registers hold only
-// what the products need, and three CTAs sit on an SM, or two where G > 8 (each warp with
-// copies of its own, two CTAs: 8 requests of 128K keys 361 us, 32 of 4K to 8K 84).
+// what the products need, and three CTAs sit on an SM, or two for pairs of heads with G > 8 (each
+// warp with copies of its own, two CTAs: 8 requests of 128K keys 361 us, 32 of 4K to 8K 84).
 // Selected slots' rows the consumers fetch themselves (Load, below), from addresses that
 // the loader has made. Heads of 64 are taken two at a time where they lie side by side, so
 // that a row in shared memory is 128 bytes (the ragged requests: 39 us, so 27).
@@ -78,14 +78,18 @@ template <int D, int HP, int NT, int LOAD>
 struct Rows8Cfg {
   static constexpr int kRows = 8 * NT;                         // query heads of a KV head in a pass
   static constexpr int kRowBytes = HP * D;
-  static constexpr int kCtas = NT * kRowBytes <= 128 ? 3 : 2;  // per SM: what registers allow
+  static constexpr int kCtas = HP * NT > 2 ? 2 : 3;             // per SM: what registers allow
+  // q's fragments in shared memory, each thread's its own, where registers do not hold them: three CTAs
+  // then (8 requests of 32K keys, 64/1 heads of 128: 60.7 us, two with q in registers 64.9; 128/1 97.6,
+  // 108.3; but pairs of 40/2 heads of 64 67.5, two 58.3)
+  static constexpr bool kKeptQ = HP == 1 && NT * D > 128;
   static constexpr int kStageBytes = 2 * kTile * kRowBytes;    // a tile's K codes, then its V codes
   // D = 128: 8 requests of 128K keys, 64/8 heads: 321 us, with four stages 349
   static constexpr int kStages = LOAD == kSlots ? (kRowBytes == 64 ? 5 : kCtas == 3 ? 3 : 4)
                                                 : (kRowBytes == 128 ? 1 : 2) * (kCtas == 3 ? 3 : 6);
   // what a tile's consumers have to know besides, made by the loader: as far ahead as
   // the codes are, or with slots further, since their addresses come this way
-  static constexpr int kInfos = LOAD == kSlots ? 8 : kStages;
+  static constexpr int kInfos = LOAD == kSlots ? (kKeptQ ? 6 : 8) : kStages;
   static constexpr int kScales = kTile * HP;
   static constexpr int kOffMeta = kStages * kStageBytes;                  // int4 [kInfos]
   static constexpr int kOffBar = kOffMeta + kInfos * 16;                 // full, empty, scaled [kInfos], meeting
@@ -94,7 +98,8 @@ struct Rows8Cfg {
   static constexpr int kOffMl = kOffAt + (LOAD == kSlots ? kInfos * kTile * 16 : 0);  // float2 [kWarps][HP][kRows]
   static constexpr int kOffParts = kOffMl + kWarps * HP * kRows * 8;      // cluster: float2 [HP][kRows]
   static constexpr int kOffScan = kOffParts + HP * kRows * 8;             // the slice, scan scratch, abort flag
-  static constexpr int kSmemBytes = kOffScan + 49 * 4;
+  static constexpr int kOffQ = (kOffScan + 49 * 4 + 15) / 16 * 16;        // uint4 [NT * D / 32][kThreads]
+  static constexpr int kSmemBytes = kKeptQ ? kOffQ + NT * D / 32 * kThreads * 16 : kOffScan + 49 * 4;
   static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
   static_assert(kWarps * HP * 8 * D * 4 == kStageBytes, "O of four warps' eight heads fits a stage");
   static_assert(kOffMeta >= 4096, "find_slice's rounds lie in the ring");
@@ -492,7 +497,8 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
   int desc_token = -1, desc_last = 0;  // the slice ends inside a token that it began: which, and its last slice
   float o[HP][NT][CH][4];
   float m[HP][NT][2], l[HP][NT][2], lr[HP][NT][2], rf[HP][NT][2];  // lr: fp16: the sum of the rounded weights
-  uint2 qf[HP][NT][CH];
+  uint2 qf[HP][C::kKeptQ ? 1 : NT][CH];
+  uint4* const kept = reinterpret_cast<uint4*>(smem + C::kOffQ) + threadIdx.x;
   bool starts = true;
   const float NEG = -INFINITY;
   // where ldmatrix's rows lie in a stage; chunk k of them is at the address with k << 4 flipped
@@ -571,7 +577,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
           l[z][x][0] = l[z][x][1] = lr[z][x][0] = lr[z][x][1] = 0.0f;
 #pragma unroll
           for (int y = 0; y < CH; ++y) o[z][x][y][0] = o[z][x][y][1] = o[z][x][y][2] = o[z][x][y][3] = 0.0f;
-          uint2(&q4)[CH] = qf[z][x];
+          uint2(&q4)[CH] = qf[z][C::kKeptQ ? 0 : x];
           const bool in = x * 8 + g < rows;
           const uint16_t* qp = q + (in ? x * 8 + g : 0) * a.q_head + c * 4;
 #pragma unroll
@@ -579,6 +585,11 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
           const float f = (a.bf16 ? to_half<CH>(q4) : 1.0f) * a.scale_log2;  // of row x * 8 + g
           rf[z][x][0] = __shfl_sync(0xffffffffu, f, 8 * c);
           rf[z][x][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+          if constexpr (C::kKeptQ) {
+#pragma unroll
+            for (int k = 0; k < CH; k += 2)
+              kept[(x * (CH / 2) + k / 2) * kThreads] = make_uint4(q4[k].x, q4[k].y, q4[k + 1].x, q4[k + 1].y);
+          }
         }
       }
     }
@@ -609,11 +620,20 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
           const int z = j / CH, k = j % CH;
           uint32_t b[4];  // keys 0-7 chunks j, j + 1; keys 8-15 chunks j, j + 1
           ldsm4(b, base ^ (j << 4));
+          uint4 q2[NT];  // chunks k and k + 1 of q
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+            if constexpr (C::kKeptQ) {
+              q2[x] = kept[(x * (CH / 2) + k / 2) * kThreads];
+            } else {
+              const uint2 q0 = qf[z][x][k], q1 = qf[z][x][k + 1];
+              q2[x] = make_uint4(q0.x, q0.y, q1.x, q1.y);
+            }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const uint32_t f[4] = {half2_of(b[u]), half2_of(b[2 + u]), half2_of_high(b[u]), half2_of_high(b[2 + u])};
 #pragma unroll
-            for (int x = 0; x < NT; ++x) E::mma(s[z][x], f, qf[z][x][k + u].x, qf[z][x][k + u].y);
+            for (int x = 0; x < NT; ++x) E::mma(s[z][x], f, u ? q2[x].z : q2[x].x, u ? q2[x].w : q2[x].y);
           }
         }
       }
