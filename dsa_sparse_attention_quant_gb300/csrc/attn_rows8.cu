@@ -22,8 +22,8 @@
 // What bounds it: one read of the codes, 2*D bytes a (key, KV head), and 0.5 of
 // scales for 4*G*D operations: HBM, in the large calls. 64/8 heads of 128: 8 requests of 128K
 // keys 318 us (6.7 TB/s), 32 of 4K to 8K 72 us (5.6: 4 us until all CTAs stream,
-// 4 between their ends, 3 of the join); 64 tokens of 2048 selected slots 70 us (3.9 TB/s:
-// rows of 128 bytes in no order; 57 us with each token's slots in order); 24 requests of 1
+// 4 between their ends, 3 of the join); 64 tokens of 2048 selected slots 64 us (4.3 TB/s:
+// rows of 128 bytes, in an order of their own: place_slots); 24 requests of 1
 // to 4001, 16/16 heads of 64, 28 us. One request of 300 keys takes 9 to 10 us, the host's time for
 // the call. More than 16 query heads a KV head: the making of fragments and the MMAs (8
 // requests of 32K keys, 64/1 heads of 128: 61 us, the keys alone 10).
@@ -69,6 +69,8 @@ constexpr float kLeastScale = 0x1p-64f, kMostScale = 0x1p126f;
 enum Load : int { kPages, kSlots };
 
 constexpr int kMostCluster = 8;
+constexpr int kFirstTiles = 6;  // a CTA's first tiles of slots, read in the list's order
+constexpr int64_t kApart = 1 << 28;
 constexpr int kThreads8 = kThreads + 32;  // the consumers, and the loader
 
 // A row in shared memory is HP heads of a slot, 128 bytes: one head of 128, or two of 64
@@ -89,13 +91,16 @@ struct Rows8Cfg {
                                                 : (kRowBytes == 128 ? 1 : 2) * (kCtas == 3 ? 3 : 6);
   // what a tile's consumers have to know besides, made by the loader: as far ahead as
   // the codes are, or with slots further, since their addresses come this way
-  static constexpr int kInfos = LOAD == kSlots ? (kKeptQ ? 6 : 8) : kStages;
+  static constexpr int kInfos = LOAD == kSlots ? (kKeptQ ? 5 : 8) : kStages;
   static constexpr int kScales = kTile * HP;
   static constexpr int kOffMeta = kStages * kStageBytes;                  // int4 [kInfos]
   static constexpr int kOffBar = kOffMeta + kInfos * 16;                 // full, empty, scaled [kInfos], meeting
   static constexpr int kOffScale = kOffBar + kInfos * 32;                 // float2 [kInfos][kScales]
   static constexpr int kOffAt = kOffScale + kInfos * kScales * 8;         // slots: longlong2 [kInfos][kTile]
-  static constexpr int kOffMl = kOffAt + (LOAD == kSlots ? kInfos * kTile * 16 : 0);  // float2 [kWarps][HP][kRows]
+  // slots: the next tiles' (a window), in the order in which they are read
+  static constexpr int kWindow = kKeptQ ? kFirstTiles : 12;
+  static constexpr int kOffIds = kOffAt + (LOAD == kSlots ? kInfos * kTile * 16 : 0);      // int [kWindow][kTile]
+  static constexpr int kOffMl = kOffIds + (LOAD == kSlots ? kWindow * kTile * 4 : 0);      // float2 [kWarps][HP][kRows]
   static constexpr int kOffParts = kOffMl + kWarps * HP * kRows * 8;      // cluster: float2 [HP][kRows]
   static constexpr int kOffScan = kOffParts + HP * kRows * 8;             // the slice, scan scratch, abort flag
   static constexpr int kOffQ = (kOffScan + 49 * 4 + 15) / 16 * 16;        // uint4 [NT * D / 32][kThreads]
@@ -294,6 +299,71 @@ struct TileWindow {
   }
 };
 
+// The slots of a window of tiles, from place j of a token's list on, into ids[]: in order,
+// or, where they lie in kApart bytes of K or more (page: a page's, or 0), brought into 16
+// stretches of the cache, from its lower to its upper end. CTAs that begin together then
+// go through the cache together, and what they read at a time lies in few of the memory's
+// pages, whose translations they share. 64 tokens of 2048 slots, 64/8 heads of 128, from
+// 64, 16 and 8 requests of 32K (2.1, 0.54 and 0.27 GB of K): 63.4, 58.6 and 57.7 us, in the
+// list's order 70.1, 63.6 and 56.1; 512 tokens of one 369, 352. (Windows of 16 tiles 63.4, heads
+// of 64 46.4; of 12 64.4, 43.1; of 8 65.7, 43.4.) Which keys make a tile changes by it, and so the
+// sums' order, but not from run to run. One warp.
+template <int TILES>
+__device__ __forceinline__ void place_slots(const int32_t* list, int j, int n, int tiles, int64_t page, int32_t* ids) {
+  const int lane = threadIdx.x & 31;
+  int id[2 * TILES];
+#pragma unroll
+  for (int i = 0; i < 2 * TILES; ++i)
+    id[i] = i < 2 * tiles && j + i * 32 + lane < n ? list[j + i * 32 + lane] : -1;
+  int lo = INT_MAX, hi = 0;
+  if (page > 0) {
+#pragma unroll
+    for (int i = 0; i < 2 * TILES; ++i) {
+      lo = min(lo, id[i] >= 0 ? id[i] : INT_MAX);
+      hi = max(hi, id[i]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+  }
+  if (hi <= lo || (hi - lo) / kBlock * page < kApart) {
+#pragma unroll
+    for (int i = 0; i < 2 * TILES; ++i)
+      if (i < 2 * tiles) ids[i * 32 + lane] = id[i];
+    __syncwarp();
+    return;
+  }
+  const int shift = max(0, 28 - __clz(hi - lo));  // (hi - lo) >> shift < 16
+  auto stretch = [&](int x) { return x >= 0 ? (x - lo) >> shift : 15; };  // absent ones come last
+  // lane b (and b + 16): the slots of stretch b so far; q: a slot's place in its stretch
+  int count = 0, q[2 * TILES];
+#pragma unroll
+  for (int i = 0; i < 2 * TILES; ++i) {
+    if (i >= 2 * tiles) break;
+    const int b = stretch(id[i]);
+    uint32_t m = 0xffffffffu;  // the lanes whose slot lies in stretch `lane % 16`
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t v = __ballot_sync(0xffffffffu, (b >> k) & 1);
+      m &= (lane >> k) & 1 ? v : ~v;
+    }
+    q[i] = __shfl_sync(0xffffffffu, count, b) + __popc(__shfl_sync(0xffffffffu, m, b) & ((1u << lane) - 1u));
+    count += __popc(m);
+  }
+  int first = count;  // of stretch `lane`, all stretches before it
+#pragma unroll
+  for (int k = 1; k < 16; k *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, first, k);
+    if (lane >= k) first += v;
+  }
+  first -= count;
+#pragma unroll
+  for (int i = 0; i < 2 * TILES; ++i) {
+    if (i >= 2 * tiles) break;
+    ids[__shfl_sync(0xffffffffu, first, stretch(id[i])) + q[i]] = id[i];
+  }
+  __syncwarp();
+}
+
 template <int D, int HP, int NT, int LOAD>
 __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
     attn_rows8_kernel(const __grid_constant__ Rows8Args a, const __grid_constant__ CUtensorMap mk,
@@ -359,28 +429,13 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
     // ---- the loader: a tile's codes and scales into a stage, stage after stage. What it
     // has to know first comes in whole batches, so that no tile waits for it by itself:
     // dense: lane i has tile i of 32: its token, tile of the token, keys and page;
-    // selected: the slots of the next kAhead tiles, lane i's i and i + 32
+    // selected: the slots of a window of tiles
     TileWindow win;
     Tile8 mine;
-    constexpr int kAhead = 3;
-    int32_t ids[kAhead][2];
+    int32_t* ids = reinterpret_cast<int32_t*>(smem + C::kOffIds);
+    int w = 0, wn = 0;  // tiles of the window: taken, in all
     const int each = SEL ? tiles_of(a.topk) : 0;  // a token's tiles
-    int t = slice->t, kt = slice->kt, ft = t, fkt = kt;  // selected: the tile at hand, the next to be fetched
-    auto fetch = [&](int32_t (&id)[2], bool in) {
-      id[0] = id[1] = -1;
-      const int j = fkt * kTile + lane;
-      const int32_t* p = a.physical + static_cast<int64_t>(ft) * a.topk + j;
-      if (in && j < a.topk) id[0] = p[0];
-      if (in && j + 32 < a.topk) id[1] = p[32];
-      if (++fkt == each) {
-        fkt = 0;
-        ++ft;
-      }
-    };
-    if (SEL) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) fetch(ids[i], i < total);
-    }
+    int t = slice->t, kt = slice->kt;
     const int t1 = t, kt1 = kt, n1st = slice->n, left1st = tiles_of(n1st) - kt;  // the first token, its tiles here
     int32_t page1st = -1;
     if (!SEL && lane < left1st && n1st > 0)
@@ -414,7 +469,14 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
           (fresh ? kFirst : 0) | (last ? kLast : 0) | (kt == 0 ? kStartsItem : 0) | (ends ? kEndsItem : 0);
       const int more = (tiles - 1 - kt) << 4;
       if (SEL) {
-        const int32_t n0 = ids[0][0], n1 = ids[0][1];
+        if (w == wn) {
+          w = 0;
+          wn = min(min(each - kt, total - it), it == 0 ? kFirstTiles : C::kWindow);
+          place_slots<C::kWindow>(a.physical + static_cast<int64_t>(t) * a.topk, kt * kTile, a.topk, wn,
+                                  wn < 8 ? 0 : a.k_page, ids);
+        }
+        const int32_t n0 = ids[w * kTile + lane], n1 = ids[w * kTile + 32 + lane];
+        ++w;
         const bool in0 = n0 >= 0 && static_cast<int64_t>(n0) < a.num_slots;
         const bool in1 = n1 >= 0 && static_cast<int64_t>(n1) < a.num_slots;
         if ((n0 != -1 && !in0) || (n1 != -1 && !in1)) flag_error(a.err, DSA_DEVERR_ID_RANGE);
@@ -467,12 +529,6 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
       cp_arrive(&scaled[stage]);
       fresh = last;
       if (SEL) {
-#pragma unroll
-        for (int i = 0; i + 1 < kAhead; ++i) {
-          ids[i][0] = ids[i + 1][0];
-          ids[i][1] = ids[i + 1][1];
-        }
-        fetch(ids[kAhead - 1], it + kAhead < total);
         if (++kt == each) {
           kt = 0;
           ++t;

@@ -337,6 +337,36 @@ def test_selected_layouts_and_bad_slots(layout, hq, hkv, d):
     check_selected(q, k, v, sc, bad, out, lse, torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 32, 4), (64, 16, 4), (64, 3, 3), (64, 24, 2), (128, 40, 2)])
+def test_selected_slots_far_apart(dtype, d, hq, hkv):
+    # K's pages are 8 MB apart, so that windows of the lists are brought into the cache's order
+    tokens, topk, blocks = 150, 2500, 40
+    q, k, v, sc, phys = selected_case(d + hq, tokens, topk, hq, hkv, d, dtype, blocks=blocks)
+    far = torch.zeros(blocks << 23, dtype=torch.uint8, device=DEV).view(F8)
+    far = torch.as_strided(far, k.shape, (1 << 23, hkv * d, d, 1))
+    far.copy_(k)
+    phys[1] = -1
+    phys[2, 700:] = -1
+    phys[3] = phys[3].clamp(max=64 * 8)      # many keys in the first stretch
+    phys[4] = phys[4, :1]                    # one slot, or none
+    phys[5] = phys[5].sort().values
+    phys[3:6] = torch.where(torch.isin(phys[3:6], phys[:3]), phys[3:6], -1)  # (slots that hold a key)
+    err = i32([0])
+    out, lse = dsa.attn_selected8(q, far, v, sc, phys, dev_err=err)
+    assert int(err.item()) == 0
+    check_lists(q, k, v, sc, [p[p >= 0].long() for p in phys], out, lse, dtype, d ** -0.5,
+                only=[0, 1, 2, 3, 4, 5, 77, 149])
+    out2, lse2 = dsa.attn_selected8(q, far, v, sc, phys)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    bad = phys.clone()
+    bad[7, 2400], bad[8, 1300], bad[9, 2499] = blocks * 64, -2, 2 ** 31 - 1
+    out, lse = dsa.attn_selected8(q, far, v, sc, bad, dev_err=err)
+    assert int(err.item()) == 4
+    bad[7, 2400] = bad[8, 1300] = bad[9, 2499] = -1
+    check_lists(q, k, v, sc, [p[p >= 0].long() for p in bad], out, lse, dtype, d ** -0.5, only=[7, 8, 9])
+
+
 def test_selected_all_slots_is_decode():
     s = Step8(21, [700, 90], [1, 1], 8, 2, 128, torch.bfloat16)
     phys = torch.full((2, 704), -1, dtype=torch.int32, device=DEV)
