@@ -37,7 +37,7 @@ struct RowsArgs {
   // work: split: slices of at least min_tiles tiles of the flat tile list, else
   // a token per slice; a CTA per slice, `joint` KV heads and pass
   int slices, min_tiles;
-  int joint;
+  int joint;  // 1 or 2
   bool split;
   int2* desc;       // [CTAs]: {token begun here and continued, its last slice}
   float2* part_ml;  // [2 * CTAs][joint][rows of a pass]

@@ -516,8 +516,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
   const bool in = head0 + r < a.group && r < krows;
   if (early) pdl_launch_dependents();
   pdl_wait();
-  // the main kernel's CTA of slice c with this head
-  auto cta = [&](int64_t c) { return (c * (a.hkv / a.joint) + h / a.joint) * a.passes + pass; };
+  // the main kernel's CTA of slice c with this head; a CTA has one head or two
+  const int two = a.joint - 1, across = a.hkv >> two, mine = h >> two;
+  auto cta = [&](int64_t c) { return (c * across + mine) * a.passes + pass; };
   const int2 d = a.desc[cta(part)];
   if (d.x < 0) return;
   float M = -INFINITY, L = 0.0f, o[V];
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
   if (in) {
 #pragma unroll 4
     for (int c = part + warp % WAYS; c <= d.y; c += WAYS) {
-      const int64_t slot = (2 * cta(c) + (c == part ? 1 : 0)) * a.joint + h % a.joint;
+      const int64_t slot = ((2 * cta(c) + (c == part ? 1 : 0)) << two) + (h & two);
       const float2 v = a.part_ml[slot * krows + r];
       const float* p = a.part_o + (slot * krows + r) * D + lane * V;
       float w[V];

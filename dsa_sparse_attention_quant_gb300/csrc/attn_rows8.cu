@@ -472,6 +472,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
         if (w == wn) {
           w = 0;
           wn = min(min(each - kt, total - it), it == 0 ? kFirstTiles : C::kWindow);
+          // (a few tiles are there sooner than they are in order)
           place_slots<C::kWindow>(a.physical + static_cast<int64_t>(t) * a.topk, kt * kTile, a.topk, wn,
                                   wn < 8 ? 0 : a.k_page, ids);
         }
