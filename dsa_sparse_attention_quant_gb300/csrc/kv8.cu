@@ -9,9 +9,11 @@
 //   code = RN(x / scale), and RN(code * old / scale) for the block's other slots
 //   where the scale rises.
 // Powers of two make x / scale exact, so each value is rounded once, and a code that
-// moves to a higher scale is rounded again only where it falls below 2^-6. All of it
-// depends on the call's rows and the block alone, not on the order of the list or of
-// the threads.
+// moves to a higher scale is rounded again only where it falls below 2^-6. A scale of
+// another kind that a block brings along stays while it suffices: its quotients and
+// products come in 32 bits in a way that leaves the rounding to a code right
+// (odd). All of it depends on the call's rows and the block alone, not on the order of
+// the list or of the threads.
 //
 // What bounds both: HBM, 4*D bytes of rows and 2*D of codes a (token, head). 8 heads of
 // 128: 30572 rows of 8 requests written in 35 us (5.4 TB/s; the claims are a launch of
@@ -78,6 +80,24 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t codes, float f) {
   values(codes, &lo, &hi);
   return e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
 }
+__device__ __forceinline__ bool power_of_two(float s) { return (__float_as_uint(s) & 0x7FFFFFu) == 0; }
+
+// A number q that stands for q + r, for a rounding to fewer bits: where r is not 0 its last
+// bit is set, towards r, so that it lies on the side of every halfway point that q + r lies
+// on. (Rounding to odd, after which a second rounding gives what one would: Boldo and Melquiond.)
+__device__ __forceinline__ float odd(float q, float r) {
+  uint32_t u = __float_as_uint(q);
+  if (r != 0.0f && !(u & 1u)) u += (__float_as_uint(r) ^ u) >> 31 ? 0xffffffffu : 1u;
+  return __uint_as_float(u);
+}
+__device__ __forceinline__ float product(float a, float b) { return odd(a * b, fmaf(a, b, -(a * b))); }
+// x / s as a number that rounds to the same code: x * inv rounded to five bits (Veltkamp's
+// splitting), among which are all codes and all points halfway between them, and moved to the
+// side of it that x / s lies on, which x - five * s tells without a rounding of its sign.
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  const float q = x * inv, c = __fmul_rn(q, 524289.0f), five = __fsub_rn(c, __fsub_rn(c, q));
+  return odd(five, fmaf(-five, s, x));
+}
 
 // ---------------------------------------------------------------------- write
 // Who writes a block: the call's tokens of a block are found by its slots, whatever
@@ -99,6 +119,34 @@ __global__ void __launch_bounds__(kThreads) write8_claim_kernel(const __grid_con
     const int32_t was = atomicCAS(at, seen, static_cast<int32_t>(t));
     if (was == seen) return;
     seen = was;
+  }
+}
+
+// The codes of a block whose scale was no power of two, which this file does not make: the
+// rows at `rows` over the scale s, and the codes that are there moved from `old` to it. A
+// function of its own, a value at a time: as a branch of write_block it costs the rows that
+// never take it 13% (30572 rows: 39.3 us, so 34.6).
+template <int D, typename T>
+__device__ __noinline__ void write_odd(const uint16_t* rows, int64_t row, uint8_t* codes, int64_t slot,
+                                       const int32_t* src, float s, float old) {
+  const float inv = 1.0f / s, f = old * inv;  // where s is above old it is a power of two, and f exact
+  const uint32_t inf = inf_bits(T());
+#pragma unroll 1
+  for (int i = 2 * (threadIdx.x & 31); i < kScaleBlock * D; i += 64) {
+    const int r = i / D, c = i % D, t = src[r];
+    uint16_t* at = reinterpret_cast<uint16_t*>(codes + r * slot + c);
+    float2 lo, hi;
+    if (t >= 0) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(rows + t * row + c);
+      lo = wide(w, T());
+      lo.x = (w & 0x7FFFu) < inf ? quotient(lo.x, s, inv) : NAN;
+      lo.y = (w >> 16 & 0x7FFFu) < inf ? quotient(lo.y, s, inv) : NAN;
+    } else {
+      if (!(s > old)) continue;
+      values(*at, &lo, &hi);
+      lo = make_float2(product(lo.x, f), product(lo.y, f));
+    }
+    *at = static_cast<uint16_t>(e4m3x4(lo.x, lo.y, 0.0f, 0.0f));
   }
 }
 
@@ -150,6 +198,12 @@ __device__ __forceinline__ void write_block(const Write8Args& a, int64_t block, 
   most = __reduce_max_sync(0xffffffffu, most);
   const float s = fmaxf(scale_of(wide(most, T()).x), old);
   const float inv = 1.0f / s;
+  if (!power_of_two(old)) {
+    write_odd<D, T>(rows, row, codes, slot, src, s, old);
+    __syncwarp();  // as below
+    if (lane == 0) *scale = s;
+    return;
+  }
   if (old > 0.0f && s > old) {
     // the rows that are there move to the higher scale
     const float f = old * inv;
@@ -210,7 +264,7 @@ __device__ __forceinline__ void write_blocks(const Write8Args& a, const Blocks<P
 
 // Few tokens: a CTA each, whose threads look the list through.
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) write8_few_kernel(const __grid_constant__ Write8Args a) {
+__global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) write8_few_kernel(const __grid_constant__ Write8Args a) {
   __shared__ Blocks<1> s;
   pdl_wait();
   const int64_t slot = a.slot_mapping[blockIdx.x], slots = a.c.num_blocks * kBlock, b = slot / kScaleBlock;

@@ -490,7 +490,8 @@ DSA_API int dsa_attn_prompt(const DsaBatch *batch, const DsaKv *kv, const int32_
  *               fp32 numbers, even, at least 2, below 2^39
  *   dtype       DSA_BF16 or DSA_FP16: of the rows that a call takes and gives
  *   num_kv_heads, head_dim, num_blocks  as in DsaKv
- * dsa_kv_write8 makes scales that are powers of two from 2^-64 to 2^120. The
+ * dsa_kv_write8 makes scales that are powers of two from 2^-64 to 2^120, and
+ * keeps another that a block has while it suffices for the rows that join. The
  * readers take any finite scales from 2^-64 to 2^120 (a smaller one of V's, 0
  * among them, counts as 2^-64); others give unspecified rows. */
 #define DSA_SCALE_BLOCK 16
@@ -515,8 +516,8 @@ typedef struct DsaKv8 {
  *           block: its other slots' codes keep their bits and stand for nothing
  *           until they are written), else the larger of need and the block's
  *           scale (one that is not positive and finite counts as none)
- *   code  = x / scale rounded to the nearest code; where the block's scale rises,
- *           its other slots' codes are rounded to it
+ *   code  = x / scale rounded once to the nearest code; where the block's scale
+ *           rises, its other slots' codes are rounded to it
  * so a sequence that grows slot by slot keeps each row within one step of its
  * block's largest, however it is cut into calls. NaN and infinities become NaN.
  * Of tokens with one slot the last of the list is written. Results do not depend

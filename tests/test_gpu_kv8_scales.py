@@ -1,0 +1,74 @@
+"""The 8-bit cache where a scale is not a power of two: what the header says of it,
+against 64 bits."""
+import pytest
+import torch
+
+from tests.test_gpu_kv8_cache import Mirror, cache8, rows
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F8 = torch.float8_e4m3fn
+
+
+def halfway(gen, n, bits):
+    """n numbers in [1, 2) of `bits` bits that end in a one: half-way between two of one bit less."""
+    return 1 + (2 * torch.randint(0, 1 << (bits - 2), (n,), generator=gen) + 1).double() * 2.0 ** (1 - bits)
+
+
+# ----------------------------------------------------------------------- write
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_write_joins_blocks_of_any_scale(dtype, d):
+    # some scales stay, some are raised
+    g = torch.Generator(device=DEV).manual_seed(d)
+    k, v, sc = cache8(g, 40, 3, d)
+    sc *= 1 + torch.rand(sc.shape, generator=g, device=DEV)
+    m = Mirror(k, v, sc)
+    m.write(*rows(g, 40, 3, d, dtype, 3.0), [64 * i + 20 for i in range(40)])
+    m.check()
+    m.write(*rows(g, 40, 3, d, dtype, 3.0), [64 * i + 21 for i in range(40)])
+    m.check()
+
+
+@pytest.mark.parametrize("n", [160, 1200])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_write_quotients_beside_a_tie(dtype, n):
+    # x / scale is half-way between two codes but for the scale's own rounding: less than 32 bits tell apart
+    g = torch.Generator().manual_seed(n)
+    blocks, hkv, d = n // 4, 4, 64
+    k, v, sc = cache8(torch.Generator(device=DEV).manual_seed(n), blocks, hkv, d)
+    new = []
+    for i in range(2):
+        x = torch.zeros((blocks * 4, hkv, d), dtype=dtype)
+        mag = (1 + torch.rand(blocks * 4 * hkv, generator=g)).to(dtype)
+        x[:, :, 7] = mag.view(-1, hkv) * (1 - 2 * torch.randint(0, 2, (blocks * 4, hkv), generator=g)).to(dtype)
+        tie = halfway(g, mag.numel(), 5) * 2.0 ** torch.randint(-5, 7, (mag.numel(),), generator=g).double()
+        sc[..., i] = (mag.double() / tie).float().view(blocks, 4, hkv).to(DEV)
+        new.append(x.to(DEV))
+    m = Mirror(k, v, sc)
+    m.write(*new, [16 * i + 5 for i in range(4 * blocks)])
+    m.check()
+
+
+@pytest.mark.parametrize("raise_by", [1, 3, 8])
+def test_write_raises_a_scale_beside_a_tie(raise_by):
+    # the codes that are there, times the old scale over the raised one, as above
+    g = torch.Generator().manual_seed(raise_by)
+    blocks, hkv, d = 60, 4, 64
+    k, v, sc = cache8(torch.Generator(device=DEV).manual_seed(1), blocks, hkv, d)
+    for i, c in enumerate((k, v)):
+        m = torch.randint(9, 16, (blocks * 4 * hkv,), generator=g)           # significand of the code, in eighths
+        code = (m.double() / 8 * 16).view(blocks, 4, hkv)
+        old = halfway(g, m.numel(), 5).view(blocks, 4, hkv) / code * 16      # in (0.5, 2)
+        old = torch.where(old >= 1, old / 2, old).float()
+        sc[..., i] = old.to(DEV)
+        at = code.float().to(DEV).to(F8)
+        for b in range(4):
+            c[:, 16 * b + 9, :, 3] = at[:, b]
+    m = Mirror(k, v, sc)
+    x = torch.full((blocks * 4, hkv, d), 0.25, dtype=torch.bfloat16, device=DEV)
+    x[:, :, 0] = 440.0 * 2.0 ** (raise_by - 1)
+    m.write(x, -x, [16 * i + 5 for i in range(4 * blocks)])
+    assert bool((m.sc == 2.0 ** (raise_by - 1)).all())
+    m.check()
