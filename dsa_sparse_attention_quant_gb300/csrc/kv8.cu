@@ -12,7 +12,7 @@
 // moves to a higher scale is rounded again only where it falls below 2^-6. A scale of
 // another kind that a block brings along stays while it suffices: its quotients and
 // products come in 32 bits in a way that leaves the rounding to a code right
-// (odd). All of it depends on the call's rows and the block alone, not on the order of
+// (odd), as those that are read back are. All of it depends on the call's rows and the block alone, not on the order of
 // the list or of the threads.
 //
 // What bounds both: HBM, 4*D bytes of rows and 2*D of codes a (token, head). 8 heads of
@@ -324,6 +324,20 @@ __global__ void __launch_bounds__(kThreads, 4) write8_many_kernel(const __grid_c
 }
 
 // ----------------------------------------------------------------------- read
+// A block's first `have` rows where its scale is no power of two: each product is rounded
+// once to the type. Apart from the others as write_odd is.
+template <int D, typename T>
+__device__ __noinline__ void read_odd(const uint8_t* codes, int64_t slot, uint16_t* rows, int64_t row, int have,
+                                      float s) {
+#pragma unroll 1
+  for (int i = 2 * (threadIdx.x & 31); i < have * D; i += 64) {
+    const int r = i / D, c = i % D;
+    float2 lo, hi;
+    values(*reinterpret_cast<const uint16_t*>(codes + r * slot + c), &lo, &hi);
+    *reinterpret_cast<uint32_t*>(rows + r * row + c) = narrow(product(lo.x, s), product(lo.y, s), T());
+  }
+}
+
 // A warp per (block of a request, head), K and V, in order; lengths are counted in
 // rounds of kThreads requests.
 template <int D, typename T>
@@ -383,6 +397,12 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__
       const float* sp = a.c.scale + page * a.c.s_page + part * a.c.s_block + h * a.c.s_head;
       const float2 s = *reinterpret_cast<const float2*>(sp);
       const int64_t row = static_cast<int64_t>(a.kv_start[q0 + i]) + first + r0;
+      if (!power_of_two(s.x) || !power_of_two(s.y)) {
+        const int64_t r = row - r0;
+        read_odd<D, T>(kp - r0 * a.c.k_slot - ch * 8, a.c.k_slot, a.k + h * a.k_rhead + r * a.k_row, a.k_row, have, s.x);
+        read_odd<D, T>(vp - r0 * a.c.v_slot - ch * 8, a.c.v_slot, a.v + h * a.v_rhead + r * a.v_row, a.v_row, have, s.y);
+        continue;
+      }
       uint16_t* ko = a.k + h * a.k_rhead + row * a.k_row + ch * 8;
       uint16_t* vo = a.v + h * a.v_rhead + row * a.v_row + ch * 8;
 #pragma unroll

@@ -1,9 +1,13 @@
 """The 8-bit cache where a scale is not a power of two: what the header says of it,
 against 64 bits."""
+import math
+
 import pytest
 import torch
 
-from tests.test_gpu_kv8_cache import Mirror, cache8, rows
+import dsa_sparse_attention_quant_gb300 as dsa
+from tests import kv8_ref
+from tests.test_gpu_kv8_cache import Mirror, cache8, i32, rows
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -13,6 +17,14 @@ F8 = torch.float8_e4m3fn
 def halfway(gen, n, bits):
     """n numbers in [1, 2) of `bits` bits that end in a one: half-way between two of one bit less."""
     return 1 + (2 * torch.randint(0, 1 << (bits - 2), (n,), generator=gen) + 1).double() * 2.0 ** (1 - bits)
+
+
+def round_to(x, dtype):
+    """x (64 bits, finite, within the range) to the type's nearest value, ties to even, in one step."""
+    info = torch.finfo(dtype)
+    e = torch.clamp(torch.frexp(x)[1].double() - 1, min=math.log2(info.tiny))
+    step = torch.exp2(e) * info.eps
+    return torch.round(x / step) * step
 
 
 # ----------------------------------------------------------------------- write
@@ -72,3 +84,35 @@ def test_write_raises_a_scale_beside_a_tie(raise_by):
     m.write(x, -x, [16 * i + 5 for i in range(4 * blocks)])
     assert bool((m.sc == 2.0 ** (raise_by - 1)).all())
     m.check()
+
+
+# ------------------------------------------------------------------------ read
+
+def read_all(k, v, sc, dtype):
+    blocks, _, hkv, d = k.shape
+    batch = dsa.Batch(i32([0, 0]), i32([64 * blocks]), torch.arange(blocks, dtype=torch.int32, device=DEV)[None],
+                      i32([]), 0, blocks)
+    out = [torch.zeros((64 * blocks, hkv, d), dtype=dtype, device=DEV) for _ in range(2)]
+    err = i32([0])
+    dsa.kv_read8(batch, k, v, sc, i32([0]), *out, dev_err=err)
+    assert int(err.item()) == 0
+    return [o.view(blocks, 64, hkv, d) for o in out]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_rounds_once(dtype, d):
+    # products half-way between two values of the type but for the scale's own rounding, and others
+    g = torch.Generator().manual_seed(d)
+    blocks, hkv = 50, 3
+    k, v, sc = cache8(torch.Generator(device=DEV).manual_seed(d), blocks, hkv, d)
+    bits = round(1 - math.log2(torch.finfo(dtype).eps))
+    for i, c in enumerate((k, v)):
+        n = blocks * 4 * hkv
+        code = (torch.randint(9, 16, (n,), generator=g).double() / 8).view(blocks, 4, hkv)
+        tie = halfway(g, n, bits + 1).view(blocks, 4, hkv)
+        sc[..., i] = (tie / code).float().to(DEV)
+        c[:, ::16, :, 3] = code.float().to(DEV).to(F8)
+    for c, s, out in zip((k, v), (sc[..., 0], sc[..., 1]), read_all(k, v, sc, dtype)):
+        want = round_to(kv8_ref.value(c, s).cpu(), dtype)
+        assert torch.equal(out.double().cpu(), want)
