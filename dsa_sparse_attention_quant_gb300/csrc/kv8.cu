@@ -324,8 +324,9 @@ __global__ void __launch_bounds__(kThreads, 4) write8_many_kernel(const __grid_c
 }
 
 // ----------------------------------------------------------------------- read
-// A block's first `have` rows where its scale is no power of two: each product is rounded
-// once to the type. Apart from the others as write_odd is.
+// A block's first `have` rows where a scale is no power of two, or V's below 2^-64: each
+// product is rounded once to the type. Apart from the others as write_odd is (V's least scale
+// taken there, for all blocks: 113K rows 114.4 us, so 107.6).
 template <int D, typename T>
 __device__ __noinline__ void read_odd(const uint8_t* codes, int64_t slot, uint16_t* rows, int64_t row, int have,
                                       float s) {
@@ -397,10 +398,11 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__
       const float* sp = a.c.scale + page * a.c.s_page + part * a.c.s_block + h * a.c.s_head;
       const float2 s = *reinterpret_cast<const float2*>(sp);
       const int64_t row = static_cast<int64_t>(a.kv_start[q0 + i]) + first + r0;
-      if (!power_of_two(s.x) || !power_of_two(s.y)) {
+      if (!power_of_two(s.x) || !power_of_two(s.y) || !(s.y >= 0x1p-64f)) {
         const int64_t r = row - r0;
         read_odd<D, T>(kp - r0 * a.c.k_slot - ch * 8, a.c.k_slot, a.k + h * a.k_rhead + r * a.k_row, a.k_row, have, s.x);
-        read_odd<D, T>(vp - r0 * a.c.v_slot - ch * 8, a.c.v_slot, a.v + h * a.v_rhead + r * a.v_row, a.v_row, have, s.y);
+        read_odd<D, T>(vp - r0 * a.c.v_slot - ch * 8, a.c.v_slot, a.v + h * a.v_rhead + r * a.v_row, a.v_row, have,
+                       fmaxf(s.y, 0x1p-64f));  // as attention takes it
         continue;
       }
       uint16_t* ko = a.k + h * a.k_rhead + row * a.k_row + ch * 8;

@@ -539,8 +539,9 @@ DSA_API int dsa_kv_write8(const void *k, int64_t k_row_stride, int64_t k_head_st
  * dsa_attn_prompt takes them (dtype and sizes as kv's). With past != 0 without
  * the request's own query tokens, keys [0, seq_lens[r] - q_len[r]): what a prompt
  * that brings its own K and V in 16 bits attends to besides. Other rows are left
- * as they were. Values are codes * scale, rounded once to the type (a power of
- * two scale leaves nothing to round within the type's range).
+ * as they were. Values are codes * scale, V's scale at least 2^-64 as above, rounded
+ * once to the type (a power of two scale leaves nothing to round within the type's
+ * range).
  *   kv_start  device int32 [num_reqs]; below 0: the request is not read
  * batch->num_blocks must equal kv->num_blocks; keys that a block-table row and
  * max_seq_len allow are at most 2^27 - 64; query_start_loc may be NULL without

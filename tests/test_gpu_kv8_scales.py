@@ -1,5 +1,5 @@
-"""The 8-bit cache where a scale is not a power of two: what the header says of it,
-against 64 bits."""
+"""The 8-bit cache where a scale is not a power of two, or a V scale less than 2^-64:
+what the header says of them, against 64 bits."""
 import math
 
 import pytest
@@ -116,3 +116,23 @@ def test_read_rounds_once(dtype, d):
     for c, s, out in zip((k, v), (sc[..., 0], sc[..., 1]), read_all(k, v, sc, dtype)):
         want = round_to(kv8_ref.value(c, s).cpu(), dtype)
         assert torch.equal(out.double().cpu(), want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_small_scales_of_values_as_attention_does(d):
+    # V's scales below 2^-64 count as 2^-64, as in the attention over the same cache
+    k, v, sc = cache8(torch.Generator(device=DEV).manual_seed(d), 3, 2, d)
+    small = [0.0, 2.0 ** -65, 1.5 * 2.0 ** -65, 2.0 ** -100, 2.0 ** -64, 1.25 * 2.0 ** -64]
+    for i, x in enumerate(small):
+        sc[i // 4, i % 4, :, 1] = x
+    ko, vo = read_all(k, v, sc, torch.bfloat16)
+    assert torch.equal(ko.double().cpu(), round_to(kv8_ref.value(k, sc[..., 0]).cpu(), torch.bfloat16))
+    want = round_to(kv8_ref.value(v, sc[..., 1].clamp(min=2.0 ** -64)).cpu(), torch.bfloat16)
+    assert torch.equal(vo.double().cpu(), want)
+    # one key: its weight is 1, so attention gives its V row (in fp32, rounded to the type)
+    q = torch.randn((1, 2, d), device=DEV).to(torch.bfloat16)
+    for i in range(len(small)):
+        slot = 16 * i + 3
+        out, _ = dsa.attn_selected8(q, k, v, sc, i32([[slot]]))
+        got, row = out[0].double().cpu(), want[slot // 64, slot % 64]
+        assert bool(((got - row).abs() <= 2.0 ** -7 * row.abs()).all()), small[i]
