@@ -46,9 +46,9 @@ struct RowsArgs {
 };
 cudaError_t launch_attn_rows(const RowsArgs& a, int head_dim, int dtype, bool selected, cudaStream_t stream);
 
-// The parts that the main kernel's slices left, added (attn_rows.cu): krows rows of the
-// workspace a CTA and KV head; early: the stream's next kernel may begin meanwhile.
-cudaError_t launch_attn_join(const RowsArgs& a, int head_dim, int dtype, int krows, bool early, cudaStream_t stream);
+// The parts that the slices of attn_rows8.cu left, added (attn_rows.cu): krows rows of the
+// workspace a CTA and KV head.
+cudaError_t launch_attn_join8(const RowsArgs& a, int head_dim, bool bf16, int krows, cudaStream_t stream);
 
 // The same rows over a cache of E4M3 codes (attn_rows8.cu): k, v and their strides
 // count bytes, the scales' strides count fp32 numbers.

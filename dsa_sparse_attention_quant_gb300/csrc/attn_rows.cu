@@ -502,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_con
 // 93), fewer a warp per row (32 of 2048, 64/8: 48.4 us, with eight 50.4).
 constexpr int kJoinWarps = 8;
 
-template <int D, typename T, int WAYS>
+// SCALED: V's scales are in the weights, and the sums come further down than O does.
+template <int D, typename T, int WAYS, bool SCALED>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ RowsArgs a, int krows,
                                                                     bool early) {
   constexpr int V = D / 32;
@@ -535,9 +536,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
       for (int i = 0; i < V; ++i) w[i] = p[i];
       // a part without a weight adds 0, or NaN where V is not finite: as within a CTA
       const float n = fmaxf(M, v.x), ref = n == -INFINITY ? 0.0f : n;
-      const float f = ex2(M - ref), e = ex2(v.x - ref);  // -inf: 0
+      float f, e;  // -inf: 0
+      if constexpr (SCALED) {
+        const float hf = half_way(M - ref), he = half_way(v.x - ref);
+        f = hf * hf;
+        e = he * he;
+        L = L * hf * hf + v.y * he * he;
+      } else {
+        f = ex2(M - ref);
+        e = ex2(v.x - ref);
+        L = L * f + v.y * e;
+      }
       M = n;
-      L = L * f + v.y * e;
 #pragma unroll
       for (int i = 0; i < V; ++i) o[i] = o[i] * f + w[i] * e;
     }
@@ -557,8 +567,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
     for (int i = 0; i < V; ++i) o[i] = 0.0f;
 #pragma unroll
     for (int w = 0; w < WAYS; ++w) {
-      const float f = ex2(sml[warp + w].x - ref);
-      L += sml[warp + w].y * f;
+      float f;
+      if constexpr (SCALED) {
+        const float half = half_way(sml[warp + w].x - ref);
+        f = half * half;
+        L += sml[warp + w].y * half * half;
+      } else {
+        f = ex2(sml[warp + w].x - ref);
+        L += sml[warp + w].y * f;
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) o[i] += so[warp + w][lane * V + i] * f;
     }
@@ -574,14 +591,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
 }
 
 // krows: rows of the workspace per main CTA and KV head; early: the next kernel's CTAs may begin.
-template <int D, typename T>
+template <int D, typename T, bool SCALED>
 cudaError_t join(const RowsArgs& a, int krows, bool early, cudaStream_t stream) {
   const int grid = a.slices * a.hkv * a.passes;
   const int rows = a.group < krows ? a.group : krows;
   if (a.slices > 4 * static_cast<int64_t>(a.n_tokens))
-    return launch_pdl(attn_join_kernel<D, T, 8>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, stream, a, krows,
+    return launch_pdl(attn_join_kernel<D, T, 8, SCALED>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, stream, a, krows,
                       early);
-  return launch_pdl(attn_join_kernel<D, T, 1>, dim3(grid, (rows + 7) / 8), dim3(32 * kJoinWarps), 0, stream, a, krows,
+  return launch_pdl(attn_join_kernel<D, T, 1, SCALED>, dim3(grid, (rows + 7) / 8), dim3(32 * kJoinWarps), 0, stream, a, krows,
                       early);
 }
 
@@ -593,7 +610,7 @@ cudaError_t launch(const RowsArgs& a, int grid, cudaStream_t stream) {
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(fn), C::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
   if ((e = launch_pdl(fn, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, a)) != cudaSuccess || !a.split) return e;
-  return join<D, T>(a, C::kRows, true, stream);
+  return join<D, T, false>(a, C::kRows, true, stream);
 }
 
 template <int D, typename T>
@@ -614,11 +631,12 @@ cudaError_t launch_attn_rows(const RowsArgs& a, int head_dim, int dtype, bool se
                          : launch_dt<64, __half>(a, grid, selected, stream);
 }
 
-cudaError_t launch_attn_join(const RowsArgs& a, int head_dim, int dtype, int krows, bool early, cudaStream_t stream) {
-  if (dtype == DSA_BF16)
-    return head_dim == 128 ? join<128, __nv_bfloat16>(a, krows, early, stream)
-                           : join<64, __nv_bfloat16>(a, krows, early, stream);
-  return head_dim == 128 ? join<128, __half>(a, krows, early, stream) : join<64, __half>(a, krows, early, stream);
+cudaError_t launch_attn_join8(const RowsArgs& a, int head_dim, bool bf16, int krows, cudaStream_t stream) {
+  if (bf16)
+    return head_dim == 128 ? join<128, __nv_bfloat16, true>(a, krows, false, stream)
+                           : join<64, __nv_bfloat16, true>(a, krows, false, stream);
+  return head_dim == 128 ? join<128, __half, true>(a, krows, false, stream)
+                         : join<64, __half, true>(a, krows, false, stream);
 }
 
 }  // namespace dsa

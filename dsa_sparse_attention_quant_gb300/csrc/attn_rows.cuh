@@ -78,6 +78,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Half of 2^d's exponent: sums that have to come further down than 2^-126 at a time are multiplied
+// by it twice. Where V's scales are in the weights (attn_rows8.cu), a part's sum may be 2^78 a key
+// and its reference 190 below the row's, and it a good part of the row's sum all the same.
+__device__ __forceinline__ float half_way(float d) { return ex2(0.5f * d); }
+
 // What a stage holds, written by the loader and read when it is consumed.
 enum : int { kFirst = 1, kLast = 2, kStartsItem = 4, kEndsItem = 8 };
 

@@ -10,7 +10,11 @@
 //   out = sum_j w_j cv_j / L,  L = sum_j w_j / sv_j,  lse = ln(2^M L)
 // for any reference M, a running maximum of the t_j that may lag (kSlack); so the
 // sums rescale, split and join as those of attn_rows.cu do, and one number per key
-// is all that the scales cost.
+// is all that the scales cost. Scales of V may be 2^184 apart (a block of zeros has the
+// least), and a key that is nothing to O still has its share e^(s_j) of L. So that w_j
+// does not end before the share counts for nothing, a scale below 2^-96 of one that has
+// moved M is taken as that (kSpread): O is off by 2^-96 of that scale's weight of e^(s_j)
+// at most. And parts' L are joined by factors that do not end where O's do (half_way).
 //
 // E4M3 codes are exact in fp16, so both products run as fp16 MMAs with fp32 sums
 // whatever q's type: bf16 rows of q are multiplied by the power of two that brings
@@ -61,6 +65,11 @@ namespace {
 constexpr int kScaleBlock = DSA_SCALE_BLOCK;
 static_assert(kWarpKeys == kScaleBlock, "a warp's keys of a tile share their scales");
 constexpr float kLeastScale = 0x1p-64f, kMostScale = 0x1p126f;
+// With the key k that made M (w_k = 2^6 or more) and a key j: w_j >= 2^6 e^(s_j - s_k) kSpread, which
+// is a number down to a share of 2^-36. Nothing in the stream pays for it but a register: where
+// shares above kSpread were added apart, by a branch for each tile, 8 requests of 32K keys, 64/4
+// heads of 128, took 65.4 us, so 64.4, and 24 of 1 to 4001 keys, 16/16 of 64, 28.4, so 27.7.
+constexpr float kSpread = 0x1p-96f;
 
 // How codes come into shared memory: TMA boxes of a page's 16 slots, asked for by the
 // loader; or 16 bytes a lane from the selected slots, asked for by the warps that use them
@@ -557,6 +566,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
   uint2 qf[HP][C::kKeptQ ? 1 : NT][CH];
   uint4* const kept = reinterpret_cast<uint4*>(smem + C::kOffQ) + threadIdx.x;
   bool starts = true;
+  float least[HP];  // V's scales count as this at least
   const float NEG = -INFINITY;
   // where ldmatrix's rows lie in a stage; chunk k of them is at the address with k << 4 flipped
   const int krow = warp * kWarpKeys + (lane & 7) + ((lane >> 4) << 3);
@@ -626,6 +636,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
       starts = flags & kStartsItem;
 #pragma unroll
       for (int z = 0; z < HP; ++z) {
+        least[z] = kLeastScale;
         const uint16_t* q = static_cast<const uint16_t*>(a.q) + mt.z * a.q_row +
                             (static_cast<int64_t>(h0 + z) * a.group + head0) * a.q_head;
 #pragma unroll
@@ -700,9 +711,9 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
         // scores in powers of two with V's scale in them; absent keys out
         const float2* sc = scales + info * C::kScales + (warp * HP + z) * kScaleBlock + (SEL ? g : 0);
         const float2 s0 = sc[0], s1 = SEL ? sc[8] : s0;
-        const float v0 = fminf(fmaxf(s0.y, kLeastScale), kMostScale), v1 = fminf(fmaxf(s1.y, kLeastScale), kMostScale);
-        const float lv0 = lg2(v0), lv1 = lg2(v1);
-        const float iv0 = rcp(v0), iv1 = rcp(v1);
+        const float v0 = fminf(fmaxf(s0.y, least[z]), kMostScale), v1 = fminf(fmaxf(s1.y, least[z]), kMostScale);
+        float lv0 = lg2(v0), lv1 = lg2(v1);
+        float iv0 = rcp(v0), iv1 = rcp(v1);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
           float(&w)[4] = s[z][x];
@@ -718,17 +729,39 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
           float(&mm)[2] = m[z][x];
           const bool move = t0 > mm[0] + (E::kHead + kSlack) || t1 > mm[1] + (E::kHead + kSlack);
           if (__any_sync(0xffffffffu, move)) {
+            float top = v0;  // the largest scale of the warp's keys
+            if constexpr (SEL) {
+              top = fmaxf((mask >> g) & 1 ? v0 : 0.0f, (mask >> (g + 8)) & 1 ? v1 : 0.0f);
+              top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+            }
+            if (top * kSpread > least[z]) {
+              least[z] = top * kSpread;
+              if constexpr (SEL) {  // (pages: they have one scale)
+                const float a0 = fmaxf(v0, least[z]), a1 = fmaxf(v1, least[z]), b0 = lg2(a0), b1 = lg2(a1);
+                w[0] += b0 - lv0;
+                w[1] += b0 - lv0;
+                w[2] += b1 - lv1;
+                w[3] += b1 - lv1;
+                t0 = fmaxf(w[0], w[2]);
+                t1 = fmaxf(w[1], w[3]);
+                lv0 = b0;
+                lv1 = b1;
+                iv0 = rcp(a0);
+                iv1 = rcp(a1);
+              }
+            }
 #pragma unroll
             for (int i = 4; i < 32; i *= 2) {
               t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, i));
               t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, i));
             }
             const float n0 = fmaxf(mm[0], t0 - E::kHead), n1 = fmaxf(mm[1], t1 - E::kHead);
-            const float f0 = mm[0] == NEG ? 0.0f : ex2(mm[0] - n0), f1 = mm[1] == NEG ? 0.0f : ex2(mm[1] - n1);
+            const float g0 = mm[0] == NEG ? 0.0f : half_way(mm[0] - n0), g1 = mm[1] == NEG ? 0.0f : half_way(mm[1] - n1);
+            const float f0 = g0 * g0, f1 = g1 * g1;
             mm[0] = n0;
             mm[1] = n1;
-            l[z][x][0] *= f0;
-            l[z][x][1] *= f1;
+            l[z][x][0] = l[z][x][0] * g0 * g0;
+            l[z][x][1] = l[z][x][1] * g1 * g1;
             lr[z][x][0] *= f0;
             lr[z][x][1] *= f1;
 #pragma unroll
@@ -826,9 +859,9 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
               const float2 v = ml[(w * HP + z) * C::kRows + r];
-              const float f = ex2(v.x - Ms);
+              const float half = half_way(v.x - Ms), f = half * half;
               const float* p = os + (w * HP + z) * 8 * D + at;
-              L = fmaf(v.y, f, L);
+              L = fmaf(v.y * half, half, L);
 #pragma unroll
               for (int i = 0; i < W; i += 4) {
                 const float4 u = *reinterpret_cast<const float4*>(p + i);
@@ -921,8 +954,8 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float e = ex2(v[k0 + k].x - ref);
-        L = fmaf(v[k0 + k].y, e, L);
+        const float half = half_way(v[k0 + k].x - ref), e = half * half;
+        L = fmaf(v[k0 + k].y * half, half, L);
 #pragma unroll
         for (int j = 0; j < W / 4; ++j) {
           sum[4 * j] = fmaf(u[k][j].x, e, sum[4 * j]);
@@ -964,7 +997,7 @@ cudaError_t launch(const Rows8Args& a, int grid, const CUtensorMap* maps, cudaSt
   if (e != cudaSuccess || !a.split) return e;
   // the next kernel is not let in while the join runs: its CTAs would take places
   // where one of this kernel's three would have to go (8 x 128K keys: 321 us, so 315)
-  return launch_attn_join(a, D, a.bf16 ? DSA_BF16 : DSA_FP16, C::kRows, false, stream);
+  return launch_attn_join8(a, D, a.bf16, C::kRows, stream);
 }
 
 template <int D, int HP, int LOAD>

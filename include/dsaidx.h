@@ -557,8 +557,8 @@ DSA_API int dsa_kv_read8(const DsaBatch *batch, const DsaKv8 *kv, const int32_t 
  * kv->dtype. Scores and sums are fp32; the weights, with V's scales in them, are
  * rounded to fp16 for the product with V's codes (2^-11 of each, or 2^-30 of the
  * row's largest, whichever is more), the result to the type when it is stored.
- * q's elements below 2^-38 of their row's largest may count as 0 (bf16). V's
- * scales that one row sees may lie up to 2^100 apart. */
+ * q's elements below 2^-38 of their row's largest may count as 0 (bf16), V's scales
+ * below 2^-96 of the largest that the row sees as that much of it. */
 DSA_API size_t dsa_attn_decode8_workspace_size(const DsaBatch *batch, int32_t num_heads,
                                        int32_t num_kv_heads, int32_t head_dim);
 DSA_API int dsa_attn_decode8(const DsaBatch *batch, const DsaKv8 *kv, const DsaAttn *attn, void *ws,
