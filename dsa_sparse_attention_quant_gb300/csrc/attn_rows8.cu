@@ -170,6 +170,11 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+// A weight as fp16 rounds it, but with all its bits however small it is: weights that are little
+// of O, by V's scale, may be a good part of L.
+__device__ __forceinline__ float to_11_bits(float e) {
+  return __uint_as_float((__float_as_uint(e) + 0x1000u) & 0xFFFFE000u);
+}
 // This thread's cp.async copies so far, as an arrival at the barrier when they have landed.
 __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
   float2* parts_ml = reinterpret_cast<float2*>(smem + C::kOffParts);
   int desc_token = -1, desc_last = 0;  // the slice ends inside a token that it began: which, and its last slice
   float o[HP][NT][CH][4];
-  float m[HP][NT][2], l[HP][NT][2], lr[HP][NT][2], rf[HP][NT][2];  // lr: fp16: the sum of the rounded weights
+  float m[HP][NT][2], l[HP][NT][2], lr[HP][NT][2], rf[HP][NT][2];  // lr: fp16: l of the rounded weights
   uint2 qf[HP][C::kKeptQ ? 1 : NT][CH];
   uint4* const kept = reinterpret_cast<uint4*>(smem + C::kOffQ) + threadIdx.x;
   bool starts = true;
@@ -778,10 +783,8 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
           l[z][x][1] = fmaf(e1, iv0, fmaf(e3, iv1, l[z][x][1]));
           const uint32_t p0 = E::pack(e0, e1), p1 = E::pack(e2, e3);
           if (!a.bf16) {
-            const float2 r0 = __half22float2(*reinterpret_cast<const __half2*>(&p0));
-            const float2 r1 = __half22float2(*reinterpret_cast<const __half2*>(&p1));
-            lr[z][x][0] = fmaf(r0.x, iv0, fmaf(r1.x, iv1, lr[z][x][0]));
-            lr[z][x][1] = fmaf(r0.y, iv0, fmaf(r1.y, iv1, lr[z][x][1]));
+            lr[z][x][0] = fmaf(to_11_bits(e0), iv0, fmaf(to_11_bits(e2), iv1, lr[z][x][0]));
+            lr[z][x][1] = fmaf(to_11_bits(e1), iv0, fmaf(to_11_bits(e3), iv1, lr[z][x][1]));
           }
           p[z][x][0] = transpose8(p0);
           p[z][x][1] = transpose8(p1);
@@ -834,7 +837,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
             if (g == 0) ml[(warp * HP + z) * C::kRows + x * 8 + 2 * c + e] = make_float2(m[z][x][e], sum);
             // fp16: O is divided by the sum of the weights that made it, so that a row with few
             // keys has not their rounding and the result's (2 requests of 53 to 167 keys: 1.47 times
-            // the error of 32-bit arithmetic, so 1.1); not where weights below 2^-14 count
+            // the error of 32-bit arithmetic, so 1.1); that sum is finite and as near where all is well
             if (!a.bf16 && fabsf(rounded - sum) <= 0x1p-10f * sum && sum > 0.0f) even[e] = sum / rounded;
           }
           float* mine = os + (warp * HP + z) * 8 * D;

@@ -106,3 +106,23 @@ def test_scales_and_scores_far_apart(keys, gap):
     for e in range(4):
         ref, want, tol, ltol = attend(s.q[0, e], kk, vv, sv, scale, torch.bfloat16)
         check(out[0, e], lse[0, e], (ref, want, tol + 448 * 2.0 ** (112 - 96), ltol), f"head {e}")
+
+
+@pytest.mark.parametrize("below", [10.2, 10.5, 11.0, 12.0, 14.0])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 2, 2), (128, 2, 1), (64, 12, 1), (128, 12, 1)])
+def test_small_share_of_keys_without_a_weight(d, hq, hkv, below):
+    # 64 keys of V = 1 and 64 of zeros (the least scale), whose scores are 2^-below of the others': a share that
+    # is the result's distance from 1. Every weight is a power of two, so that nothing else is rounded but scores of
+    # the zeros (2^-19 of their share, which is 2^-10 at most) and the result
+    k, v, sc = dsa.new_kv_cache8(2, hkv, d)
+    k[1], v[0] = (torch.full((64, hkv, d), x, device=DEV).to(k.dtype) for x in (-1.0, 64.0))
+    sc[..., 0] = 1.0
+    sc[0, :, :, 1], sc[1, :, :, 1] = 2.0 ** -6, 2.0 ** -64
+    q = torch.ones((1, hq, d), dtype=torch.float16, device=DEV)
+    batch = dsa.Batch(i32([0, 1]), i32([128]), i32([[0, 1]]), i32([0]), 1, 2)
+    slots = torch.arange(128, dtype=torch.int32, device=DEV)[None]
+    scale = below * math.log(2) / d
+    want = 1 / (1 + 2.0 ** -below)
+    for out, _ in (dsa.attn_decode8(batch, q, k, v, sc, scale=scale),
+                   dsa.attn_selected8(q, k, v, sc, slots, scale=scale)):
+        assert float((out.double() - want).abs().max()) <= 2.0 ** -12 + 2.0 ** -20
