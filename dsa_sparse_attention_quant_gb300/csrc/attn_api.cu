@@ -139,6 +139,11 @@ constexpr int kMinTiles = 2;
 // token of 2048 slots, 40/2: 12.6, 11.7.
 constexpr int kMostCluster = 8, kClusterTiles = 64;
 
+int64_t row_tiles(int64_t keys) { return keys > 0 ? (keys + kBlock - 1) / kBlock : 1; }
+
+// The kernels count a call's (token, tile) pairs in 32 bits.
+bool rows_fit(int64_t tokens, int64_t keys) { return tokens <= INT_MAX / row_tiles(keys); }
+
 // One slice per CTA place: cut two or four times finer, so that CTAs that stream
 // slower take less, the partials and the CTAs' starts cost more than that gains
 // (32 requests of 4K to 8K keys: 130.8, 134.4, 145.0 us).
@@ -153,7 +158,7 @@ RowsPlan rows_plan(int64_t tokens, int64_t keys, int heads, int hkv, int head_di
   const int per_sm = cache == kIn8 && (p.rows == 8 || joint == 1) ? 3 : 2;
   p.passes = (group + p.rows - 1) / p.rows;
   const int64_t across = static_cast<int64_t>(hkv / joint) * p.passes;  // CTAs a slice
-  const int64_t tiles = keys > 0 ? (keys + kBlock - 1) / kBlock : 1;
+  const int64_t tiles = row_tiles(keys);
   p.split = tiles > kDirectTiles || tokens * across > per_sm * kDirectSms;
   p.slices = tokens;
   p.cluster = 1;
@@ -279,6 +284,7 @@ Cache8Args cache8_args(const DsaKv8& kv) {
 template <typename F>
 int run_rows(RowsArgs& a, int* cluster, int64_t tokens, int64_t keys, int head_dim, Cache cache, size_t need, void* ws,
              size_t ws_bytes, F launch) {
+  if (!rows_fit(tokens, keys)) return DSA_EINVAL;
   const RowsPlan most = rows_plan(tokens, keys, a.heads, a.hkv, head_dim, cache, a.joint, kMostSms);
   if (most.ctas > INT_MAX || most.slices * a.hkv * most.passes > INT_MAX) return DSA_EINVAL;
   if (need > 0 && (ws == nullptr || !aligned16(ws))) return DSA_EINVAL;
@@ -304,9 +310,11 @@ int run_rows(RowsArgs& a, int* cluster, int64_t tokens, int64_t keys, int head_d
 // Scratch of a call over a cache in 16 bits, and in 8: the latter whatever the cache's
 // strides, which decide how many heads a CTA takes.
 size_t rows_bytes(int64_t tokens, int64_t keys, int heads, int hkv, int head_dim) {
+  if (!rows_fit(tokens, keys)) return 0;
   return rows_plan(tokens, keys, heads, hkv, head_dim, kIn16, 1, kMostSms).bytes;
 }
 size_t rows8_bytes(int64_t tokens, int64_t keys, int heads, int hkv, int head_dim) {
+  if (!rows_fit(tokens, keys)) return 0;
   const size_t one = rows_plan(tokens, keys, heads, hkv, head_dim, kIn8, 1, kMostSms).bytes;
   if (head_dim == 128 || hkv % 2 != 0) return one;
   const size_t two = rows_plan(tokens, keys, heads, hkv, head_dim, kIn8, 2, kMostSms).bytes;

@@ -111,7 +111,8 @@ __device__ __forceinline__ int token_keys(const RowsArgs& a, int t, int* req, bo
   return max(0, sl - (q1 - t) + 1);
 }
 
-__device__ __forceinline__ int tiles_of(int n) { return n > 0 ? (n + kTile - 1) / kTile : 1; }
+// (n up to 2^31 - 1)
+__device__ __forceinline__ int tiles_of(int n) { return n > 0 ? (n - 1) / kTile + 1 : 1; }
 
 // The tiles of a CTA's slice, in order.
 struct Cursor {

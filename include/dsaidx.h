@@ -425,7 +425,8 @@ typedef struct DsaAttn {
  * left as they were. batch->num_blocks must equal kv->num_blocks and every
  * seq_len is at most max_seq_len. The length of the keys is split over CTAs
  * where that helps and joined in a fixed order: the same call on the same
- * device gives the same bits.
+ * device gives the same bits. The decode tokens times the pages that the
+ * block-table row and max_seq_len allow each are at most 2^31 - 1.
  *   ws, ws_bytes  device scratch, 16-byte aligned, of
  *                 dsa_attn_decode_workspace_size() bytes; its contents need not
  *                 be kept between calls, and calls that may overlap on the GPU
@@ -445,7 +446,7 @@ DSA_API int dsa_attn_decode(const DsaBatch *batch, const DsaKv *kv, const DsaAtt
  *   physical  device int32 [n_tokens, topk]: slots page*64 + slot, -1 = none,
  *             in any order and anywhere in the row; a slot named twice counts
  *             twice
- *   topk      >= 1
+ *   topk      >= 1; n_tokens times ceil(topk / 64) is at most 2^31 - 1
  *   ws        as for dsa_attn_decode, dsa_attn_selected_workspace_size() bytes
  * Other slots outside the cache flag DSA_DEVERR_ID_RANGE and are left out. */
 DSA_API size_t dsa_attn_selected_workspace_size(int64_t n_tokens, int32_t topk, int32_t num_heads,
