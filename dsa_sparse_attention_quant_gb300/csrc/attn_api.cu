@@ -584,6 +584,7 @@ int dsa_attn_prompt(const DsaBatch* batch, const DsaKv* kv, const int32_t* kv_st
   a.num_tokens = batch->num_tokens;
   a.first_token = batch->num_decode_tokens;
   a.max_keys = packed ? batch->max_seq_len : max_keys(batch);
+  if (a.max_keys > INT_MAX - 127) a.max_keys = INT_MAX - 127;  // whole tiles of 128 keys are counted in 32 bits
   a.pair_heads = a.group % 2 == 0;
   a.head_units = a.pair_heads ? a.heads / 2 : a.heads;
   const int64_t unit = a.pair_heads ? 128 : 256;

@@ -470,8 +470,8 @@ DSA_API int dsa_attn_selected(const DsaKv *kv, const DsaAttn *attn, const int32_
  * batch->req_id_per_token is not read, but may not be NULL.
  * Flags: DSA_DEVERR_SEQ_RANGE (negative q_len, query tokens before
  * num_decode_tokens or beyond num_tokens: the request is refused, none of its
- * rows is written; seq_len negative or beyond the block-table row, max_seq_len
- * or the packed rows: its rows are empty), DSA_DEVERR_BLOCK_RANGE (the rows
+ * rows is written; seq_len negative or beyond the block-table row, max_seq_len,
+ * the packed rows or 2^31 - 128: its rows are empty), DSA_DEVERR_BLOCK_RANGE (the rows
  * that see the page are unspecified), DSA_DEVERR_TIMEOUT. No workspace. */
 DSA_API int dsa_attn_prompt(const DsaBatch *batch, const DsaKv *kv, const int32_t *kv_start,
                     const DsaAttn *attn, int32_t *dev_err, dsa_stream_t stream);

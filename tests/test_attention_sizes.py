@@ -90,3 +90,20 @@ def test_decode_row_of_the_greatest_length(bits):
     mean = torch.softmax(s, 1) @ v.abs()
     assert bool(((out[0].double() - want).abs() <= (2.0 ** -5 + 2.0 ** -6.9 + 2.0 ** -7) * mean).all())
     assert bool(((lse[0].double() - torch.logsumexp(s, 1) - math.log(MOST / 64)).abs() <= 2.0 ** -6).all())
+
+
+@pytest.mark.gpu
+def test_prompt_behind_a_context_of_the_greatest_length():
+    # 2^31 - 128 keys are the most that are read; a longer sequence is flagged and its rows are empty
+    g = torch.Generator(device=DEV).manual_seed(3)
+    args, _ = cache(16, g)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    table = torch.zeros((2, 1 << 25), dtype=torch.int32, device=DEV)
+    q = torch.randn((3, 4, 64), generator=g, device=DEV).to(torch.bfloat16)
+    for n in (MOST, MOST - 126):
+        b = dsa.Batch(i32([0, 2, 3]), i32([n, 5]), table, i32([0, 0, 1]), 0, 1, max_seq_len=MOST)
+        err = i32([0])
+        out, lse = dsa.attn_prompt(b, q, *args, dev_err=err)
+        assert int(err.item()) == 16
+        assert bool((out[:2] == 0).all()) and bool((lse[:2] == -math.inf).all())
+        assert bool(torch.isfinite(lse[2]).all())
