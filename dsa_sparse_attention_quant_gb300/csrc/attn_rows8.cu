@@ -78,7 +78,8 @@ constexpr float kSpread = 0x1p-96f;
 enum Load : int { kPages, kSlots };
 
 constexpr int kMostCluster = 8;
-constexpr int kFirstTiles = 6;  // a CTA's first tiles of slots, read in the list's order
+constexpr int kFirstTiles = 6;    // a CTA's first tiles of slots, read in the list's order
+constexpr int kOrderedTiles = 8;  // fewer tiles of slots at a time are there sooner than they are in order
 constexpr int64_t kApart = 1 << 28;
 constexpr int kThreads8 = kThreads + 32;  // the consumers, and the loader
 
@@ -107,7 +108,7 @@ struct Rows8Cfg {
   static constexpr int kOffScale = kOffBar + kInfos * 32;                 // float2 [kInfos][kScales]
   static constexpr int kOffAt = kOffScale + kInfos * kScales * 8;         // slots: longlong2 [kInfos][kTile]
   // slots: the next tiles' (a window), in the order in which they are read
-  static constexpr int kWindow = kKeptQ ? kFirstTiles : 12;
+  static constexpr int kWindow = kKeptQ ? kFirstTiles : 12;  // (kKeptQ: no room for more)
   static constexpr int kOffIds = kOffAt + (LOAD == kSlots ? kInfos * kTile * 16 : 0);      // int [kWindow][kTile]
   static constexpr int kOffMl = kOffIds + (LOAD == kSlots ? kWindow * kTile * 4 : 0);      // float2 [kWarps][HP][kRows]
   static constexpr int kOffParts = kOffMl + kWarps * HP * kRows * 8;      // cluster: float2 [HP][kRows]
@@ -313,39 +314,21 @@ struct TileWindow {
   }
 };
 
-// The slots of a window of tiles, from place j of a token's list on, into ids[]: in order,
-// or, where they lie in kApart bytes of K or more (page: a page's, or 0), brought into 16
-// stretches of the cache, from its lower to its upper end. CTAs that begin together then
-// go through the cache together, and what they read at a time lies in few of the memory's
-// pages, whose translations they share. 64 tokens of 2048 slots, 64/8 heads of 128, from
-// 64, 16 and 8 requests of 32K (2.1, 0.54 and 0.27 GB of K): 63.4, 58.6 and 57.7 us, in the
-// list's order 70.1, 63.6 and 56.1; 512 tokens of one 369, 352. (Windows of 16 tiles 63.4, heads
-// of 64 46.4; of 12 64.4, 43.1; of 8 65.7, 43.4.) Which keys make a tile changes by it, and so the
-// sums' order, but not from run to run. One warp.
+// A window's slots (id[i] of lane l: place 32 i + l, -1 behind the list) into ids[], brought
+// into 16 stretches of the cache from its lower to its upper end, if they lie in kApart
+// bytes of K or more (page: a page's). One warp.
 template <int TILES>
-__device__ __forceinline__ void place_slots(const int32_t* list, int j, int n, int tiles, int64_t page, int32_t* ids) {
+__device__ __forceinline__ bool order_slots(const int (&id)[2 * TILES], int tiles, int64_t page, int32_t* ids) {
   const int lane = threadIdx.x & 31;
-  int id[2 * TILES];
-#pragma unroll
-  for (int i = 0; i < 2 * TILES; ++i)
-    id[i] = i < 2 * tiles && j + i * 32 + lane < n ? list[j + i * 32 + lane] : -1;
   int lo = INT_MAX, hi = 0;
-  if (page > 0) {
 #pragma unroll
-    for (int i = 0; i < 2 * TILES; ++i) {
-      lo = min(lo, id[i] >= 0 ? id[i] : INT_MAX);
-      hi = max(hi, id[i]);
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
+  for (int i = 0; i < 2 * TILES; ++i) {
+    lo = min(lo, id[i] >= 0 ? id[i] : INT_MAX);
+    hi = max(hi, id[i]);
   }
-  if (hi <= lo || (hi - lo) / kBlock * page < kApart) {
-#pragma unroll
-    for (int i = 0; i < 2 * TILES; ++i)
-      if (i < 2 * tiles) ids[i * 32 + lane] = id[i];
-    __syncwarp();
-    return;
-  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (hi <= lo || (hi - lo) / kBlock * page < kApart) return false;
   const int shift = max(0, 28 - __clz(hi - lo));  // (hi - lo) >> shift < 16
   auto stretch = [&](int x) { return x >= 0 ? (x - lo) >> shift : 15; };  // absent ones come last
   // lane b (and b + 16): the slots of stretch b so far; q: a slot's place in its stretch
@@ -375,6 +358,31 @@ __device__ __forceinline__ void place_slots(const int32_t* list, int j, int n, i
     if (i >= 2 * tiles) break;
     ids[__shfl_sync(0xffffffffu, first, stretch(id[i])) + q[i]] = id[i];
   }
+  __syncwarp();
+  return true;
+}
+
+// The slots of a window of tiles, from place j of a token's list on, into ids[]: in order,
+// or, of kOrderedTiles tiles or more that lie far apart, in the cache's. CTAs that begin
+// together then go through the cache together, and what they read at a time lies in few of
+// the memory's pages, whose translations they share. 64 tokens of 2048 slots, 64/8 heads of
+// 128, from 64, 16 and 8 requests of 32K (2.1, 0.54 and 0.27 GB of K): 63.4, 58.6 and 57.7 us,
+// in the list's order 70.1, 63.6 and 56.1; 512 tokens of one 369, 352. Windows of 8, 12 and 16
+// tiles, in a run of their own: 65.7, 64.4 and 63.4, heads of 64 43.4, 43.1 and 46.4. Which keys
+// make a tile changes by it, and so the sums' order, but not from run to run. The forms with q in
+// shared memory have no room for such windows and read in the list's order. One warp.
+template <int TILES>
+__device__ __forceinline__ void place_slots(const int32_t* list, int j, int n, int tiles, int64_t page, int32_t* ids) {
+  const int lane = threadIdx.x & 31;
+  int id[2 * TILES];
+#pragma unroll
+  for (int i = 0; i < 2 * TILES; ++i)
+    id[i] = i < 2 * tiles && j + i * 32 + lane < n ? list[j + i * 32 + lane] : -1;
+  if constexpr (TILES >= kOrderedTiles)
+    if (tiles >= kOrderedTiles && order_slots<TILES>(id, tiles, page, ids)) return;
+#pragma unroll
+  for (int i = 0; i < 2 * TILES; ++i)
+    if (i < 2 * tiles) ids[i * 32 + lane] = id[i];
   __syncwarp();
 }
 
@@ -486,9 +494,7 @@ __global__ void __launch_bounds__(kThreads8, Rows8Cfg<D, HP, NT, LOAD>::kCtas)
         if (w == wn) {
           w = 0;
           wn = min(min(each - kt, total - it), it == 0 ? kFirstTiles : C::kWindow);
-          // (a few tiles are there sooner than they are in order)
-          place_slots<C::kWindow>(a.physical + static_cast<int64_t>(t) * a.topk, kt * kTile, a.topk, wn,
-                                  wn < 8 ? 0 : a.k_page, ids);
+          place_slots<C::kWindow>(a.physical + static_cast<int64_t>(t) * a.topk, kt * kTile, a.topk, wn, a.k_page, ids);
         }
         const int32_t n0 = ids[w * kTile + lane], n1 = ids[w * kTile + 32 + lane];
         ++w;
