@@ -44,6 +44,13 @@ struct RowsArgs {
   float* part_o;    // [2 * CTAs][joint][rows of a pass][D]
   int32_t* err;
 };
+// How the kernels take work, for the host's plan, which sizes the scratch that they write:
+// a pass's rows (query heads of a KV head), and CTAs per SM.
+constexpr int rows_of(int group) { return group <= 16 ? 16 : 32; }
+constexpr int rows8_of(int group) { return group <= 8 ? 8 : 16; }
+constexpr int kRowsCtas = 2;
+constexpr int rows8_ctas(int rows, int joint) { return rows * joint > 16 ? 2 : 3; }  // what registers allow
+constexpr int kMostCluster = 8;
 cudaError_t launch_attn_rows(const RowsArgs& a, int head_dim, int dtype, bool selected, cudaStream_t stream);
 
 // The parts that the slices of attn_rows8.cu left, added (attn_rows.cu): krows rows of the

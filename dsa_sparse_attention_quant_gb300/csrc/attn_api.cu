@@ -137,7 +137,7 @@ constexpr int kMinTiles = 2;
 // 128: 11.5 us, cut into slices 14.3; 16 tokens of 1024 slots, 32/8: 15.8, 18.1; but one
 // request of 8192, 32/8: 15.9, 13.5; and with more than 8 query heads a KV head one
 // token of 2048 slots, 40/2: 12.6, 11.7.
-constexpr int kMostCluster = 8, kClusterTiles = 64;
+constexpr int kClusterTiles = 64;
 
 int64_t row_tiles(int64_t keys) { return keys > 0 ? (keys + kBlock - 1) / kBlock : 1; }
 
@@ -152,10 +152,8 @@ RowsPlan rows_plan(int64_t tokens, int64_t keys, int heads, int hkv, int head_di
                    int sms) {
   RowsPlan p{};
   const int group = heads / hkv;
-  // the kernels' tiles of query heads, and their CTAs per SM (RowsCfg, Rows8Cfg)
-  p.rows = cache == kIn8 ? 8 : 16;
-  if (p.rows < group) p.rows *= 2;
-  const int per_sm = cache == kIn8 && (p.rows == 8 || joint == 1) ? 3 : 2;
+  p.rows = cache == kIn8 ? rows8_of(group) : rows_of(group);
+  const int per_sm = cache == kIn8 ? rows8_ctas(p.rows, joint) : kRowsCtas;
   p.passes = (group + p.rows - 1) / p.rows;
   const int64_t across = static_cast<int64_t>(hkv / joint) * p.passes;  // CTAs a slice
   const int64_t tiles = row_tiles(keys);

@@ -49,6 +49,7 @@ namespace {
 template <int D, int MT>
 struct RowsCfg {
   static constexpr int kRows = 16 * MT;
+  static_assert(kRows == rows_of(kRows) && rows_of(kRows - 15) == kRows, "the host's plan has these rows a pass");
   static constexpr int kRowBytes = D * 2;
   static constexpr int kStageBytes = 2 * kWarpKeys * kRowBytes;  // a warp's K rows, then its V rows
   // As many stages as leave room for two CTAs on an SM (D = 128: three of 8 KB
@@ -60,12 +61,12 @@ struct RowsCfg {
   static constexpr int kOffQ = kOffO + 2 * kRows * D * 4;               // MT = 2: the item's q rows
   static constexpr int kOffScan = kOffQ + (MT == 2 ? kRows * kRowBytes : 0);  // the slice, scan scratch
   static constexpr int kSmemBytes = kOffScan + 48 * 4;
-  static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(kRowsCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
   static_assert(kOffMeta >= 4096, "find_slice's rounds lie in the ring");
 };
 
 template <int D, typename T, int MT, bool SEL>
-__global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, kRowsCtas) attn_rows_kernel(const __grid_constant__ RowsArgs a) {
   using C = RowsCfg<D, MT>;
   using E = Elem<T>;
   constexpr int S = C::kStages;
@@ -615,7 +616,7 @@ cudaError_t launch(const RowsArgs& a, int grid, cudaStream_t stream) {
 
 template <int D, typename T>
 cudaError_t launch_dt(const RowsArgs& a, int grid, bool sel, cudaStream_t stream) {
-  if (a.group <= 16)
+  if (rows_of(a.group) == 16)
     return sel ? launch<D, T, 1, true>(a, grid, stream) : launch<D, T, 1, false>(a, grid, stream);
   return sel ? launch<D, T, 2, true>(a, grid, stream) : launch<D, T, 2, false>(a, grid, stream);
 }

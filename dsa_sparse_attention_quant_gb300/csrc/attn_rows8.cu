@@ -77,7 +77,6 @@ constexpr float kSpread = 0x1p-96f;
 // heads a slot 93, single rows 184).
 enum Load : int { kPages, kSlots };
 
-constexpr int kMostCluster = 8;
 constexpr int kFirstTiles = 6;    // a CTA's first tiles of slots, read in the list's order
 constexpr int kOrderedTiles = 8;  // fewer tiles of slots at a time are there sooner than they are in order
 constexpr int64_t kApart = 1 << 28;
@@ -90,7 +89,8 @@ template <int D, int HP, int NT, int LOAD>
 struct Rows8Cfg {
   static constexpr int kRows = 8 * NT;                         // query heads of a KV head in a pass
   static constexpr int kRowBytes = HP * D;
-  static constexpr int kCtas = HP * NT > 2 ? 2 : 3;             // per SM: what registers allow
+  static constexpr int kCtas = rows8_ctas(kRows, HP);           // per SM
+  static_assert(kRows == rows8_of(kRows) && rows8_of(kRows - 7) == kRows, "the host's plan has these rows a pass");
   // q's fragments in shared memory, each thread's its own, where registers do not hold them: three CTAs
   // then (8 requests of 32K keys, 64/1 heads of 128: 60.7 us, two with q in registers 64.9; 128/1 97.6,
   // 108.3; but pairs of 40/2 heads of 64 67.5, two 58.3)
@@ -1011,7 +1011,8 @@ cudaError_t launch(const Rows8Args& a, int grid, const CUtensorMap* maps, cudaSt
 
 template <int D, int HP, int LOAD>
 cudaError_t launch_rows(const Rows8Args& a, int grid, const CUtensorMap* maps, cudaStream_t stream) {
-  return a.group <= 8 ? launch<D, HP, 1, LOAD>(a, grid, maps, stream) : launch<D, HP, 2, LOAD>(a, grid, maps, stream);
+  return rows8_of(a.group) == 8 ? launch<D, HP, 1, LOAD>(a, grid, maps, stream)
+                                : launch<D, HP, 2, LOAD>(a, grid, maps, stream);
 }
 
 }  // namespace
