@@ -332,7 +332,8 @@ def kv_write8(k, v, slot_mapping, k_cache, v_cache, kv_scale, ws=None, dev_err=N
     """Quantise the rows k and v [tokens, heads, head_dim] (bf16 or fp16) into the
     8-bit cache (``new_kv_cache8``) at their slots (int64, -1 = padding). A block's
     scale is made anew when its first slot is written and may rise after that, which
-    rounds the rows that are there to the raised one."""
+    rounds the rows that are there to the raised one; it does not fall again when the
+    row that raised it is written over."""
     kv, dev, heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, k, "k rows")
     n = _list8(slot_mapping, "slot_mapping", torch.int64, dev)
     want = (n, heads, d)
@@ -353,8 +354,8 @@ def kv_read8(batch, k_cache, v_cache, kv_scale, kv_start, k, v, past: bool = Fal
     """Read sequences back from the 8-bit cache: key s of each request r with
     kv_start[r] >= 0 (int32 [num_reqs]) into row kv_start[r] + s of k and v [rows,
     heads, head_dim] (bf16 or fp16), as ``attn_prompt`` takes packed keys; with
-    ``past`` without the request's own query tokens. Other rows stay as they were.
-    Returns (k, v)."""
+    ``past`` without the request's own query tokens. Other rows stay as they were;
+    without any rows nothing is read, or flagged. Returns (k, v)."""
     kv, dev, heads, d, dtype = _kv8(k_cache, v_cache, kv_scale, k, "k rows")
     n = k.shape[0] if k.dim() else 0
     kp, kr, kh = _rows8(k, "k rows", (n, heads, d), dtype, dev)

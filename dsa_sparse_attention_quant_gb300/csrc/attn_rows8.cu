@@ -25,8 +25,8 @@
 //
 // What bounds it: one read of the codes, 2*D bytes a (key, KV head), and 0.5 of
 // scales for 4*G*D operations: HBM, in the large calls. 64/8 heads of 128: 8 requests of 128K
-// keys 318 us (6.7 TB/s), 32 of 4K to 8K 72 us (5.6: 4 us until all CTAs stream,
-// 4 between their ends, 3 of the join); 64 tokens of 2048 selected slots 64 us (4.3 TB/s:
+// keys 316 us (6.8 TB/s), 32 of 4K to 8K 73 us (5.6: 4 us until all CTAs stream,
+// 4 between their ends, 3 of the join); 64 tokens of 2048 selected slots 63 us (4.3 TB/s:
 // rows of 128 bytes, in an order of their own: place_slots); 24 requests of 1
 // to 4001, 16/16 heads of 64, 28 us. One request of 300 keys takes 9 to 10 us, the host's time for
 // the call. More than 16 query heads a KV head: the making of fragments and the MMAs (8
@@ -66,8 +66,8 @@ constexpr int kScaleBlock = DSA_SCALE_BLOCK;
 static_assert(kWarpKeys == kScaleBlock, "a warp's keys of a tile share their scales");
 constexpr float kLeastScale = 0x1p-64f, kMostScale = 0x1p126f;
 // With the key k that made M (w_k = 2^6 or more) and a key j: w_j >= 2^6 e^(s_j - s_k) kSpread, which
-// is a number down to a share of 2^-36. Nothing in the stream pays for it but a register: where
-// shares above kSpread were added apart, by a branch for each tile, 8 requests of 32K keys, 64/4
+// is a number down to a share of 2^-36. Nothing in the stream pays for it but a register; where
+// the shares of such keys were added apart, by a branch for each tile, 8 requests of 32K keys, 64/4
 // heads of 128, took 65.4 us, so 64.4, and 24 of 1 to 4001 keys, 16/16 of 64, 28.4, so 27.7.
 constexpr float kSpread = 0x1p-96f;
 

@@ -17,9 +17,9 @@
 //
 // What bounds both: HBM, 4*D bytes of rows and 2*D of codes a (token, head). 8 heads of
 // 128: 30572 rows of 8 requests written in 35 us (5.4 TB/s; the claims are a launch of
-// their own), 113K rows of 8 requests of up to 16K read back in 109 us (6.5 TB/s, two
-// thirds of it writes). 64 rows written, or 301 read back, take 8 to 9 us, the host's
-// time for the call.
+// their own), 113K rows of 8 requests of up to 16K read back in 107 us (6.6 TB/s, two
+// thirds of it writes). 64 rows written, or 301 read back, take 8 us, the host's
+// time for the call, of which the GPU's is 3 to 4.
 #include "attn.h"
 #include "common.cuh"
 
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) write8_claim_kernel(const __grid_con
 // The codes of a block whose scale was no power of two, which this file does not make: the
 // rows at `rows` over the scale s, and the codes that are there moved from `old` to it. A
 // function of its own, a value at a time: as a branch of write_block it costs the rows that
-// never take it 13% (30572 rows: 39.3 us, so 34.6).
+// never take it 13% (30572 rows: 39.3 us, so 34.9).
 template <int D, typename T>
 __device__ __noinline__ void write_odd(const uint16_t* rows, int64_t row, uint8_t* codes, int64_t slot,
                                        const int32_t* src, float s, float old) {

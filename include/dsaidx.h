@@ -520,7 +520,9 @@ typedef struct DsaKv8 {
  *   code  = x / scale rounded once to the nearest code; where the block's scale
  *           rises, its other slots' codes are rounded to it
  * so a sequence that grows slot by slot keeps each row within one step of its
- * block's largest, however it is cut into calls. NaN and infinities become NaN.
+ * block's largest, however it is cut into calls. A scale does not fall before its
+ * block is opened anew: a row that is written over (a rejected draft) leaves the
+ * scale that it raised, and the other rows as they were rounded to it. NaN and infinities become NaN.
  * Of tokens with one slot the last of the list is written. Results do not depend
  * on timing, nor on the order of the list but for that.
  *   k, v, slot_mapping  as for dsa_kv_write; n_tokens at most 2^31 - 1
